@@ -316,8 +316,9 @@ w4a16_status w4a16_moe_grouped_gemm(int kind, const void* packed, int num_expert
                                     const w4a16_plan_t* plan, void* workspace, size_t ws_bytes,
                                     void* stream);
 
-/* Element types of w4a16_topk_softmax's logits. */
-enum { W4A16_DTYPE_F32 = 0, W4A16_DTYPE_BF16 = 1 };
+/* Element types of w4a16_topk_softmax's logits; W4A16_DTYPE_FP8 (e4m3) only
+ * for the rows of w4a16_moe_few_tokens. */
+enum { W4A16_DTYPE_F32 = 0, W4A16_DTYPE_BF16 = 1, W4A16_DTYPE_FP8 = 2 };
 
 /*
  * Routing front end: router logits -> the top-k routing tensors the align
@@ -433,6 +434,106 @@ w4a16_status w4a16_moe_layer(const void* packed_gate_up, const void* packed_down
                              const float* topk_weights, float* out, int flags,
                              const w4a16_plan_t* plan, void* workspace, size_t ws_bytes,
                              void* stream);
+
+/* 8-bit output forms of w4a16_add_rms_norm: none, one scale per row, or one
+ * scale per 128 columns. */
+enum { W4A16_FP8_NONE = 0, W4A16_FP8_ROW = -1, W4A16_FP8_GROUP = 128 };
+
+/*
+ * The norm in front of the expert layer, with the residual's addition (glue
+ * the pages leave outside the timed pair; its form is this library's reading):
+ *   h = x + residual                     (FP32; h = x when residual is NULL)
+ *   residual_out = bf16(h)
+ *   y = h * rsqrt(mean(h^2) + eps) * weight        (FP32, from the unrounded h)
+ *   out = bf16(y)
+ *   scales = max(amax(|y|), 1e-10) / 448, over each group of 128 columns
+ *            (W4A16_FP8_GROUP; the last group may be shorter) or over the row
+ *            (W4A16_FP8_ROW);  out_fp8 = e4m3(y / scale), round to nearest.
+ * The 8-bit form is what w4a16_moe_few_tokens takes with W4A16_DTYPE_FP8.
+ *   x        BF16 [rows, hidden], row stride x_stride elements;
+ *   residual BF16 [rows, hidden], row stride residual_stride, or NULL;
+ *   weight   BF16 [hidden];
+ *   out      BF16 [rows, hidden] or NULL; residual_out BF16 [rows, hidden],
+ *            given exactly when residual is (it may be residual itself when
+ *            residual_stride == hidden; no other output may overlap an input);
+ *   out_fp8  e4m3 [rows, hidden] and scales FP32 [rows, ceil(hidden/128)] or
+ *            [rows, 1]: both given unless fp8_group is W4A16_FP8_NONE, then
+ *            both NULL. At least one of out and out_fp8 is given.
+ * A group that holds a NaN or an infinity after the norm has a NaN scale and
+ * NaN codes.
+ * hidden a multiple of 8 up to 16384 (else W4A16_ERR_UNSUPPORTED), strides
+ * multiples of 8 and at least hidden, BF16 pointers 16-byte and out_fp8 8-byte
+ * aligned, eps finite and not negative (else W4A16_ERR_INVALID_ARG). No
+ * workspace, no host synchronisation: graph-capturable.
+ */
+w4a16_status w4a16_add_rms_norm(const uint16_t* x, long long x_stride, const uint16_t* residual,
+                                long long residual_stride, const uint16_t* weight, float eps,
+                                int rows, int hidden, uint16_t* out, uint16_t* residual_out,
+                                uint8_t* out_fp8, float* scales, int fp8_group, void* stream);
+
+/*
+ * The router's product: logits[t, e] = sum over c of x[t, c] * weight[e, c],
+ * FP32 accumulation; the logits w4a16_topk_softmax, w4a16_moe_route_align and
+ * w4a16_moe_few_tokens take.
+ *   x      BF16 [tokens, hidden], row stride x_stride elements;
+ *   weight BF16 [num_experts, hidden]; logits FP32 [tokens, num_experts].
+ * hidden a multiple of 8, num_experts at most 1024 (else
+ * W4A16_ERR_UNSUPPORTED), x_stride a multiple of 8 and at least hidden, x and
+ * weight 16-byte and logits 4-byte aligned (else W4A16_ERR_INVALID_ARG). The
+ * order of the additions depends on the sizes only. No workspace, no host
+ * synchronisation: graph-capturable.
+ */
+w4a16_status w4a16_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
+                                 int tokens, int hidden, int num_experts, float* logits,
+                                 void* stream);
+
+/* Most tokens of one w4a16_moe_few_tokens call. */
+enum { W4A16_FEW_TOKENS_MAX = 32 };
+
+/* Device workspace bytes of w4a16_moe_few_tokens for up to `tokens` tokens (0
+ * on bad sizes). The caller zero-fills a new workspace once; every call leaves
+ * its counters zero. One workspace serves calls that are ordered on one
+ * stream. Host only. */
+size_t w4a16_moe_few_tokens_workspace_size(int tokens, int topk, int hidden, int inter);
+
+/*
+ * A whole MoE layer for up to W4A16_FEW_TOKENS_MAX tokens: routing, gate_up,
+ * the activation, down and the top-k weighted sum
+ *   out[t, :] = sum over s of topk_weights[t, s] *
+ *               (silu(x[t] . Wgate_e^T) * (x[t] . Wup_e^T)) . Wdown_e^T,
+ * e = topk_ids[t, s], over the picks of this GPU's experts. Unlike the indexed
+ * GEMMs it keeps weights (q - 8) * scale, the activation and every sum in
+ * FP32 (no BF16 rounding in between), and adds in an order that depends only
+ * on the sizes and the routing: repeated calls give the same bits.
+ *   packed_gate_up  [num_experts, 2*inter, hidden], W4A16_LAYOUT_KTILE64_GLU16;
+ *   packed_down     [num_experts, hidden, inter], W4A16_LAYOUT_KTILE64;
+ *   x, x_dtype      BF16 [tokens, hidden] (W4A16_DTYPE_BF16, x_scales NULL), or
+ *                   e4m3 [tokens, hidden] with FP32 x_scales [tokens,
+ *                   ceil(hidden/128)] (W4A16_DTYPE_FP8): the value of element c
+ *                   is x * x_scales[t, c / 128];
+ *   logits          NULL: topk_ids (int32 [tokens, topk], any value outside
+ *                   [0, num_experts) = not of this GPU) and topk_weights (FP32
+ *                   [tokens, topk]) are inputs and the four arguments after
+ *                   logits are ignored; else [tokens, num_global_experts] of
+ *                   logits_dtype: the routing of w4a16_topk_softmax, and
+ *                   topk_ids and topk_weights receive it;
+ *   out             FP32 [tokens, hidden], written, or added to with
+ *                   W4A16_FLAG_ACCUMULATE (the only flag).
+ * Limits: hidden % 32 == 0, inter % 64 == 0, tokens <= W4A16_FEW_TOKENS_MAX,
+ * topk <= 32 (and <= num_global_experts with logits), num_experts and
+ * num_global_experts <= 1024 (else W4A16_ERR_UNSUPPORTED); packed weights, x
+ * and out 16-byte aligned (else W4A16_ERR_INVALID_ARG); ws_bytes >=
+ * w4a16_moe_few_tokens_workspace_size(tokens, topk, hidden, inter) (else
+ * W4A16_ERR_WORKSPACE). No host synchronisation: graph-capturable. A
+ * device-side wait that gives up is reported by w4a16_read_device_status.
+ */
+w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed_down,
+                                  int num_experts, int hidden, int inter, const void* x,
+                                  int x_dtype, const float* x_scales, int tokens, int topk,
+                                  const void* logits, int logits_dtype, int num_global_experts,
+                                  int renormalize, int expert_offset, int32_t* topk_ids,
+                                  float* topk_weights, float* out, int flags, void* workspace,
+                                  size_t ws_bytes, void* stream);
 
 /*
  * No-allocation variant of w4a16_moe_indexed_gemm. The pages have no

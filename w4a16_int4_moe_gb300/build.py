@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a16moe.so")
 
 SOURCES = ["api.cu", "moe_gemm.cu", "align.cu", "prepack.cu", "act.cu", "noalloc.cu", "permute.cu",
-           "topk.cu", "det.cu"]
+           "topk.cu", "det.cu", "norm.cu", "router.cu", "moe_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -806,6 +806,118 @@ w4a16_status w4a16_moe_layer(const void* packed_gate_up, const void* packed_down
   return W4A16_OK;
 }
 
+w4a16_status w4a16_add_rms_norm(const uint16_t* x, long long x_stride, const uint16_t* residual,
+                                long long residual_stride, const uint16_t* weight, float eps,
+                                int rows, int hidden, uint16_t* out, uint16_t* residual_out,
+                                uint8_t* out_fp8, float* scales, int fp8_group, void* stream) {
+  if (rows < 0 || hidden <= 0 || !(eps >= 0.f) || std::isinf(eps)) return W4A16_ERR_INVALID_ARG;
+  if (hidden % 8 != 0 || hidden > kNormMaxHidden) return W4A16_ERR_UNSUPPORTED;
+  if (fp8_group != W4A16_FP8_NONE && fp8_group != W4A16_FP8_ROW && fp8_group != W4A16_FP8_GROUP)
+    return W4A16_ERR_UNSUPPORTED;
+  if (rows == 0) return W4A16_OK;
+  const bool fp8 = fp8_group != W4A16_FP8_NONE;
+  if (x == nullptr || weight == nullptr || (residual == nullptr) != (residual_out == nullptr))
+    return W4A16_ERR_INVALID_ARG;
+  if (fp8 != (out_fp8 != nullptr) || fp8 != (scales != nullptr) || (out == nullptr && !fp8))
+    return W4A16_ERR_INVALID_ARG;
+  if (x_stride < hidden || x_stride % 8 != 0) return W4A16_ERR_INVALID_ARG;
+  if (residual != nullptr && (residual_stride < hidden || residual_stride % 8 != 0))
+    return W4A16_ERR_INVALID_ARG;
+  if (residual != nullptr && residual == residual_out && residual_stride != hidden)
+    return W4A16_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(out) ||
+      !aligned16(residual_out) || (reinterpret_cast<uintptr_t>(out_fp8) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(scales) & 3u) != 0)
+    return W4A16_ERR_INVALID_ARG;
+  const int sms = current_sm_count();
+  if (sms <= 0) return W4A16_ERR_CUDA;
+  NormArgs a = {x,    x_stride, residual, residual_stride, weight, eps,      rows,
+                hidden, out,    residual_out, out_fp8,     scales, fp8_group};
+  return cuda_status(launch_add_rms_norm(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
+                                 int tokens, int hidden, int num_experts, float* logits,
+                                 void* stream) {
+  if (tokens < 0 || hidden <= 0 || num_experts <= 0) return W4A16_ERR_INVALID_ARG;
+  if (hidden % 8 != 0 || num_experts > 1024) return W4A16_ERR_UNSUPPORTED;
+  if (tokens == 0) return W4A16_OK;
+  if (x == nullptr || weight == nullptr || logits == nullptr) return W4A16_ERR_INVALID_ARG;
+  if (x_stride < hidden || x_stride % 8 != 0) return W4A16_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(weight) || (reinterpret_cast<uintptr_t>(logits) & 3u) != 0)
+    return W4A16_ERR_INVALID_ARG;
+  const int sms = current_sm_count();
+  if (sms <= 0) return W4A16_ERR_CUDA;
+  return cuda_status(launch_router_logits(x, x_stride, weight, tokens, hidden, num_experts, logits,
+                                          sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t w4a16_moe_few_tokens_workspace_size(int tokens, int topk, int hidden, int inter) {
+  if (tokens < 0 || topk <= 0 || hidden <= 0 || inter <= 0) return 0;
+  return few_workspace_bytes(tokens, topk, hidden, inter);
+}
+
+w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed_down,
+                                  int num_experts, int hidden, int inter, const void* x,
+                                  int x_dtype, const float* x_scales, int tokens, int topk,
+                                  const void* logits, int logits_dtype, int num_global_experts,
+                                  int renormalize, int expert_offset, int32_t* topk_ids,
+                                  float* topk_weights, float* out, int flags, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  if (num_experts <= 0 || hidden <= 0 || inter <= 0 || tokens < 0 || topk <= 0)
+    return W4A16_ERR_INVALID_ARG;
+  if (x_dtype != W4A16_DTYPE_BF16 && x_dtype != W4A16_DTYPE_FP8) return W4A16_ERR_INVALID_ARG;
+  if ((flags & ~W4A16_FLAG_ACCUMULATE) != 0) return W4A16_ERR_INVALID_ARG;
+  if (hidden % kGroup != 0 || inter % 64 != 0 || tokens > W4A16_FEW_TOKENS_MAX || topk > 32 ||
+      num_experts > 1024)
+    return W4A16_ERR_UNSUPPORTED;
+  if (logits != nullptr) {
+    if (logits_dtype != W4A16_DTYPE_F32 && logits_dtype != W4A16_DTYPE_BF16)
+      return W4A16_ERR_INVALID_ARG;
+    if (num_global_experts <= 0) return W4A16_ERR_INVALID_ARG;
+    if (num_global_experts > 1024 || topk > num_global_experts) return W4A16_ERR_UNSUPPORTED;
+  }
+  if (packed_gate_up == nullptr || packed_down == nullptr) return W4A16_ERR_INVALID_ARG;
+  if (tokens == 0) return W4A16_OK;
+  if (x == nullptr || topk_ids == nullptr || topk_weights == nullptr || out == nullptr)
+    return W4A16_ERR_INVALID_ARG;
+  if ((x_dtype == W4A16_DTYPE_FP8) != (x_scales != nullptr)) return W4A16_ERR_INVALID_ARG;
+  if (!aligned16(packed_gate_up) || !aligned16(packed_down) || !aligned16(x) || !aligned16(out))
+    return W4A16_ERR_INVALID_ARG;
+  if (workspace == nullptr ||
+      ws_bytes < w4a16_moe_few_tokens_workspace_size(tokens, topk, hidden, inter))
+    return W4A16_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return W4A16_ERR_INVALID_ARG;
+  const int sms = current_sm_count();
+  if (sms <= 0) return W4A16_ERR_CUDA;
+  FewArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.gate_up = static_cast<const uint8_t*>(packed_gate_up);
+  a.down = static_cast<const uint8_t*>(packed_down);
+  a.gate_up_expert_bytes = static_cast<long long>(packed_expert_bytes(2 * inter, hidden));
+  a.down_expert_bytes = static_cast<long long>(packed_expert_bytes(hidden, inter));
+  a.num_experts = num_experts;
+  a.hidden = hidden;
+  a.inter = inter;
+  a.x = x;
+  a.x_fp8 = x_dtype == W4A16_DTYPE_FP8;
+  a.x_scales = x_scales;
+  a.tokens = tokens;
+  a.topk = topk;
+  a.logits = logits;
+  a.bf16_logits = logits_dtype == W4A16_DTYPE_BF16;
+  a.num_global = num_global_experts;
+  a.renormalize = renormalize != 0;
+  a.expert_offset = expert_offset;
+  a.topk_ids = topk_ids;
+  a.topk_weights = topk_weights;
+  a.out = out;
+  a.accumulate = (flags & W4A16_FLAG_ACCUMULATE) != 0;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  a.timeout_cycles = wait_timeout_cycles();
+  return cuda_status(launch_moe_few(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
 w4a16_status w4a16_read_device_status(void* workspace, int* detail, void* stream) {
   if (workspace == nullptr) return W4A16_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -201,6 +201,51 @@ cudaError_t launch_topk_softmax(const void* logits, int bf16_logits, int tokens,
                                 int32_t* topk_ids, float* topk_weights, int sms,
                                 cudaStream_t stream);
 
+// The residual's addition and the RMS norm (norm.cu).
+struct NormArgs {
+  const uint16_t* x;
+  long long x_stride;
+  const uint16_t* residual;
+  long long residual_stride;
+  const uint16_t* weight;
+  float eps;
+  int rows, hidden;
+  uint16_t* out;
+  uint16_t* residual_out;
+  uint8_t* out_fp8;
+  float* scales;
+  int fp8_group;  // W4A16_FP8_*
+};
+constexpr int kNormMaxHidden = 16384;
+cudaError_t launch_add_rms_norm(const NormArgs& args, int sms, cudaStream_t stream);
+
+// The router's product (router.cu).
+cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
+                                 int tokens, int hidden, int num_experts, float* logits, int sms,
+                                 cudaStream_t stream);
+
+// The whole layer for a few tokens (moe_few.cu).
+struct FewArgs {
+  const uint8_t* gate_up;
+  const uint8_t* down;
+  long long gate_up_expert_bytes, down_expert_bytes;
+  int num_experts, hidden, inter;
+  const void* x;
+  int x_fp8;
+  const float* x_scales;
+  int tokens, topk;
+  const void* logits;  // NULL: topk_ids and topk_weights are inputs
+  int bf16_logits, num_global, renormalize, expert_offset;
+  int32_t* topk_ids;
+  float* topk_weights;
+  float* out;
+  int accumulate;
+  uint8_t* workspace;
+  long long timeout_cycles;
+};
+size_t few_workspace_bytes(int tokens, int topk, int hidden, int inter);
+cudaError_t launch_moe_few(const FewArgs& args, int sms, cudaStream_t stream);
+
 cudaError_t launch_silu_and_mul(const uint16_t* in, int rows, int inter, uint16_t* out,
                                 cudaStream_t stream);
 

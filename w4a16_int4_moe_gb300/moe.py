@@ -236,6 +236,53 @@ class W4A16MoE:
         self.align(topk_ids, stream)
         return self.experts(x, topk_weights, out=out, stream=stream)
 
+    def _few_workspace(self) -> torch.Tensor:
+        if not hasattr(self, "_few_ws"):
+            if self.gate_up.layout != ops.W4A16_LAYOUT_KTILE64_GLU16:
+                raise ValueError("few_tokens needs GLU16 gate_up weights")
+            rows = min(self.max_tokens, ops.W4A16_FEW_TOKENS_MAX)
+            self._few_ws = torch.zeros(
+                ops.w4a16_moe_few_tokens_workspace_size(rows, self.topk, self.hidden, self.inter),
+                dtype=torch.uint8, device=self.device)
+        return self._few_ws
+
+    def _few(self, x, ids, weights, x_scales, out, stream, **routing) -> torch.Tensor:
+        if x.shape[0] > self.max_tokens:
+            raise ValueError("more tokens than the layer was planned for")
+        return ops.w4a16_moe_few_tokens(
+            self.gate_up.packed, self.down.packed, self.num_experts, self.hidden, self.inter, x,
+            ids, weights, self._few_workspace(), x_scales=x_scales, out=out, stream=stream,
+            **routing)
+
+    def few_tokens(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                   x_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+        """forward() for up to W4A16_FEW_TOKENS_MAX tokens in one launch
+        (w4a16_moe_few_tokens): the arguments and the result of forward, with
+        the activation kept in FP32 and a fixed order of additions. x may also
+        be e4m3 [T, H] with x_scales FP32 [T, ceil(H/128)]. Needs
+        W4A16_LAYOUT_KTILE64_GLU16 gate_up weights."""
+        return self._few(x, topk_ids, topk_weights, x_scales, out, stream)
+
+    def few_tokens_from_logits(self, x: torch.Tensor, router_logits: torch.Tensor,
+                               expert_offset: int = 0, renormalize: bool = True,
+                               x_scales: Optional[torch.Tensor] = None,
+                               out: Optional[torch.Tensor] = None, routing=None,
+                               stream=None) -> torch.Tensor:
+        """few_tokens from router logits [T, E_global], the routing in the same
+        launch. routing: (topk_ids int32, topk_weights fp32) [T, topk] tensors
+        that receive it (the layer's own buffers when None)."""
+        tokens = x.shape[0]
+        if routing is None:
+            if not hasattr(self, "_route_ids"):
+                self._route_ids = torch.empty((self.max_tokens, self.topk), dtype=torch.int32,
+                                              device=self.device)
+                self._route_w = torch.empty((self.max_tokens, self.topk), dtype=torch.float32,
+                                            device=self.device)
+            routing = (self._route_ids[:tokens], self._route_w[:tokens])
+        return self._few(x, routing[0], routing[1], x_scales, out, stream, logits=router_logits,
+                         renormalize=renormalize, expert_offset=expert_offset)
+
     def experts(self, x: torch.Tensor, topk_weights: torch.Tensor,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """gate_up(+act) and down over the routing tensors already aligned."""
@@ -251,3 +298,43 @@ class W4A16MoE:
             self.activation(tokens, stream)
         self.down_gemm(tokens, topk_weights, out, stream)
         return out
+
+
+class MoEBlock:
+    """The MoE half of a decoder layer on one GPU: the residual's addition and
+    the RMS norm, the router's product, and the layer's experts.
+
+    Up to W4A16_FEW_TOKENS_MAX tokens (with GLU16 gate_up weights) take three
+    launches: norm, router, experts; more tokens take the layer's GEMM path
+    (W4A16MoE.forward_from_logits). fp8_rows=True hands the few-token experts
+    the norm's 8-bit rows (the form that tokens have after an exchange in 8
+    bits); the router always reads the BF16 rows."""
+
+    def __init__(self, norm_weight: torch.Tensor, router_weight: torch.Tensor, experts: W4A16MoE,
+                 eps: float = 1e-6, expert_offset: int = 0, renormalize: bool = True,
+                 fp8_rows: bool = False):
+        if norm_weight.shape != (experts.hidden,) or router_weight.shape[1] != experts.hidden:
+            raise ValueError("norm and router weights do not match the layer's hidden size")
+        self.norm_weight, self.router_weight, self.layer = norm_weight, router_weight, experts
+        self.eps, self.expert_offset, self.renormalize = eps, expert_offset, renormalize
+        self.fp8_rows = fp8_rows
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, stream=None):
+        """x, residual BF16 [T, H] -> (fp32 [T, H] of this GPU's experts, the
+        new residual BF16 [T, H], x itself when none was given)."""
+        few = (x.shape[0] <= ops.W4A16_FEW_TOKENS_MAX
+               and self.layer.gate_up.layout == ops.W4A16_LAYOUT_KTILE64_GLU16)
+        fp8 = few and self.fp8_rows
+        y, new_residual, y8, scales = ops.w4a16_add_rms_norm(
+            x, self.norm_weight, self.eps, residual=residual,
+            fp8_group=ops.W4A16_FP8_GROUP if fp8 else ops.W4A16_FP8_NONE, stream=stream)
+        logits = ops.w4a16_router_logits(y, self.router_weight, stream=stream)
+        if few:
+            result = self.layer.few_tokens_from_logits(
+                y8 if fp8 else y, logits, self.expert_offset, self.renormalize, x_scales=scales,
+                out=out, stream=stream)
+        else:
+            result = self.layer.forward_from_logits(y, logits, self.expert_offset,
+                                                    self.renormalize, out=out, stream=stream)
+        return result, x if residual is None else new_residual

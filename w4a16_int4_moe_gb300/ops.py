@@ -36,6 +36,11 @@ W4A16_LAYOUT_KTILE64 = 0
 W4A16_LAYOUT_KTILE64_GLU16 = 1
 W4A16_DTYPE_F32 = 0
 W4A16_DTYPE_BF16 = 1
+W4A16_DTYPE_FP8 = 2
+W4A16_FP8_NONE = 0
+W4A16_FP8_ROW = -1
+W4A16_FP8_GROUP = 128
+W4A16_FEW_TOKENS_MAX = 32
 W4A16_FLAG_SYNC_STATUS = 4
 
 # Every symbol include/w4a16moe.h declares.
@@ -46,6 +51,8 @@ EXPORTED = (
     "w4a16_silu_and_mul", "w4a16_read_device_status", "w4a16_moe_indexed_gemm_noalloc",
     "w4a16_topk_softmax", "w4a16_deterministic_bytes", "w4a16_layer_workspace_size",
     "w4a16_moe_layer", "w4a16_moe_route_align", "w4a16_grouped_plan", "w4a16_plan_info",
+    "w4a16_add_rms_norm", "w4a16_router_logits", "w4a16_moe_few_tokens_workspace_size",
+    "w4a16_moe_few_tokens",
 )
 
 
@@ -80,6 +87,8 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
+_L = ctypes.c_longlong
+_F = ctypes.c_float
 
 
 def load_library(path: Optional[str] = None):
@@ -121,6 +130,11 @@ def load_library(path: Optional[str] = None):
                                  ctypes.POINTER(Plan), _P, _Z, _P]),
         "w4a16_moe_indexed_gemm_noalloc": (_I, [_I, _P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _I,
                                                 _P, _P, _I, ctypes.POINTER(Plan), _P]),
+        "w4a16_add_rms_norm": (_I, [_P, _L, _P, _L, _P, _F, _I, _I, _P, _P, _P, _P, _I, _P]),
+        "w4a16_router_logits": (_I, [_P, _L, _P, _I, _I, _I, _P, _P]),
+        "w4a16_moe_few_tokens_workspace_size": (_Z, [_I, _I, _I, _I]),
+        "w4a16_moe_few_tokens": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _P, _I, _I, _I, _I,
+                                      _P, _P, _P, _I, _P, _Z, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -377,6 +391,149 @@ def w4a16_silu_and_mul(x: torch.Tensor, out: Optional[torch.Tensor] = None, stre
         out = torch.empty((rows, inter), dtype=torch.bfloat16, device=x.device)
     _check("w4a16_silu_and_mul", load_library().w4a16_silu_and_mul(
         _ptr(x), rows, inter, _ptr(out), _stream(stream)))
+    return out
+
+
+# The calls of the layer's latency-bound path (one token up to a small batch)
+# pass plain integers: no ctypes object is built per pointer, and the current
+# stream is read without making a Stream object.
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index or 0)
+
+
+def _refuse(fn: str, why: str):
+    raise W4A16Error(fn, W4A16_ERR_INVALID_ARG, why)
+
+
+def _need(fn: str, what: str, t: torch.Tensor, dtype, shape):
+    """t is a contiguous tensor of this type and shape, else W4A16_ERR_INVALID_ARG."""
+    if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
+            or not t.is_cuda):
+        _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, "
+                    f"not contiguous {dtype} {tuple(shape)} on a GPU")
+
+
+def _rows(fn: str, what: str, t: torch.Tensor):
+    """t is BF16 [rows, columns] with adjacent columns; returns its row stride."""
+    if (t.dtype != torch.bfloat16 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)
+            or not t.is_cuda):
+        _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} of strides {t.stride()} on {t.device}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def w4a16_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                       residual: Optional[torch.Tensor] = None,
+                       fp8_group: int = W4A16_FP8_NONE, bf16_out: bool = True, out=None,
+                       stream=None):
+    """h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight.
+    Returns (bf16(y), bf16(h), e4m3(y / scale), scale), each None when not
+    asked for: bf16_out, residual, fp8_group (W4A16_FP8_GROUP: a scale per 128
+    columns, W4A16_FP8_ROW: one per row). out: the four tensors to write, None
+    for an absent one (it then decides which of y and its 8-bit form is
+    written, and the third entry may be the residual itself). x and residual
+    BF16 [T, H], rows may be strided."""
+    fn = "w4a16_add_rms_norm"
+    x_stride = _rows(fn, "x", x)
+    rows, hidden = x.shape
+    r_stride = 0
+    _need(fn, "weight", weight, torch.bfloat16, (hidden,))
+    if residual is not None:
+        r_stride = _rows(fn, "residual", residual)
+        if residual.shape != x.shape:
+            _refuse(fn, f"residual {tuple(residual.shape)} for x {tuple(x.shape)}")
+    if fp8_group not in (W4A16_FP8_NONE, W4A16_FP8_ROW, W4A16_FP8_GROUP):
+        raise W4A16Error(fn, W4A16_ERR_UNSUPPORTED, f"fp8_group {fp8_group}")
+    groups = 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP)
+    if out is None:
+        def new(dtype, *shape):
+            return torch.empty(shape, dtype=dtype, device=x.device)
+        out = (new(torch.bfloat16, rows, hidden) if bf16_out else None,
+               new(torch.bfloat16, rows, hidden) if residual is not None else None,
+               new(torch.float8_e4m3fn, rows, hidden) if fp8_group else None,
+               new(torch.float32, rows, groups) if fp8_group else None)
+    else:
+        for what, t, dtype, shape in (
+                ("out", out[0], torch.bfloat16, (rows, hidden)),
+                ("residual_out", out[1], torch.bfloat16, (rows, hidden)),
+                ("out_fp8", out[2], torch.float8_e4m3fn, (rows, hidden)),
+                ("scales", out[3], torch.float32, (rows, groups))):
+            if t is not None:
+                _need(fn, what, t, dtype, shape)
+    y, res_out, y8, scales = out
+    _check(fn, load_library().w4a16_add_rms_norm(
+        x.data_ptr(), x_stride, _addr(residual), r_stride, weight.data_ptr(), eps, rows, hidden,
+        _addr(y), _addr(res_out), _addr(y8), _addr(scales), fp8_group,
+        _raw_stream(x.device, stream)))
+    return out
+
+
+def w4a16_router_logits(x: torch.Tensor, weight: torch.Tensor,
+                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x BF16 [T, H] (rows may be strided), weight BF16 [E, H] -> FP32 [T, E]."""
+    fn = "w4a16_router_logits"
+    x_stride = _rows(fn, "x", x)
+    tokens, hidden = x.shape
+    experts = weight.shape[0]
+    _need(fn, "weight", weight, torch.bfloat16, (experts, hidden))
+    if out is None:
+        out = torch.empty((tokens, experts), dtype=torch.float32, device=x.device)
+    else:
+        _need(fn, "out", out, torch.float32, (tokens, experts))
+    _check(fn, load_library().w4a16_router_logits(
+        x.data_ptr(), x_stride, weight.data_ptr(), tokens, hidden, experts, out.data_ptr(),
+        _raw_stream(x.device, stream)))
+    return out
+
+
+def w4a16_moe_few_tokens_workspace_size(tokens: int, topk: int, hidden: int, inter: int) -> int:
+    return int(load_library().w4a16_moe_few_tokens_workspace_size(tokens, topk, hidden, inter))
+
+
+def w4a16_moe_few_tokens(packed_gate_up: torch.Tensor, packed_down: torch.Tensor,
+                         num_experts: int, hidden: int, inter: int, x: torch.Tensor,
+                         topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                         workspace: torch.Tensor, x_scales: Optional[torch.Tensor] = None,
+                         logits: Optional[torch.Tensor] = None, renormalize: bool = True,
+                         expert_offset: int = 0, out: Optional[torch.Tensor] = None,
+                         flags: int = 0, stream=None) -> torch.Tensor:
+    """The whole layer for up to W4A16_FEW_TOKENS_MAX tokens: out FP32 [T, H].
+    x BF16 [T, H], or e4m3 [T, H] with x_scales FP32 [T, ceil(H/128)]. Without
+    logits, topk_ids and topk_weights [T, topk] are the routing; with logits
+    (FP32 or BF16 [T, E_global]) they receive it."""
+    fn = "w4a16_moe_few_tokens"
+    tokens, topk = topk_ids.shape
+    fp8 = x_scales is not None
+    _need(fn, "x", x, torch.float8_e4m3fn if fp8 else torch.bfloat16, (tokens, hidden))
+    _need(fn, "topk_ids", topk_ids, torch.int32, (tokens, topk))
+    _need(fn, "topk_weights", topk_weights, torch.float32, (tokens, topk))
+    if fp8:
+        _need(fn, "x_scales", x_scales, torch.float32,
+              (tokens, -(-hidden // W4A16_FP8_GROUP)))
+    lg_type, experts = W4A16_DTYPE_F32, 0
+    if logits is not None:
+        if logits.dtype == torch.bfloat16:
+            lg_type = W4A16_DTYPE_BF16
+        experts = logits.shape[1]
+        _need(fn, "logits", logits,
+              torch.bfloat16 if lg_type == W4A16_DTYPE_BF16 else torch.float32,
+              (tokens, experts))
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=torch.float32, device=x.device)
+    else:
+        _need(fn, "out", out, torch.float32, (tokens, hidden))
+    _check(fn, load_library().w4a16_moe_few_tokens(
+        packed_gate_up.data_ptr(), packed_down.data_ptr(), num_experts, hidden, inter,
+        x.data_ptr(), W4A16_DTYPE_FP8 if fp8 else W4A16_DTYPE_BF16, _addr(x_scales), tokens, topk,
+        _addr(logits), lg_type, experts, 1 if renormalize else 0, expert_offset,
+        topk_ids.data_ptr(), topk_weights.data_ptr(), out.data_ptr(), flags,
+        workspace.data_ptr(), workspace.numel(), _raw_stream(x.device, stream)))
     return out
 
 
