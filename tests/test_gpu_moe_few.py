@@ -275,3 +275,18 @@ def test_block_runs_norm_router_and_experts(cuda_dev, tokens, fp8):
     half = ref.E4M3_HALF if fp8 and tokens <= ops.W4A16_FEW_TOKENS_MAX else 4 * ref.BF16_HALF
     got = out.cpu().numpy().astype(np.float64)
     assert np.linalg.norm(got - want) <= half * np.linalg.norm(want)
+
+
+def test_expired_waits_are_reported_and_the_next_call_is_right(cuda_dev, monkeypatch):
+    # a bound far below the time of the first weight copy: the waits run out,
+    # every warp still ends, the status says so, and the counters are clean
+    p = wl.uniform_problem(9, 2048, 512, 8, 2, seed=41)
+    packed, ws = _packed(p, cuda_dev), _workspace(p, cuda_dev)
+    want = _run(p, cuda_dev, packed=packed, ws=ws)
+    monkeypatch.setenv("W4A16_WAIT_TIMEOUT_CYCLES", "100")
+    ops.w4a16_moe_few_tokens(packed[0], packed[1], 8, 2048, 512, bf16_tensor(p.x, cuda_dev),
+                             dev(p.topk_ids, cuda_dev), dev(p.topk_weights, cuda_dev), ws)
+    st, word = ops.w4a16_read_device_status(ws)
+    assert st == ops.W4A16_ERR_TIMEOUT and 0x1021 <= word <= 0x1024, hex(word)
+    monkeypatch.delenv("W4A16_WAIT_TIMEOUT_CYCLES")
+    assert torch.equal(_run(p, cuda_dev, packed=packed, ws=ws), want)

@@ -66,7 +66,7 @@ def test_few_tokens_refusals(lib):
                 dict(gu=P + 8), dict(dn=P + 4), dict(x=P + 2), dict(out=P + 4), dict(ws=P + 8)):
         assert call(**bad) == INV, bad
     for bad in (dict(H=240), dict(I=96), dict(t=33), dict(k=33), dict(E=1025), dict(eg=1025),
-                dict(eg=1)):
+                dict(eg=1), dict(H=1 << 21), dict(I=1 << 21)):
         assert call(**bad) == UNS, bad
     assert call(ws=None) == WS and call(wsb=need - 1) == WS
     assert call(t=0, x=None, ids=None, w=None, out=None, ws=None, wsb=0) == OK
