@@ -18,19 +18,32 @@ __device__ __forceinline__ void route_token(const void* __restrict__ logits, int
                                             int32_t* __restrict__ topk_ids,
                                             float* __restrict__ topk_weights) {
   const int lane = threadIdx.x & 31;
-  // this lane's logits: experts lane, lane + 32, ...
+  // this lane's logits: experts lane, lane + 32, ... (the loads carry no
+  // branch, so that all of them are in flight at once); keys order them as
+  // integers (0: never chosen; -0 counts as +0; a NaN or a value at or below
+  // the lowest finite number is not chosen)
   float v[kPer];
+  uint32_t key[kPer];
   float mx = -FLT_MAX;
+  const long long row = static_cast<long long>(t) * num_experts;
+  if (bf16_logits) {
+    const uint16_t* from = static_cast<const uint16_t*>(logits) + row;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      v[i] = __uint_as_float(
+          static_cast<uint32_t>(__ldg(from + min(lane + 32 * i, num_experts - 1))) << 16);
+  } else {
+    const float* from = static_cast<const float*>(logits) + row;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = __ldg(from + min(lane + 32 * i, num_experts - 1));
+  }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = -FLT_MAX;
-    if (e < num_experts) {
-      const long long at = static_cast<long long>(t) * num_experts + e;
-      v[i] = bf16_logits ? __bfloat162float(static_cast<const __nv_bfloat16*>(logits)[at])
-                         : static_cast<const float*>(logits)[at];
-      mx = fmaxf(mx, v[i]);
-    }
+    const bool in = lane + 32 * i < num_experts;
+    if (!in) v[i] = -FLT_MAX;
+    mx = fmaxf(mx, v[i]);
+    const uint32_t bits = __float_as_uint(v[i] + 0.f);
+    key[i] = v[i] > -FLT_MAX ? ((bits >> 31) != 0 ? ~bits : bits | 0x80000000u) : 0u;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -41,41 +54,51 @@ __device__ __forceinline__ void route_token(const void* __restrict__ logits, int
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
 
-  // k rounds of arg-max (largest logit, then lowest id); lane s keeps round s
-  uint32_t taken = 0;
-  float my_p = 0.f, sel_sum = 0.f;
-  int my_id = -1;
-  for (int s = 0; s < topk; ++s) {
-    float bv = -FLT_MAX;
-    int be = 0x7fffffff;
+  // k rounds of arg-max (largest logit, then lowest id) over the lanes' own
+  // best ones, two warp reductions a round. A lane keeps its two largest; it
+  // looks through its others only when it has lost both. Lane s keeps round s.
+  uint32_t best = 0u, next = 0u, taken = 0u;
+  int best_i = 0, next_i = 0;
+  const auto two_best = [&]() {
+    best = next = 0u;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      if (e < num_experts && !(taken & (1u << i)) && (v[i] > bv || (v[i] == bv && e < be))) {
-        bv = v[i];
-        be = e;
+      const uint32_t k = (taken >> i & 1u) != 0u ? 0u : key[i];
+      if (k > best) {
+        next = best;
+        next_i = best_i;
+        best = k;
+        best_i = i;
+      } else if (k > next) {
+        next = k;
+        next_i = i;
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (ov > bv || (ov == bv && oe < be)) {
-        bv = ov;
-        be = oe;
-      }
-    }
-    // no expert left to choose (the rest are masked with -inf logits): the
-    // slot holds id -1 and weight 0
-    const bool found = be < num_experts;
-    if (found && (be & 31) == lane) taken |= 1u << (be >> 5);
-    const float p = found ? expf(bv - mx) / sum : 0.f;
-    sel_sum += p;
+  };
+  two_best();
+  float my_v = 0.f;
+  int my_id = -1;
+#pragma unroll 1
+  for (int s = 0; s < topk; ++s) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    if (top == 0u) break;  // no expert left to choose: the other slots hold id -1 and weight 0
+    const int e = static_cast<int>(__reduce_min_sync(
+        0xffffffffu, best == top ? static_cast<uint32_t>(lane + 32 * best_i) : 0xffffffffu));
     if (lane == s) {
-      my_p = p;
-      my_id = found ? be : -1;
+      my_v = __uint_as_float((top >> 31) != 0 ? top & 0x7FFFFFFFu : ~top);
+      my_id = e;
+    }
+    if ((e & 31) == lane) {
+      taken |= 1u << best_i;
+      best = next;
+      best_i = next_i;
+      next = 0u;
+      if (best == 0u) two_best();
     }
   }
+  const float my_p = my_id >= 0 ? expf(my_v - mx) / sum : 0.f;
+  float sel_sum = 0.f;
+  for (int s = 0; s < topk; ++s) sel_sum += __shfl_sync(0xffffffffu, my_p, s);
   if (lane < topk) {
     const int loc = my_id - expert_offset;
     const long long at = static_cast<long long>(t) * topk + lane;
