@@ -519,10 +519,9 @@ size_t w4a16_moe_few_tokens_workspace_size(int tokens, int topk, int hidden, int
  *                   topk_ids and topk_weights receive it;
  *   out             FP32 [tokens, hidden], written, or added to with
  *                   W4A16_FLAG_ACCUMULATE (the only flag).
- * Limits: hidden % 32 == 0, inter % 64 == 0, both at most 2^20 (with 8-bit
- * rows hidden at most 16384), tokens * topk * hidden * inter < 2^43,
- * tokens <= W4A16_FEW_TOKENS_MAX,
- * topk <= 32 (and <= num_global_experts with logits), num_experts and
+ * Limits: hidden % 32 == 0, inter % 64 == 0, both at most 2^20, tokens *
+ * topk * hidden * inter < 2^43, tokens <= W4A16_FEW_TOKENS_MAX, topk <= 32
+ * (and <= num_global_experts with logits), num_experts and
  * num_global_experts <= 1024 (else W4A16_ERR_UNSUPPORTED); packed weights, x
  * and out 16-byte aligned (else W4A16_ERR_INVALID_ARG); ws_bytes >=
  * w4a16_moe_few_tokens_workspace_size(tokens, topk, hidden, inter) (else

@@ -871,7 +871,7 @@ w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed
   if (hidden % kGroup != 0 || inter % 64 != 0 || tokens > W4A16_FEW_TOKENS_MAX || topk > 32 ||
       num_experts > 1024)
     return W4A16_ERR_UNSUPPORTED;
-  if (!few_supported(tokens, topk, num_experts, hidden, inter, x_dtype == W4A16_DTYPE_FP8))
+  if (!few_supported(tokens, topk, num_experts, hidden, inter))
     return W4A16_ERR_UNSUPPORTED;
   if (logits != nullptr) {
     if (logits_dtype != W4A16_DTYPE_F32 && logits_dtype != W4A16_DTYPE_BF16)

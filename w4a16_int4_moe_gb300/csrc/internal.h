@@ -245,7 +245,7 @@ struct FewArgs {
 };
 size_t few_workspace_bytes(int tokens, int topk, int hidden, int inter);
 // Whether the kernel's lists and at least the smallest ring fit in shared memory.
-bool few_supported(int tokens, int topk, int num_experts, int hidden, int inter, bool fp8);
+bool few_supported(int tokens, int topk, int num_experts, int hidden, int inter);
 cudaError_t launch_moe_few(const FewArgs& args, int sms, cudaStream_t stream);
 
 cudaError_t launch_silu_and_mul(const uint16_t* in, int rows, int inter, uint16_t* out,

@@ -15,17 +15,24 @@
 //   * two threads copy the stages into a shared-memory ring (bulk copies);
 //     they run through both products without waiting for the activation, so
 //     the ring is full of down weights when the activation is complete;
-//   * sixteen warps turn the codes into 16-bit integers in registers and feed
-//     them to m16n8k16 MMAs: weights are the M side, the rows of an expert
-//     (at most eight per pass over its weights) the N side. q - 8 is exact in
-//     16 bits; the scale of a group of 32 is applied to the group's FP32 sum,
-//     so no weight is rounded. The dequantised weights never leave registers:
-//     through TMEM, as the tcgen05 kernel of the large batches needs them, the
-//     same stream reaches 0.4 of the copy bandwidth;
-//   * the activation is handed to the second product as three BF16 parts whose
-//     sum is the FP32 value (each part cuts off 8 bits): one or two rows put
-//     their parts into different columns of one MMA, more rows take three
-//     MMAs into one accumulator;
+//   * sixteen warps feed the codes to m16n8k16 MMAs of FP16 operands: the bits
+//     000qqqq and 000qqqq0000 are subnormal FP16 numbers, q * 2^-24 and
+//     q * 2^-20, so a word of eight codes becomes four MMA registers with one
+//     shift and four ANDs. The 8 that every code is too large comes off as the
+//     number that the sums start from, -8 times the sum of the columns' values
+//     in the group, made once per row. Weights are the M side, the rows of an
+//     expert (at most four per pass over its weights) the N side; the scale of
+//     a group of 32 is applied to the group's FP32 sum, so no weight is
+//     rounded. The codes never leave registers: through TMEM, as the tcgen05
+//     kernel of the large batches needs them, the same stream reaches 0.4 of
+//     the copy bandwidth, and as BF16 pairs q - 8 for BF16 MMAs 0.55 (430
+//     instructions a stage and warp, 190 of them on the half-rate integer
+//     pipe). e4m3 MMAs, for which the code bytes would do as they are, cost
+//     more: mma.sync converts their operands;
+//   * the rows are put into FP16 first, times a power of two per block of 128
+//     columns (a BF16 value fits exactly down to 2^-32 of its block's largest;
+//     rows in e4m3 fit as they are); the FP32 activation goes into two FP16
+//     parts per block of 64, 22 bits, each part a column of the MMA;
 //   * two warps finish the items from shared memory while the others go on.
 //
 // An item (gate_up: one tile of one expert; down: one tile over all experts)
@@ -39,6 +46,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -62,8 +70,10 @@ constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
 constexpr int kFewThreads = kComputeThreads + 32 * kWeightWarps + kEpilogueThreads;
 constexpr int kWStage = 2 * kStepBytes;      // packed bytes of a stage: two 64-k steps
 constexpr int kStageK = 2 * kKStep;
-constexpr int kRowsPerPass = 8;              // rows of an expert per pass over its weights (MMA N)
-constexpr int kParts = 3;                    // BF16 parts of an activation value
+constexpr int kRowsPerPass = 4;              // rows of an expert per pass over its weights
+constexpr int kActParts = 2;                 // FP16 parts of an activation value
+constexpr float kPartScale = 2048.f;         // the second part is the rest times this
+constexpr float kCodeScale = 16777216.f;     // a code is q * 2^-24
 constexpr int kSumPitch = 132;               // FP32 sums [row][128 + 4]
 constexpr int kMaxCtas = 192;
 constexpr int kMinSlots = 4;
@@ -72,13 +82,15 @@ constexpr int kFewMaxSmem = 232448;
 constexpr long long kFewDrainCycles = 4000000000LL;
 
 // waits that can give up (status word detail)
-enum { kWhereRing = 0x21, kWhereData = 0x22, kWhereAct = 0x23, kWhereSums = 0x24 };
+enum { kWhereRing = 0x21, kWhereData = 0x22, kWhereAct = 0x23, kWhereSums = 0x24,
+       kWhereRows = 0x25 };
 
-// Workspace: status words, counters, the CTAs' shares, the activation parts.
+// Workspace: status words, counters, the CTAs' shares, the operands (Operand).
 struct FewCounters {
   int act_done;               // finished gate_up items
   int exits;                  // CTAs that are through
-  int pad[2];
+  int rows_done;              // CTAs whose share of the rows is in FP16
+  int pad;
   int item[2][kMaxCtas];      // arrivals at the item that a CTA begins and does not finish
 };
 constexpr size_t kCounterBytes = (sizeof(FewCounters) + 255) / 256 * 256;
@@ -86,6 +98,25 @@ constexpr size_t kCounterBytes = (sizeof(FewCounters) + 255) / 256 * 256;
 __host__ __device__ inline int max_rows(int tokens, int topk) { return tokens * topk; }
 __host__ __device__ inline size_t share_floats(int tokens) {
   return static_cast<size_t>(tokens > kRowsPerPass ? tokens : kRowsPerPass) * kTileRows;
+}
+
+// An MMA operand: `rows` rows of k FP16 values, of every group of 32 the start
+// of its sums (-8 times the values' sum, as the codes are too large by 8), and
+// of every `block` columns the factor of the values. Rows are padded to whole
+// stages of 128 columns in the starts and factors.
+struct Operand {
+  size_t starts, factors, bytes;  // byte offsets, total
+  int groups, blocks;             // of a row
+};
+__host__ __device__ inline Operand operand(size_t rows, int k, int block) {
+  Operand o;
+  const int stages = (k + kStageK - 1) / kStageK;
+  o.groups = stages * (kStageK / kGroup);
+  o.blocks = stages * (kStageK / block);
+  o.starts = rows * k * 2;  // (k is a multiple of 32)
+  o.factors = o.starts + rows * o.groups * 4;
+  o.bytes = (o.factors + rows * o.blocks * 4 + 15) / 16 * 16;
+  return o;
 }
 
 // FP32 sums: two buffers of an item's sums by warpgroup (gate_up), or one of
@@ -96,9 +127,9 @@ inline int sum_floats(int tokens) { return std::max(2 * kItemSums, kGroups * tok
 // Shared memory of a call, all offsets in bytes.
 struct FewSmem {
   int slots, ring;
-  int sums, ids, weights, mask, base, row_token, row_weight, chunks, x_scales, total;
+  int sums, ids, weights, mask, base, row_token, row_weight, chunks, total;
 };
-FewSmem few_smem(int tokens, int topk, int num_experts, int hidden, bool fp8) {
+FewSmem few_smem(int tokens, int topk, int num_experts) {
   FewSmem s;
   const int rows = max_rows(tokens, topk);
   int at = 1024;  // barriers and scalars
@@ -115,7 +146,6 @@ FewSmem few_smem(int tokens, int topk, int num_experts, int hidden, bool fp8) {
   s.row_token = take(4 * static_cast<size_t>(rows));
   s.row_weight = take(4 * static_cast<size_t>(rows));
   s.chunks = take(4 * static_cast<size_t>(rows));
-  s.x_scales = take(fp8 ? 4 * static_cast<size_t>(tokens) * ((hidden + 127) / 128) : 0);
   s.ring = at;
   s.slots = std::min(kMaxSlots, (kFewMaxSmem - at) / kWStage);
   s.total = at + s.slots * kWStage;
@@ -129,25 +159,14 @@ struct FewParams {
 
 // ------------------------------------------------------------------ MMA ---
 
-// c = a . b (first) or c + a . b
-template <bool kF16, bool kFirst>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  const float i0 = kFirst ? 0.f : c[0], i1 = kFirst ? 0.f : c[1], i2 = kFirst ? 0.f : c[2],
-              i3 = kFirst ? 0.f : c[3];
-  if constexpr (kF16) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(i0), "f"(i1),
-          "f"(i2), "f"(i3));
-  } else {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(i0), "f"(i1),
-          "f"(i2), "f"(i3));
-  }
+// d = a . b + c
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2),
+        "f"(c3));
 }
 
 // (volatile keeps them behind the wait for their slot and before its release)
@@ -162,137 +181,110 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&w)[4
                : "r"(addr));
 }
 
-// Codes 2i and 2i + 1 of a packed word as the pair (q - 8, q - 8): the nibble
-// becomes the low mantissa bits of 128 (BF16) or 1024 (FP16), the difference
-// to 136 or 1032 is exact.
-template <bool kF16>
-__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i) {
-  constexpr uint32_t kBase = kF16 ? 0x64006400u : 0x43004300u;
-  constexpr uint32_t kZero = kF16 ? 0x64086408u : 0x43084308u;
-  const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | kBase;
-  uint32_t r;
-  if constexpr (kF16)
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(kZero));
-  else
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(kZero));
-  return r;
+// The power of two that takes a block whose largest |value| has these bits to
+// [2^14, 2^15), inside FP16 (at most 2^127, for blocks that are nearly zero).
+__device__ __forceinline__ float block_factor(uint32_t max_bits) {
+  const int e = static_cast<int>(max_bits >> 23);
+  return __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
 }
 
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
-      : "=r"(r)
-      : "r"(two));
-  return r;
-}
+// Value k of a row as the MMAs take it: the codes k = 2, 3 of every four lie
+// four bits higher in their word, times 16.
+__device__ __forceinline__ float column_value(int k, float y) { return k & 2 ? y * 0.0625f : y; }
+constexpr float kStartScale = -8.f / kCodeScale;
 
-// The column values of a lane, two groups of 32 k: thread t of a quad takes
-// k = 8t .. 8t + 7 of each group of its column, 16 bytes (8 in e4m3) of a row
-// in global memory. They come straight into registers, right after the same
-// groups of the stage before were used: a few rows stay in L1 and L2, and
-// copying them through the ring cost one warp 730 cycles a stage, against the
-// 390 of the copy bandwidth. Groups from `valid` on are left as they are.
-template <bool kF16, bool kConst>
-__device__ __forceinline__ void load_cols(const uint8_t* from, int valid, uint4& b0, uint4& b1) {
-  const auto load = [](const uint8_t* p, uint4& b) {
-    if constexpr (kF16) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-      b.x = v.x;
-      b.y = v.y;
-    } else if constexpr (kConst) {
-      b = __ldg(reinterpret_cast<const uint4*>(p));
-    } else {  // written by this launch: not the read-only path
-      b = *reinterpret_cast<const uint4*>(p);
-    }
-  };
-  if (valid > 0) load(from, b0);
-  if (valid > 1) load(from + (kF16 ? 32 : 64), b1);
+// The columns of one stage in a lane's registers: thread t of a quad holds
+// k = 8t .. 8t + 7 of each of the four groups of its MMA column, and the starts
+// and factors of the columns that it accumulates. They come straight from L1
+// or L2, right after the same groups of the stage before were used (a few rows
+// stay there; copying them through the ring cost one warp 730 cycles a stage,
+// against the 390 of the copy bandwidth). All of it was written by this
+// launch: no read-only loads. kCols: accumulated columns of a thread.
+template <int kCols>
+struct Cols {
+  uint4 b[4];
+  float4 start[kCols];  // of the four groups
+};
+__device__ __forceinline__ uint4 load16(const void* from) {
+  return *reinterpret_cast<const uint4*>(from);
 }
 
 // kG groups of 32 k of one 64-k step: 32 weight rows of this warp (two 16-row
-// MMA tiles) times eight columns, kP parts per column value (b[group][part]);
-// acc += scale * sum of every group.
+// MMA tiles) times eight columns, of which a thread keeps the even one or
+// both; acc += scale * sum of every group.
 // k order inside a group: thread t of a quad holds word t of each weight row
-// (k = 8t .. 8t + 7) and the same eight values of its column; the two MMAs
-// take code pairs (0, 1) and (2, 3), so both operands use one order.
+// (k = 8t .. 8t + 7) and the same eight values of its column; the first MMA
+// takes k = 8t .. 8t + 3, the second the rest, so both operands use one order.
 // The scales of four rows and both groups come as one transposed ldmatrix
 // whose addresses repeat two 16-byte runs.
-template <int kP, bool kF16, int kG>
-__device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales,
-                                         const uint4 (&b)[2][kP], float (&acc)[2][4]) {
+template <int kCols, int kG>
+__device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const uint4& b0,
+                                         const uint4& b1, const float2 (&start)[kCols],
+                                         float (&acc)[2][2 * kCols]) {
+  constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
   uint32_t w[kG][4], sc[4];
 #pragma unroll
   for (int g = 0; g < kG; ++g) ldmatrix_x4(codes + g * (kTileRows * 16), w[g]);
   ldmatrix_x4_trans(scales, sc);
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
-    uint4 v[kP];
-#pragma unroll
-    for (int p = 0; p < kP; ++p) {
-      v[p] = b[g][p];
-      if constexpr (kF16)
-        v[p] = make_uint4(e4m3_pair(b[g][p].x & 0xFFFFu), e4m3_pair(b[g][p].x >> 16),
-                          e4m3_pair(b[g][p].y & 0xFFFFu), e4m3_pair(b[g][p].y >> 16));
-    }
+    const uint4 b = g == 0 ? b0 : b1;
+    const float i0 = g == 0 ? start[0].x : start[0].y;
+    const float i1 = kCols == 1 ? 0.f : g == 0 ? start[kCols - 1].x : start[kCols - 1].y;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t w0 = w[g][2 * mt], w1 = w[g][2 * mt + 1];
+      const uint32_t w0 = w[g][2 * mt], w1 = w[g][2 * mt + 1], v0 = w0 >> 8, v1 = w1 >> 8;
+      const uint32_t a0[4] = {w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh};
+      const uint32_t a1[4] = {v0 & kLow, v1 & kLow, v0 & kHigh, v1 & kHigh};
       float c[4];
-      const uint32_t a0[4] = {code_pair<kF16>(w0, 0), code_pair<kF16>(w1, 0),
-                              code_pair<kF16>(w0, 1), code_pair<kF16>(w1, 1)};
-      const uint32_t a1[4] = {code_pair<kF16>(w0, 2), code_pair<kF16>(w1, 2),
-                              code_pair<kF16>(w0, 3), code_pair<kF16>(w1, 3)};
-      mma16816<kF16, true>(c, a0, v[kP - 1].x, v[kP - 1].y);
-      mma16816<kF16, false>(c, a1, v[kP - 1].z, v[kP - 1].w);
-#pragma unroll
-      for (int p = kP - 2; p >= 0; --p) {  // smallest part first
-        mma16816<kF16, false>(c, a0, v[p].x, v[p].y);
-        mma16816<kF16, false>(c, a1, v[p].z, v[p].w);
-      }
+      mma16816(c, a0, b.x, b.y, i0, i1, i0, i1);
+      mma16816(c, a1, b.z, b.w, c[0], c[1], c[2], c[3]);
       const uint32_t pair = sc[2 * g + mt];
       const float s0 = __uint_as_float(pair << 16), s1 = __uint_as_float(pair & 0xFFFF0000u);
-      acc[mt][0] = fmaf(s0, c[0], acc[mt][0]);
-      acc[mt][1] = fmaf(s0, c[1], acc[mt][1]);
-      acc[mt][2] = fmaf(s1, c[2], acc[mt][2]);
-      acc[mt][3] = fmaf(s1, c[3], acc[mt][3]);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        acc[mt][i] = fmaf(s0, c[i], acc[mt][i]);
+        acc[mt][kCols + i] = fmaf(s1, c[2 + i], acc[mt][kCols + i]);
+      }
     }
   }
 }
 
-// One stage: its `valid` groups (1..4), then the columns of the next stage
-// (`next_valid` groups at `next`, 0 for none) in the registers they leave.
-template <bool kF16, bool kConst>
+// One stage: its `valid` groups (1..4), scaled by the factors of its two 64-k
+// steps, then, into the registers they leave, the columns of the next stage
+// (`next_valid` groups at `next`, 0 for none).
+template <int kCols>
 __device__ __forceinline__ void stage_mma(int valid, uint32_t codes, uint32_t scales,
-                                          uint4 (&b)[4], const uint8_t* next, int next_valid,
-                                          float (&acc)[2][4]) {
-  const auto step = [&](uint32_t cs, uint32_t ss, int n, const uint4& b0, const uint4& b1) {
-    const uint4 cols[2][1] = {{b0}, {b1}};
+                                          Cols<kCols>& x, float2 factor, const uint8_t* next,
+                                          int next_valid, float (&acc)[2][2 * kCols]) {
+  const auto step = [&](auto st, int n, int next_n) {
+    constexpr int kS = decltype(st)::value;
+    float2 start[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i)
+      start[i] = kS == 0 ? make_float2(x.start[i].x, x.start[i].y)
+                         : make_float2(x.start[i].z, x.start[i].w);
+    float part[2][2 * kCols] = {};
     if (n >= 2)
-      step_mma<1, kF16, 2>(cs, ss, cols, acc);
+      step_mma<kCols, 2>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
+                         x.b[2 * kS + 1], start, part);
     else if (n == 1)
-      step_mma<1, kF16, 1>(cs, ss, cols, acc);
+      step_mma<kCols, 1>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
+                         x.b[2 * kS + 1], start, part);
+    const float f = kS == 0 ? factor.x : factor.y;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2 * kCols; ++i) acc[mt][i] = fmaf(f, part[mt][i], acc[mt][i]);
+    if (next_n > 0) x.b[2 * kS] = load16(next + kS * 128);
+    if (next_n > 1) x.b[2 * kS + 1] = load16(next + kS * 128 + 64);
   };
-  step(codes, scales, valid, b[0], b[1]);
-  load_cols<kF16, kConst>(next, next_valid, b[0], b[1]);
-  step(codes + kStepBytes, scales + kStepBytes, valid - 2, b[2], b[3]);
-  load_cols<kF16, kConst>(next + (kF16 ? 64 : 128), next_valid - 2, b[2], b[3]);
-}
-
-// A stage with the kParts parts of every column value, part_bytes apart.
-__device__ __forceinline__ void stage_mma_parts(int valid, uint32_t codes, uint32_t scales,
-                                                const uint8_t* from, long long part_bytes,
-                                                float (&acc)[2][4]) {
-#pragma unroll 1
-  for (int g0 = 0; g0 < valid; g0 += 2) {  // (the intermediate size is a multiple of 64)
-    uint4 b[2][kParts];
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-      for (int p = 0; p < kParts; ++p)
-        b[g][p] = *reinterpret_cast<const uint4*>(from + (g0 + g) * 64 + p * part_bytes);
-    step_mma<kParts, false, 2>(codes, scales, b, acc);
-    codes += kStepBytes;
-    scales += kStepBytes;
+  if (valid >= 4 && next_valid >= 4) {  // nearly always: no branch inside
+    step(std::integral_constant<int, 0>(), 2, 2);
+    step(std::integral_constant<int, 1>(), 2, 2);
+  } else {
+    step(std::integral_constant<int, 0>(), valid, next_valid);
+    step(std::integral_constant<int, 1>(), valid - 2, next_valid - 2);
   }
 }
 
@@ -370,7 +362,6 @@ struct Split {
 
 }  // namespace
 
-template <bool kFp8>
 __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const FewParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const FewArgs& a = p.a;
@@ -380,12 +371,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
 
   const uint32_t bar_w = smem_u32(smem), bar_e = bar_w + 8 * kMaxSlots;  // slots full, slots free
   const uint32_t bar_sf = bar_w + 16 * kMaxSlots, bar_se = bar_sf + 16;  // sums full, free
-  const uint32_t bar_act = bar_se + 16;                                  // activation complete
-  int* scalars = reinterpret_cast<int*>(smem + 16 * kMaxSlots + 48);
+  const uint32_t bar_act = bar_se + 16, bar_rows = bar_act + 8;  // activation, rows in FP16
+  int* scalars = reinterpret_cast<int*>(smem + 16 * kMaxSlots + 64);
   volatile int* abort_flag = scalars;
   int* last_arrival = scalars + 1;
   int* num_chunks_p = scalars + 2;
   int* warp_sums = scalars + 4;  // [16]
+  uint32_t* block_top = reinterpret_cast<uint32_t*>(scalars + 20);  // [2][kRowsPerPass]
   float* sums = reinterpret_cast<float*>(smem + sm.sums);
   int* s_ids = reinterpret_cast<int*>(smem + sm.ids);
   float* s_weights = reinterpret_cast<float*>(smem + sm.weights);
@@ -394,14 +386,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   int* row_token = reinterpret_cast<int*>(smem + sm.row_token);
   float* row_weight = reinterpret_cast<float*>(smem + sm.row_weight);
   uint32_t* chunks = reinterpret_cast<uint32_t*>(smem + sm.chunks);
-  float* s_xscales = reinterpret_cast<float*>(smem + sm.x_scales);
   const uint32_t ring = smem_u32(smem + sm.ring);
 
   int* status = reinterpret_cast<int*>(a.workspace);
   FewCounters* counters = reinterpret_cast<FewCounters*>(a.workspace + kStatusBytes);
   float* shares = reinterpret_cast<float*>(a.workspace + kStatusBytes + kCounterBytes);
   const size_t share = share_floats(a.tokens);
-  uint16_t* act = reinterpret_cast<uint16_t*>(shares + 2 * kMaxCtas * share);
+  // the two operands: the rows, and the activation's parts (row r, part p: row 2r + p)
+  uint8_t* x_op = reinterpret_cast<uint8_t*>(shares + 2 * kMaxCtas * share);
+  const Operand xo = operand(a.tokens, a.hidden, kStageK);
+  uint8_t* act_op = x_op + xo.bytes;
+  const Operand ao = operand(static_cast<size_t>(rows_cap) * kActParts, a.inter, kKStep);
 
   // ---- setup: barriers, routing, the rows of every expert ----
   if (warp == kFewThreads / 32 - 1) {
@@ -415,13 +410,84 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     }
     if (lane == 0) {
       mbar_init(bar_act, 1);
+      mbar_init(bar_rows, 1);
       *abort_flag = 0;
     }
     fence_mbar_init();
   }
   for (int e = tid; e < a.num_experts; e += kFewThreads) s_mask[e] = 0u;
+  if (warp >= kComputeWarps) {
+    // this CTA's share of the rows into FP16: sixteen lanes a block of 128
+    const int half = (tid - kComputeThreads) >> 4, l16 = lane & 15;
+    constexpr int kHalves = (kFewThreads - kComputeThreads) / 16;
+    const int row_blocks = (a.hidden + kStageK - 1) / kStageK;  // of the input's scales too
+    const int blocks = a.tokens * row_blocks;
+    for (int b0 = blockIdx.x * kHalves; b0 < blocks; b0 += gridDim.x * kHalves) {
+      const int blk = min(b0 + half, blocks - 1);  // (the last ones may repeat a block)
+      const int tok = blk / row_blocks, kb = blk - tok * row_blocks, k0 = kb * kStageK + l16 * 8;
+      const long long at = static_cast<long long>(tok) * a.hidden + k0;
+      const bool in = k0 < a.hidden;
+      float y[8];
+      float out_factor;
+      if (a.x_fp8) {
+        uint2 v = make_uint2(0u, 0u);
+        if (in) v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.x) + at));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t two = (i < 2 ? v.x : v.y) >> (i & 1) * 16 & 0xFFFFu;
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two),
+                                                           __NV_E4M3);
+          const float2 f = __half22float2(__half2(h));
+          y[2 * i] = f.x;
+          y[2 * i + 1] = f.y;
+        }
+        out_factor = __ldg(a.x_scales + blk);
+      } else {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (in) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + at));
+        const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top = max(top, max((word[i] & 0x7FFFu) << 16, word[i] & 0x7FFF0000u));
+          y[2 * i] = __uint_as_float(word[i] << 16);
+          y[2 * i + 1] = __uint_as_float(word[i] & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float factor = block_factor(top);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= factor;
+        out_factor = 1.f / factor;
+      }
+      float sum = 0.f;
+      uint32_t packed[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum += y[2 * i] + y[2 * i + 1];
+        const __half2 h = __floats2half2_rn(column_value(2 * i, y[2 * i]),
+                                            column_value(2 * i + 1, y[2 * i + 1]));
+        packed[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);  // four lanes a group of 32
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (in)
+        *reinterpret_cast<uint4*>(x_op + at * 2) =
+            make_uint4(packed[0], packed[1], packed[2], packed[3]);
+      if ((l16 & 3) == 0)
+        reinterpret_cast<float*>(x_op + xo.starts)[tok * xo.groups + kb * 4 + (l16 >> 2)] =
+            sum * kStartScale;
+      if (l16 == 0)
+        reinterpret_cast<float*>(x_op + xo.factors)[tok * xo.blocks + kb] = out_factor;
+    }
+    asm volatile("bar.sync 2, %0;" ::"n"(kFewThreads - kComputeThreads) : "memory");
+    if (tid == kComputeThreads) {
+      __threadfence();
+      atomicAdd(&counters->rows_done, 1);
+    }
+  }
   if (a.logits != nullptr) {
-    for (int t = warp; t < a.tokens; t += kFewThreads / 32) {
+    for (int t = warp; t < a.tokens && warp < kComputeWarps; t += kComputeWarps) {
       if (a.num_global <= 512)
         route_token<16>(a.logits, a.bf16_logits, t, a.num_global, a.topk, a.renormalize,
                         a.expert_offset, a.num_experts, s_ids, s_weights);
@@ -435,10 +501,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
       s_weights[i] = a.topk_weights[i];
     }
   }
-  if constexpr (kFp8) {
-    const int n = a.tokens * ((a.hidden + kStageK - 1) / kStageK);
-    for (int i = tid; i < n; i += kFewThreads) s_xscales[i] = a.x_scales[i];
-  }
   __syncthreads();
   if (a.logits != nullptr && blockIdx.x == 0)
     for (int i = tid; i < rows_cap; i += kFewThreads) {
@@ -451,7 +513,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     if (e >= 0 && e < a.num_experts) atomicOr(s_mask + e, 1u << (i / a.topk));
   }
   __syncthreads();
-  // running sums over the experts of (rows, passes of up to eight rows):
+  // running sums over the experts of (rows, passes of up to four rows):
   // thread i of the first 512 holds experts 2i and 2i + 1
   const auto rows_and_passes = [](uint32_t mask) {
     const uint32_t n = __popc(mask);
@@ -518,6 +580,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
            i < static_cast<long long>(a.tokens) * a.hidden;
            i += static_cast<long long>(gridDim.x) * kFewThreads)
         a.out[i] = 0.f;
+    if (tid == 0) {
+      __threadfence();
+      if (atomicAdd(&counters->exits, 1) == static_cast<int>(gridDim.x) - 1) {
+        counters->rows_done = 0;
+        counters->exits = 0;
+      }
+    }
     return;
   }
   // gate_up items: expert (pass) by expert, tile by tile; down items: tile by
@@ -628,41 +697,43 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
 
     if (gu_count > 0) {
       const int S = gu.stages;
-      // this lane's column of item q: row g of the pass (columns past the rows
-      // repeat row 0 and are not used), from k = 8t on
-      const auto item_cols = [&](int q) {
+      if (live)
+        live = __all_sync(0xffffffffu, few_wait(bar_rows, 0, abort_flag, status, kWhereRows,
+                                                a.timeout_cycles));
+      // thread t of a quad accumulates row t of the pass, as MMA column 2t
+      // (column 2t + 1 is a copy; rows past the last repeat it)
+      const auto token_of = [&](int q, int r) {
         const uint32_t ch = chunks[q / tiles0];
-        const int n = static_cast<int>((ch >> 10) & 7u) + 1;
-        const int tok = row_token[static_cast<int>(ch >> 16) + (g < n ? g : 0)];
-        return static_cast<const uint8_t*>(a.x) +
-               static_cast<long long>(tok) * a.hidden * (kFp8 ? 1 : 2) + t * (kFp8 ? 8 : 16);
+        return row_token[static_cast<int>(ch >> 16) + min(r, static_cast<int>(ch >> 10 & 7u))];
       };
-      constexpr int kStageBytes = kStageK * (kFp8 ? 1 : 2);
-      uint4 b[4] = {};
+      const uint8_t* cols = nullptr;   // from k = 8t on
+      const float* starts = nullptr;
+      const float* factors = nullptr;
+      const auto point = [&](int q) {
+        cols = x_op + static_cast<long long>(token_of(q, g >> 1)) * a.hidden * 2 + t * 16;
+        const int tok = token_of(q, t);
+        starts = reinterpret_cast<const float*>(x_op + xo.starts) + tok * xo.groups;
+        factors = reinterpret_cast<const float*>(x_op + xo.factors) + tok * xo.blocks;
+      };
+      Cols<1> x = {};
+      float next_factor = 0.f;
       int at = gu_begin + grp;
       int next_q = at / S, next_s = at - next_q * S;  // item and stage of `at`
-      const uint8_t* cols = nullptr;
       if (at < gu_end) {
-        cols = item_cols(next_q);
-        const uint8_t* from = cols + next_s * kStageBytes;
-        load_cols<kFp8, true>(from, groups0 - 4 * next_s, b[0], b[1]);
-        load_cols<kFp8, true>(from + kStageBytes / 2, groups0 - 4 * next_s - 2, b[2], b[3]);
+        point(next_q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < groups0 - 4 * next_s) x.b[i] = load16(cols + next_s * (2 * kStageK) + i * 64);
+        x.start[0] = *reinterpret_cast<const float4*>(starts + 4 * next_s);
+        next_factor = factors[next_s];
       }
       const int q_end = (gu_end - 1) / S;
       for (int q = gu_begin / S; q <= q_end; ++q) {
         // item q: this group's stages of it, then its sums to the epilogue
-        const float* xs0 = s_xscales;
-        const float* xs1 = s_xscales;
-        if constexpr (kFp8) {
-          const uint32_t ch = chunks[q / tiles0];
-          const int n1 = static_cast<int>((ch >> 10) & 7u);
-          const int row0 = static_cast<int>(ch >> 16);
-          xs0 += row_token[row0 + min(2 * t, n1)] * S;
-          xs1 += row_token[row0 + min(2 * t + 1, n1)] * S;
-        }
-        float acc[2][4] = {};
+        float acc[2][2] = {};
+#pragma unroll 1
         while (next_q == q && at < gu_end) {
-          const int st = next_s, valid = groups0 - 4 * st;
+          const int valid = groups0 - 4 * next_s;
           at += kGroups;
           next_s += kGroups;
           while (next_s >= S) {
@@ -670,40 +741,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
             ++next_q;
           }
           int next_valid = 0;
+          const float factor = next_factor;
+          float4 next_start = make_float4(0.f, 0.f, 0.f, 0.f);
           if (at < gu_end) {
-            if (next_q != q) cols = item_cols(next_q);
+            if (next_q != q) point(next_q);
             next_valid = groups0 - 4 * next_s;
+            next_start = *reinterpret_cast<const float4*>(starts + 4 * next_s);
+            next_factor = factors[next_s];
           }
-          const uint8_t* next = cols + next_s * kStageBytes;
           const uint32_t base = wait_stage();
-          if constexpr (kFp8) {
-            // the rows' scales cover exactly one stage
-            const float x0 = xs0[st], x1 = xs1[st];
-            float part[2][4] = {};
-            stage_mma<true, true>(valid, base + codes_at, base + scales_at, b, next, next_valid,
-                                  part);
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              acc[mt][0] = fmaf(x0, part[mt][0], acc[mt][0]);
-              acc[mt][1] = fmaf(x1, part[mt][1], acc[mt][1]);
-              acc[mt][2] = fmaf(x0, part[mt][2], acc[mt][2]);
-              acc[mt][3] = fmaf(x1, part[mt][3], acc[mt][3]);
-            }
-          } else {
-            stage_mma<false, true>(valid, base + codes_at, base + scales_at, b, next, next_valid,
-                                   acc);
-          }
+          stage_mma<1>(valid, base + codes_at, base + scales_at, x, make_float2(factor, factor),
+                       cols + next_s * (2 * kStageK), next_valid, acc);
+          x.start[0] = next_start;
           free_stage();
         }
         // [row of the pass][128] of this warpgroup, in the buffers by turns
         const int buf = (uses0 + uses1) & 1;
         wait_sums(bar_se + 8 * buf, buf ? uses1 : uses0);
-        float* my = sums + buf * kItemSums + grp * (kRowsPerPass * kSumPitch) + m0 + g;
+        float* my = sums + buf * kItemSums + grp * (kRowsPerPass * kSumPitch) + t * kSumPitch + m0 + g;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            my[(2 * t + (i & 1)) * kSumPitch + mt * 16 + (i >> 1) * 8] = acc[mt][i];
+          for (int h = 0; h < 2; ++h) my[mt * 16 + h * 8] = acc[mt][h] * kCodeScale;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_sf + 8 * buf);
         if (buf)
@@ -721,27 +780,36 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         live = __all_sync(0xffffffffu, few_wait(bar_act, 0, abort_flag, status, kWhereAct,
                                                 a.timeout_cycles));
       float* my = sums + grp * (a.tokens * kSumPitch) + m0;
-      // this lane's column of a pass of one or two rows, whose parts fill one
-      // MMA's columns (part p of row r is column 2p + r), or else its row
-      const auto pass_cols = [&](int c) {
+      // thread t of a quad accumulates row t of the pass, its two parts as MMA
+      // columns 2t and 2t + 1 (rows past the last repeat it)
+      const uint8_t* cols = nullptr;  // from k = 8t on
+      const float* starts = nullptr;  // of the first part, then of the second
+      const float* factors = nullptr;
+      const auto point = [&](int c) {
         const uint32_t ch = chunks[c];
-        const int n = static_cast<int>((ch >> 10) & 7u) + 1;
-        const int row = n <= 2 ? g & (n - 1) : (g < n ? g : 0);
-        const int part = n <= 2 && g >> 1 < kParts ? g >> 1 : 0;
-        return reinterpret_cast<const uint8_t*>(act) +
-               ((static_cast<long long>(ch >> 16) + row) * kParts + part) * a.inter * 2 + t * 16;
+        const int last = static_cast<int>(ch >> 10 & 7u), row0 = static_cast<int>(ch >> 16);
+        const long long part_row = (row0 + min(g >> 1, last)) * kActParts + (g & 1);
+        cols = act_op + part_row * a.inter * 2 + t * 16;
+        const long long first = (row0 + min(t, last)) * kActParts;
+        starts = reinterpret_cast<const float*>(act_op + ao.starts) + first * ao.groups;
+        factors = reinterpret_cast<const float*>(act_op + ao.factors) + first * ao.blocks;
       };
-      constexpr int kStageBytes = 2 * kStageK;
-      uint4 b[4] = {};
+      const auto load_starts = [&](int st, float4 (&to)[2]) {
+        to[0] = *reinterpret_cast<const float4*>(starts + 4 * st);
+        to[1] = *reinterpret_cast<const float4*>(starts + ao.groups + 4 * st);
+      };
+      Cols<2> x = {};
+      float2 next_factor = make_float2(0.f, 0.f);  // of both 64-k steps
       int at = dn_begin + ((grp - gu_count) & 3);
       int next_c = at / S, next_s = at - next_c * S;  // pass and stage of `at`
       next_c %= num_chunks;
-      const uint8_t* cols = nullptr;
       if (at < dn_end) {
-        cols = pass_cols(next_c);
-        const uint8_t* from = cols + next_s * kStageBytes;
-        load_cols<false, false>(from, groups1 - 4 * next_s, b[0], b[1]);
-        load_cols<false, false>(from + kStageBytes / 2, groups1 - 4 * next_s - 2, b[2], b[3]);
+        point(next_c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < groups1 - 4 * next_s) x.b[i] = load16(cols + next_s * (2 * kStageK) + i * 64);
+        load_starts(next_s, x.start);
+        next_factor = *reinterpret_cast<const float2*>(factors + 2 * next_s);
       }
       const int tile_stages = num_chunks * S;
       const int tile_end = (dn_end - 1) / tile_stages;
@@ -754,66 +822,47 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         const int stop = min(dn_end, (tile + 1) * tile_stages);
         while (at < stop) {
           const uint32_t ch = chunks[next_c];
-          const int n = static_cast<int>((ch >> 10) & 7u) + 1;
-          const int row0 = static_cast<int>(ch >> 16);
-          const bool packed = n <= 2;
+          const int last = static_cast<int>(ch >> 10 & 7u), row = static_cast<int>(ch >> 16) + t;
           float acc[2][4] = {};
           bool more = true;  // own stages left in this pass
 #pragma unroll 1
           while (more) {
-            const int st = next_s, valid = groups1 - 4 * st;
-            const uint8_t* here = cols;
+            const int valid = groups1 - 4 * next_s;
             at += kGroups;
             next_s += kGroups;
             more = next_s < S && at < stop;
             int next_valid = 0;
+            const float2 factor = next_factor;
+            float4 next_start[2] = {};
             if (at < dn_end) {
               if (next_s >= S) {
                 do {
                   next_s -= S;
                   if (++next_c == num_chunks) next_c = 0;
                 } while (next_s >= S);
-                cols = pass_cols(next_c);
+                point(next_c);
               }
               next_valid = groups1 - 4 * next_s;
+              load_starts(next_s, next_start);
+              next_factor = *reinterpret_cast<const float2*>(factors + 2 * next_s);
             }
-            const uint8_t* next = cols + next_s * kStageBytes;
             const uint32_t base = wait_stage();
-            if (packed) {
-              stage_mma<false, false>(valid, base + codes_at, base + scales_at, b, next,
-                                      next_valid, acc);
-            } else {
-              stage_mma_parts(min(4, valid), base + codes_at, base + scales_at,
-                              here + st * kStageBytes, static_cast<long long>(a.inter) * 2, acc);
-              load_cols<false, false>(next, next_valid, b[0], b[1]);
-              load_cols<false, false>(next + kStageBytes / 2, next_valid - 2, b[2], b[3]);
-            }
+            stage_mma<2>(valid, base + codes_at, base + scales_at, x, factor,
+                         cols + next_s * (2 * kStageK), next_valid, acc);
+            x.start[0] = next_start[0];
+            x.start[1] = next_start[1];
             free_stage();
           }
-          if (packed) {
+          if (t <= last) {
+            const float w = row_weight[row] * kCodeScale;
+            float* dst = my + row_token[row] * kSumPitch + g;
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float v = t < kParts ? acc[mt][i] : 0.f;
-                v += __shfl_xor_sync(0xffffffffu, v, 2);  // (first + third part), second
-                v += __shfl_xor_sync(0xffffffffu, v, 1);
-                acc[mt][i] = v;
+              for (int h = 0; h < 2; ++h) {
+                const float v = fmaf(acc[mt][2 * h + 1], 1.f / kPartScale, acc[mt][2 * h]);
+                dst[mt * 16 + h * 8] = fmaf(w, v, dst[mt * 16 + h * 8]);
               }
-          }
-          const int last = packed ? (t == 0 ? n : 0) : n;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = 2 * t + i;
-            if (r < last) {
-              const float w = row_weight[row0 + r];
-              float* dst = my + row_token[row0 + r] * kSumPitch + g;
-#pragma unroll
-              for (int mt = 0; mt < 2; ++mt) {
-                dst[mt * 16] = fmaf(w, acc[mt][i], dst[mt * 16]);
-                dst[mt * 16 + 8] = fmaf(w, acc[mt][2 + i], dst[mt * 16 + 8]);
-              }
-            }
           }
           __syncwarp();
         }
@@ -827,6 +876,27 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     const int etid = tid - 32 * kWarpEpilogue0;
     bool live = true;
     uint32_t items = 0;  // sums taken, the two buffers by turns
+    // every CTA's arrivals at a counter, then one at a barrier of this CTA
+    const auto pass_on = [&](int* counter, int want, uint32_t bar, int where) {
+      const long long t0 = clock64();
+      while (true) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+        if (v >= want) {
+          mbar_arrive(bar);
+          break;
+        }
+        if (*abort_flag) break;
+        if (clock64() - t0 > a.timeout_cycles) {
+          *abort_flag = 1;
+          atomicCAS(status, 0, 0x1000 | where);
+          break;
+        }
+      }
+    };
+    if (gu_count > 0 && etid == 0)
+      pass_on(&counters->rows_done, static_cast<int>(gridDim.x), bar_rows, kWhereRows);
+    __syncwarp();
     if (gu_count > 0) {
       const int S = gu.stages;
       int q = gu_begin / S, at = gu_begin;
@@ -844,35 +914,60 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
                                                   status, kWhereSums, a.timeout_cycles));
         constexpr int kStride = kRowsPerPass * kSumPitch;
         const float* from0 = sums + buf * kItemSums;
-        // act = silu(gate) * up of column c, row r, as three BF16 parts
-        const auto put_act = [&](int c, int r, float gate, float up) {
-          const float v = gate / (1.f + expf(-gate)) * up;
-          uint16_t* dst =
-              act + static_cast<long long>(row0 + r) * kParts * a.inter + inner * 64 + c;
-          const uint32_t bits = __float_as_uint(v);
-          if ((bits & 0x7F800000u) == 0x7F800000u) {  // infinity or NaN: one part
-            dst[0] = static_cast<uint16_t>(bits >> 16 | ((bits & 0xFFFFu) != 0 ? 0x40u : 0u));
-            dst[a.inter] = 0;
-            dst[2 * a.inter] = 0;
-          } else {
-            const float r1 = v - __uint_as_float(bits & 0xFFFF0000u);
-            const uint32_t bits1 = __float_as_uint(r1);
-            const float r2 = r1 - __uint_as_float(bits1 & 0xFFFF0000u);
-            dst[0] = static_cast<uint16_t>(bits >> 16);
-            dst[a.inter] = static_cast<uint16_t>(bits1 >> 16);
-            dst[2 * a.inter] = static_cast<uint16_t>(__float_as_uint(r2) >> 16);
-          }
+        // act = silu(gate) * up of column c and the pass's rows, as two FP16
+        // parts, in the power of two of the block of 64 columns
+        const auto put_act = [&](int c, const float (&gate)[kRowsPerPass],
+                                 const float (&up)[kRowsPerPass]) {
+          float v[kRowsPerPass];
+#pragma unroll
+          for (int r = 0; r < kRowsPerPass; ++r)
+            if (r < n) {
+              v[r] = gate[r] / (1.f + expf(-gate[r])) * up[r];
+              const uint32_t top =
+                  __reduce_max_sync(0xffffffffu, __float_as_uint(v[r]) & 0x7FFFFFFFu);
+              if (lane == 0) block_top[(etid >> 5) * kRowsPerPass + r] = top;
+            }
+          epilogue_sync();
+#pragma unroll
+          for (int r = 0; r < kRowsPerPass; ++r)
+            if (r < n) {
+              const float factor = block_factor(max(block_top[r], block_top[kRowsPerPass + r]));
+              const float y = v[r] * factor;
+              const __half hi = __float2half_rn(y);
+              // (0 beside an infinity or a NaN)
+              float rest = (y - __half2float(hi)) * kPartScale;
+              if (!(fabsf(y) < INFINITY)) rest = 0.f;
+              const float value[kActParts] = {__half2float(hi), __half2float(__float2half_rn(rest))};
+              const long long row = static_cast<long long>(row0 + r) * kActParts;
+#pragma unroll
+              for (int p = 0; p < kActParts; ++p) {
+                reinterpret_cast<__half*>(act_op)[(row + p) * a.inter + inner * 64 + c] =
+                    __float2half_rn(column_value(c, value[p]));
+                float sum = value[p];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0)
+                  reinterpret_cast<float*>(act_op + ao.starts)[(row + p) * ao.groups + inner * 2 +
+                                                              (etid >> 5)] = sum * kStartScale;
+              }
+              if (etid == 0)
+                reinterpret_cast<float*>(act_op + ao.factors)[row * ao.blocks + inner] =
+                    1.f / factor;
+            }
         };
         // thread = activation column; its gate and up rows of the tile
         const int c = etid, at_g = (c >> 4) * 32 + (c & 15);
         bool finish = whole;
+        float gate[kRowsPerPass] = {}, up[kRowsPerPass] = {};
         if (whole) {
-          for (int r = 0; r < n; ++r) {
-            const float* f = from0 + r * kSumPitch + at_g;
-            const float gate = (f[0] + f[kStride]) + (f[2 * kStride] + f[3 * kStride]);
-            f += 16;
-            put_act(c, r, gate, (f[0] + f[kStride]) + (f[2 * kStride] + f[3 * kStride]));
-          }
+#pragma unroll
+          for (int r = 0; r < kRowsPerPass; ++r)
+            if (r < n) {
+              const float* f = from0 + r * kSumPitch + at_g;
+              gate[r] = (f[0] + f[kStride]) + (f[2 * kStride] + f[3 * kStride]);
+              f += 16;
+              up[r] = (f[0] + f[kStride]) + (f[2 * kStride] + f[3 * kStride]);
+            }
         } else {
           float4* dst =
               reinterpret_cast<float4*>(shares + (2 * cta + (cta == cta0 ? 1 : 0)) * share);
@@ -887,7 +982,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
           // the CTA that arrives last adds the shares, in the CTAs' order
           finish = epilogue_arrive(&counters->item[0][cta0], cta1 - cta0, last_arrival, etid);
           if (finish) {
-            float gate[kRowsPerPass] = {}, up[kRowsPerPass] = {};
 #pragma unroll 2
             for (int b = cta0; b <= cta1; ++b) {
               const float* f = shares + (2 * b + (b == cta0 ? 1 : 0)) * share + at_g;
@@ -898,12 +992,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
                   up[r] += __ldcg(f + r * kTileRows + 16);
                 }
             }
-#pragma unroll
-            for (int r = 0; r < kRowsPerPass; ++r)
-              if (r < n) put_act(c, r, gate[r], up[r]);
           }
         }
         if (finish) {
+          put_act(c, gate, up);
           epilogue_sync();
           if (etid == 0) {
             __threadfence();
@@ -915,28 +1007,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         ++q;
       }
     }
-    if (dn_end > dn_begin && etid == 0) {
-      // every gate_up item of every CTA is out: the activation is complete
-      const long long t0 = clock64();
-      const int want = num_chunks * tiles0;
-      while (true) {
-        int v;
-        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];"
-                     : "=r"(v)
-                     : "l"(&counters->act_done)
-                     : "memory");
-        if (v >= want) {
-          mbar_arrive(bar_act);
-          break;
-        }
-        if (*abort_flag) break;
-        if (clock64() - t0 > a.timeout_cycles) {
-          *abort_flag = 1;
-          atomicCAS(status, 0, 0x1000 | kWhereAct);
-          break;
-        }
-      }
-    }
+    if (dn_end > dn_begin && etid == 0)  // every gate_up item of every CTA is out
+      pass_on(&counters->act_done, num_chunks * tiles0, bar_act, kWhereAct);
     __syncwarp();
     if (dn_end > dn_begin) {
       const int tile_stages = num_chunks * dn.stages;
@@ -995,6 +1067,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
       for (int i = etid; i < 2 * kMaxCtas; i += kEpilogueThreads) counters->item[0][i] = 0;
       if (etid == 0) {
         counters->act_done = 0;
+        counters->rows_done = 0;
         counters->exits = 0;
       }
     }
@@ -1002,37 +1075,35 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
 }
 
 size_t few_workspace_bytes(int tokens, int topk, int hidden, int inter) {
-  (void)hidden;
   const int t = std::max(1, tokens);
+  const size_t rows = max_rows(t, topk);
   return kStatusBytes + kCounterBytes + 2 * kMaxCtas * share_floats(t) * sizeof(float) +
-         static_cast<size_t>(max_rows(t, topk)) * kParts * inter * 2;
+         operand(t, hidden, kStageK).bytes + operand(rows * kActParts, inter, kKStep).bytes;
 }
 
-bool few_supported(int tokens, int topk, int num_experts, int hidden, int inter, bool fp8) {
+bool few_supported(int tokens, int topk, int num_experts, int hidden, int inter) {
   if (tokens == 0) return true;
   const long long rows = max_rows(tokens, topk);
   // the stage counts and the tile and column indexes stay inside 32 bits
   if (static_cast<long long>(hidden) > (1 << 20) || static_cast<long long>(inter) > (1 << 20))
     return false;
-  if (fp8 && hidden > 16384) return false;  // the rows' scales stay in shared memory
   // passes (at most one a row) x tiles x stages of either product
   const long long stages = std::max<long long>(
       static_cast<long long>(inter / 64) * ((hidden + kStageK - 1) / kStageK),
       static_cast<long long>((hidden + kTileRows - 1) / kTileRows) *
           ((inter + kStageK - 1) / kStageK));
   if (rows * stages >= (1LL << 30)) return false;
-  return rows <= 1024 && few_smem(tokens, topk, num_experts, hidden, fp8).slots >= kMinSlots;
+  return rows <= 1024 && few_smem(tokens, topk, num_experts).slots >= kMinSlots;
 }
 
 cudaError_t launch_moe_few(const FewArgs& args, int sms, cudaStream_t stream) {
   FewParams p;
   p.a = args;
-  p.s = few_smem(args.tokens, args.topk, args.num_experts, args.hidden, args.x_fp8 != 0);
-  auto kernel = args.x_fp8 ? w4a16_moe_few_kernel<true> : w4a16_moe_few_kernel<false>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem);
+  p.s = few_smem(args.tokens, args.topk, args.num_experts);
+  const cudaError_t e = cudaFuncSetAttribute(
+      w4a16_moe_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<std::min(sms, kMaxCtas), kFewThreads, p.s.total, stream>>>(p);
+  w4a16_moe_few_kernel<<<std::min(sms, kMaxCtas), kFewThreads, p.s.total, stream>>>(p);
   return cudaGetLastError();
 }
 
