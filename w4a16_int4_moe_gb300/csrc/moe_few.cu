@@ -9,7 +9,7 @@
 // them once. The kernel is built around that stream:
 //
 //   * one persistent CTA per SM; both products are cut into stages of 128
-//     weight rows x 128 k (9216 packed bytes) and every CTA takes an equal,
+//     weight rows x 256 k (18432 packed bytes) and every CTA takes an equal,
 //     contiguous run of them, first of gate_up, then of down, so that all SMs
 //     read the same number of bytes whatever the number of experts;
 //   * two threads copy the stages into a shared-memory ring (bulk copies);
@@ -19,8 +19,8 @@
 //     000qqqq and 000qqqq0000 are subnormal FP16 numbers, q * 2^-24 and
 //     q * 2^-20, so a word of eight codes becomes four MMA registers with one
 //     shift and four ANDs. The 8 that every code is too large comes off as the
-//     number that the sums start from, -8 times the sum of the columns' values
-//     in the group, made once per row. Weights are the M side, the rows of an
+//     number that a group's sums start from, -8 times the columns, from two
+//     more MMAs a group. Weights are the M side, the rows of an
 //     expert (at most four per pass over its weights) the N side; the scale of
 //     a group of 32 is applied to the group's FP32 sum, so no weight is
 //     rounded. The codes never leave registers: through TMEM, as the tcgen05
@@ -68,8 +68,9 @@ constexpr int kWarpEpilogue0 = kComputeWarps + kWeightWarps;
 constexpr int kEpilogueWarps = 2;
 constexpr int kEpilogueThreads = 32 * kEpilogueWarps;
 constexpr int kFewThreads = kComputeThreads + 32 * kWeightWarps + kEpilogueThreads;
-constexpr int kWStage = 2 * kStepBytes;      // packed bytes of a stage: two 64-k steps
-constexpr int kStageK = 2 * kKStep;
+constexpr int kWStage = 4 * kStepBytes;      // packed bytes of a stage: four 64-k steps
+constexpr int kStageK = 4 * kKStep;
+constexpr int kHalfK = kStageK / 2;          // columns that a lane holds at a time
 constexpr int kRowsPerPass = 4;              // rows of an expert per pass over its weights
 constexpr int kActParts = 2;                 // FP16 parts of an activation value
 constexpr float kPartScale = 2048.f;         // the second part is the rest times this
@@ -77,7 +78,7 @@ constexpr float kCodeScale = 16777216.f;     // a code is q * 2^-24
 constexpr int kSumPitch = 132;               // FP32 sums [row][128 + 4]
 constexpr int kMaxCtas = 192;
 constexpr int kMinSlots = 4;
-constexpr int kMaxSlots = 16;  // 147 KB in flight (more measured slower)
+constexpr int kMaxSlots = 8;  // 147 KB in flight (more measured slower)
 constexpr int kFewMaxSmem = 232448;
 constexpr long long kFewDrainCycles = 4000000000LL;
 
@@ -100,21 +101,16 @@ __host__ __device__ inline size_t share_floats(int tokens) {
   return static_cast<size_t>(tokens > kRowsPerPass ? tokens : kRowsPerPass) * kTileRows;
 }
 
-// An MMA operand: `rows` rows of k FP16 values, of every group of 32 the start
-// of its sums (-8 times the values' sum, as the codes are too large by 8), and
-// of every `block` columns the factor of the values. Rows are padded to whole
-// stages of 128 columns in the starts and factors.
+// An MMA operand: `rows` rows of k FP16 values, and of every `block` columns
+// the factor of the values (a row's factors padded to whole stages).
 struct Operand {
-  size_t starts, factors, bytes;  // byte offsets, total
-  int groups, blocks;             // of a row
+  size_t factors, bytes;  // byte offset, total
+  int blocks;             // of a row
 };
 __host__ __device__ inline Operand operand(size_t rows, int k, int block) {
   Operand o;
-  const int stages = (k + kStageK - 1) / kStageK;
-  o.groups = stages * (kStageK / kGroup);
-  o.blocks = stages * (kStageK / block);
-  o.starts = rows * k * 2;  // (k is a multiple of 32)
-  o.factors = o.starts + rows * o.groups * 4;
+  o.blocks = (k + kStageK - 1) / kStageK * (kStageK / block);
+  o.factors = rows * k * 2;  // (k is a multiple of 32)
   o.bytes = (o.factors + rows * o.blocks * 4 + 15) / 16 * 16;
   return o;
 }
@@ -191,19 +187,15 @@ __device__ __forceinline__ float block_factor(uint32_t max_bits) {
 // Value k of a row as the MMAs take it: the codes k = 2, 3 of every four lie
 // four bits higher in their word, times 16.
 __device__ __forceinline__ float column_value(int k, float y) { return k & 2 ? y * 0.0625f : y; }
-constexpr float kStartScale = -8.f / kCodeScale;
 
-// The columns of one stage in a lane's registers: thread t of a quad holds
-// k = 8t .. 8t + 7 of each of the four groups of its MMA column, and the starts
-// and factors of the columns that it accumulates. They come straight from L1
-// or L2, right after the same groups of the stage before were used (a few rows
-// stay there; copying them through the ring cost one warp 730 cycles a stage,
-// against the 390 of the copy bandwidth). All of it was written by this
-// launch: no read-only loads. kCols: accumulated columns of a thread.
-template <int kCols>
+// The columns of half a stage in a lane's registers: thread t of a quad holds
+// k = 8t .. 8t + 7 of each of the four groups of its MMA column. They come
+// straight from L1 or L2, right after the same groups of the half before were
+// used (a few rows stay there; copying them through the ring cost one warp 730
+// cycles per 128 columns, against the 390 of the copy bandwidth). They were
+// written by this launch: no read-only loads.
 struct Cols {
   uint4 b[4];
-  float4 start[kCols];  // of the four groups
 };
 __device__ __forceinline__ uint4 load16(const void* from) {
   return *reinterpret_cast<const uint4*>(from);
@@ -219,9 +211,10 @@ __device__ __forceinline__ uint4 load16(const void* from) {
 // whose addresses repeat two 16-byte runs.
 template <int kCols, int kG>
 __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const uint4& b0,
-                                         const uint4& b1, const float2 (&start)[kCols],
+                                         const uint4& b1,
                                          float (&acc)[2][2 * kCols]) {
   constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+  const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};
   uint32_t w[kG][4], sc[4];
 #pragma unroll
   for (int g = 0; g < kG; ++g) ldmatrix_x4(codes + g * (kTileRows * 16), w[g]);
@@ -229,48 +222,45 @@ __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const 
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
     const uint4 b = g == 0 ? b0 : b1;
-    const float i0 = g == 0 ? start[0].x : start[0].y;
-    const float i1 = kCols == 1 ? 0.f : g == 0 ? start[kCols - 1].x : start[kCols - 1].y;
+    float i[4];
+    mma16816(i, minus8, b.x, b.y, 0.f, 0.f, 0.f, 0.f);
+    mma16816(i, minus8, b.z, b.w, i[0], i[1], i[2], i[3]);
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const uint32_t w0 = w[g][2 * mt], w1 = w[g][2 * mt + 1], v0 = w0 >> 8, v1 = w1 >> 8;
       const uint32_t a0[4] = {w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh};
       const uint32_t a1[4] = {v0 & kLow, v1 & kLow, v0 & kHigh, v1 & kHigh};
       float c[4];
-      mma16816(c, a0, b.x, b.y, i0, i1, i0, i1);
+      mma16816(c, a0, b.x, b.y, i[0], i[1], i[2], i[3]);
       mma16816(c, a1, b.z, b.w, c[0], c[1], c[2], c[3]);
       const uint32_t pair = sc[2 * g + mt];
       const float s0 = __uint_as_float(pair << 16), s1 = __uint_as_float(pair & 0xFFFF0000u);
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        acc[mt][i] = fmaf(s0, c[i], acc[mt][i]);
-        acc[mt][kCols + i] = fmaf(s1, c[2 + i], acc[mt][kCols + i]);
+      for (int j = 0; j < kCols; ++j) {
+        acc[mt][j] = fmaf(s0, c[j], acc[mt][j]);
+        acc[mt][kCols + j] = fmaf(s1, c[2 + j], acc[mt][kCols + j]);
       }
     }
   }
 }
 
-// One stage: its `valid` groups (1..4), scaled by the factors of its two 64-k
-// steps, then, into the registers they leave, the columns of the next stage
-// (`next_valid` groups at `next`, 0 for none).
+// Half a stage: its `valid` groups (1..4, none for 0 or less), scaled by the
+// factors of its two 64-k steps, then, into the registers they leave, the
+// columns of the next half (`next_valid` groups at `next`).
+// kCols: accumulated columns of a thread.
 template <int kCols>
-__device__ __forceinline__ void stage_mma(int valid, uint32_t codes, uint32_t scales,
-                                          Cols<kCols>& x, float2 factor, const uint8_t* next,
-                                          int next_valid, float (&acc)[2][2 * kCols]) {
+__device__ __forceinline__ void half_mma(int valid, uint32_t codes, uint32_t scales, Cols& x,
+                                         float2 factor, const uint8_t* next, int next_valid,
+                                         float (&acc)[2][2 * kCols]) {
   const auto step = [&](auto st, int n, int next_n) {
     constexpr int kS = decltype(st)::value;
-    float2 start[kCols];
-#pragma unroll
-    for (int i = 0; i < kCols; ++i)
-      start[i] = kS == 0 ? make_float2(x.start[i].x, x.start[i].y)
-                         : make_float2(x.start[i].z, x.start[i].w);
     float part[2][2 * kCols] = {};
     if (n >= 2)
       step_mma<kCols, 2>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
-                         x.b[2 * kS + 1], start, part);
+                         x.b[2 * kS + 1], part);
     else if (n == 1)
       step_mma<kCols, 1>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
-                         x.b[2 * kS + 1], start, part);
+                         x.b[2 * kS + 1], part);
     const float f = kS == 0 ? factor.x : factor.y;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
@@ -285,6 +275,23 @@ __device__ __forceinline__ void stage_mma(int valid, uint32_t codes, uint32_t sc
   } else {
     step(std::integral_constant<int, 0>(), valid, next_valid);
     step(std::integral_constant<int, 1>(), valid - 2, next_valid - 2);
+  }
+}
+
+// A stage in two halves; factor[h]: of the steps of half h.
+template <int kCols>
+__device__ __forceinline__ void stage_mma(int valid, uint32_t codes, uint32_t scales, Cols& x,
+                                          float4 factor, const uint8_t* here, const uint8_t* next,
+                                          int next_valid, float (&acc)[2][2 * kCols]) {
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    half_mma<kCols>(valid, codes, scales, x, make_float2(factor.x, factor.y),
+                    h == 0 ? here + 2 * kHalfK : next, h == 0 ? valid - 4 : next_valid, acc);
+    valid -= 4;
+    codes += 2 * kStepBytes;
+    scales += 2 * kStepBytes;
+    factor.x = factor.z;
+    factor.y = factor.w;
   }
 }
 
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   const size_t share = share_floats(a.tokens);
   // the two operands: the rows, and the activation's parts (row r, part p: row 2r + p)
   uint8_t* x_op = reinterpret_cast<uint8_t*>(shares + 2 * kMaxCtas * share);
-  const Operand xo = operand(a.tokens, a.hidden, kStageK);
+  const Operand xo = operand(a.tokens, a.hidden, kHalfK);
   uint8_t* act_op = x_op + xo.bytes;
   const Operand ao = operand(static_cast<size_t>(rows_cap) * kActParts, a.inter, kKStep);
 
@@ -420,11 +427,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     // this CTA's share of the rows into FP16: sixteen lanes a block of 128
     const int half = (tid - kComputeThreads) >> 4, l16 = lane & 15;
     constexpr int kHalves = (kFewThreads - kComputeThreads) / 16;
-    const int row_blocks = (a.hidden + kStageK - 1) / kStageK;  // of the input's scales too
+    const int row_blocks = (a.hidden + kHalfK - 1) / kHalfK;  // of the input's scales too
     const int blocks = a.tokens * row_blocks;
     for (int b0 = blockIdx.x * kHalves; b0 < blocks; b0 += gridDim.x * kHalves) {
       const int blk = min(b0 + half, blocks - 1);  // (the last ones may repeat a block)
-      const int tok = blk / row_blocks, kb = blk - tok * row_blocks, k0 = kb * kStageK + l16 * 8;
+      const int tok = blk / row_blocks, kb = blk - tok * row_blocks, k0 = kb * kHalfK + l16 * 8;
       const long long at = static_cast<long long>(tok) * a.hidden + k0;
       const bool in = k0 < a.hidden;
       float y[8];
@@ -460,23 +467,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         for (int i = 0; i < 8; ++i) y[i] *= factor;
         out_factor = 1.f / factor;
       }
-      float sum = 0.f;
       uint32_t packed[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        sum += y[2 * i] + y[2 * i + 1];
         const __half2 h = __floats2half2_rn(column_value(2 * i, y[2 * i]),
                                             column_value(2 * i + 1, y[2 * i + 1]));
         packed[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);  // four lanes a group of 32
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       if (in)
         *reinterpret_cast<uint4*>(x_op + at * 2) =
             make_uint4(packed[0], packed[1], packed[2], packed[3]);
-      if ((l16 & 3) == 0)
-        reinterpret_cast<float*>(x_op + xo.starts)[tok * xo.groups + kb * 4 + (l16 >> 2)] =
-            sum * kStartScale;
       if (l16 == 0)
         reinterpret_cast<float*>(x_op + xo.factors)[tok * xo.blocks + kb] = out_factor;
     }
@@ -594,8 +594,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   const int steps0 = (a.hidden + kKStep - 1) / kKStep, steps1 = (a.inter + kKStep - 1) / kKStep;
   const int groups0 = a.hidden / kGroup, groups1 = a.inter / kGroup;
   const int tiles0 = a.inter / 64, tiles1 = (a.hidden + kTileRows - 1) / kTileRows;
-  const Split gu(num_chunks * tiles0, (steps0 + 1) / 2, gridDim.x);
-  const Split dn(num_chunks * tiles1, (steps1 + 1) / 2, gridDim.x);
+  const Split gu(num_chunks * tiles0, (steps0 + 3) / 4, gridDim.x);
+  const Split dn(num_chunks * tiles1, (steps1 + 3) / 4, gridDim.x);
   const int cta = blockIdx.x;
   const int gu_begin = cta < gu.grid ? gu.begin(cta) : 0, gu_end = cta < gu.grid ? gu.begin(cta + 1) : 0;
   const int dn_begin = cta < dn.grid ? dn.begin(cta) : 0, dn_end = cta < dn.grid ? dn.begin(cta + 1) : 0;
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
             ok = false;
             break;
           }
-          const uint32_t bytes = min(2, steps - 2 * s) * kStepBytes;
+          const uint32_t bytes = min(4, steps - 4 * s) * kStepBytes;
           mbar_arrive_expect_tx(bar_w + 8 * slot, bytes);
           bulk_g2s(ring + slot * kWStage, src + static_cast<long long>(s) * kWStage, bytes,
                    bar_w + 8 * slot, policy);
@@ -707,25 +707,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         return row_token[static_cast<int>(ch >> 16) + min(r, static_cast<int>(ch >> 10 & 7u))];
       };
       const uint8_t* cols = nullptr;   // from k = 8t on
-      const float* starts = nullptr;
       const float* factors = nullptr;
       const auto point = [&](int q) {
         cols = x_op + static_cast<long long>(token_of(q, g >> 1)) * a.hidden * 2 + t * 16;
         const int tok = token_of(q, t);
-        starts = reinterpret_cast<const float*>(x_op + xo.starts) + tok * xo.groups;
         factors = reinterpret_cast<const float*>(x_op + xo.factors) + tok * xo.blocks;
       };
-      Cols<1> x = {};
-      float next_factor = 0.f;
+      Cols x = {};
+      float2 next_factor = make_float2(0.f, 0.f);  // of both halves
       int at = gu_begin + grp;
       int next_q = at / S, next_s = at - next_q * S;  // item and stage of `at`
       if (at < gu_end) {
         point(next_q);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (i < groups0 - 4 * next_s) x.b[i] = load16(cols + next_s * (2 * kStageK) + i * 64);
-        x.start[0] = *reinterpret_cast<const float4*>(starts + 4 * next_s);
-        next_factor = factors[next_s];
+          if (i < groups0 - 8 * next_s) x.b[i] = load16(cols + next_s * (2 * kStageK) + i * 64);
+        next_factor = *reinterpret_cast<const float2*>(factors + 2 * next_s);
       }
       const int q_end = (gu_end - 1) / S;
       for (int q = gu_begin / S; q <= q_end; ++q) {
@@ -733,7 +730,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         float acc[2][2] = {};
 #pragma unroll 1
         while (next_q == q && at < gu_end) {
-          const int valid = groups0 - 4 * next_s;
+          const int valid = groups0 - 8 * next_s;
+          const uint8_t* here = cols + next_s * (2 * kStageK);
           at += kGroups;
           next_s += kGroups;
           while (next_s >= S) {
@@ -741,18 +739,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
             ++next_q;
           }
           int next_valid = 0;
-          const float factor = next_factor;
-          float4 next_start = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float2 factor = next_factor;
           if (at < gu_end) {
             if (next_q != q) point(next_q);
-            next_valid = groups0 - 4 * next_s;
-            next_start = *reinterpret_cast<const float4*>(starts + 4 * next_s);
-            next_factor = factors[next_s];
+            next_valid = groups0 - 8 * next_s;
+            next_factor = *reinterpret_cast<const float2*>(factors + 2 * next_s);
           }
           const uint32_t base = wait_stage();
-          stage_mma<1>(valid, base + codes_at, base + scales_at, x, make_float2(factor, factor),
+          stage_mma<1>(valid, base + codes_at, base + scales_at, x,
+                       make_float4(factor.x, factor.x, factor.y, factor.y), here,
                        cols + next_s * (2 * kStageK), next_valid, acc);
-          x.start[0] = next_start;
           free_stage();
         }
         // [row of the pass][128] of this warpgroup, in the buffers by turns
@@ -783,7 +779,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
       // thread t of a quad accumulates row t of the pass, its two parts as MMA
       // columns 2t and 2t + 1 (rows past the last repeat it)
       const uint8_t* cols = nullptr;  // from k = 8t on
-      const float* starts = nullptr;  // of the first part, then of the second
       const float* factors = nullptr;
       const auto point = [&](int c) {
         const uint32_t ch = chunks[c];
@@ -791,15 +786,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         const long long part_row = (row0 + min(g >> 1, last)) * kActParts + (g & 1);
         cols = act_op + part_row * a.inter * 2 + t * 16;
         const long long first = (row0 + min(t, last)) * kActParts;
-        starts = reinterpret_cast<const float*>(act_op + ao.starts) + first * ao.groups;
         factors = reinterpret_cast<const float*>(act_op + ao.factors) + first * ao.blocks;
       };
-      const auto load_starts = [&](int st, float4 (&to)[2]) {
-        to[0] = *reinterpret_cast<const float4*>(starts + 4 * st);
-        to[1] = *reinterpret_cast<const float4*>(starts + ao.groups + 4 * st);
-      };
-      Cols<2> x = {};
-      float2 next_factor = make_float2(0.f, 0.f);  // of both 64-k steps
+      Cols x = {};
+      float4 next_factor = make_float4(0.f, 0.f, 0.f, 0.f);  // of the four 64-k steps
       int at = dn_begin + ((grp - gu_count) & 3);
       int next_c = at / S, next_s = at - next_c * S;  // pass and stage of `at`
       next_c %= num_chunks;
@@ -807,9 +797,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         point(next_c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (i < groups1 - 4 * next_s) x.b[i] = load16(cols + next_s * (2 * kStageK) + i * 64);
-        load_starts(next_s, x.start);
-        next_factor = *reinterpret_cast<const float2*>(factors + 2 * next_s);
+          if (i < groups1 - 8 * next_s) x.b[i] = load16(cols + next_s * (2 * kStageK) + i * 64);
+        next_factor = *reinterpret_cast<const float4*>(factors + 4 * next_s);
       }
       const int tile_stages = num_chunks * S;
       const int tile_end = (dn_end - 1) / tile_stages;
@@ -827,13 +816,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
           bool more = true;  // own stages left in this pass
 #pragma unroll 1
           while (more) {
-            const int valid = groups1 - 4 * next_s;
+            const int valid = groups1 - 8 * next_s;
+            const uint8_t* here = cols + next_s * (2 * kStageK);
             at += kGroups;
             next_s += kGroups;
             more = next_s < S && at < stop;
             int next_valid = 0;
-            const float2 factor = next_factor;
-            float4 next_start[2] = {};
+            const float4 factor = next_factor;
             if (at < dn_end) {
               if (next_s >= S) {
                 do {
@@ -842,15 +831,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
                 } while (next_s >= S);
                 point(next_c);
               }
-              next_valid = groups1 - 4 * next_s;
-              load_starts(next_s, next_start);
-              next_factor = *reinterpret_cast<const float2*>(factors + 2 * next_s);
+              next_valid = groups1 - 8 * next_s;
+              next_factor = *reinterpret_cast<const float4*>(factors + 4 * next_s);
             }
             const uint32_t base = wait_stage();
-            stage_mma<2>(valid, base + codes_at, base + scales_at, x, factor,
+            stage_mma<2>(valid, base + codes_at, base + scales_at, x, factor, here,
                          cols + next_s * (2 * kStageK), next_valid, acc);
-            x.start[0] = next_start[0];
-            x.start[1] = next_start[1];
             free_stage();
           }
           if (t <= last) {
@@ -943,12 +929,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
               for (int p = 0; p < kActParts; ++p) {
                 reinterpret_cast<__half*>(act_op)[(row + p) * a.inter + inner * 64 + c] =
                     __float2half_rn(column_value(c, value[p]));
-                float sum = value[p];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane == 0)
-                  reinterpret_cast<float*>(act_op + ao.starts)[(row + p) * ao.groups + inner * 2 +
-                                                              (etid >> 5)] = sum * kStartScale;
               }
               if (etid == 0)
                 reinterpret_cast<float*>(act_op + ao.factors)[row * ao.blocks + inner] =
@@ -1078,7 +1058,7 @@ size_t few_workspace_bytes(int tokens, int topk, int hidden, int inter) {
   const int t = std::max(1, tokens);
   const size_t rows = max_rows(t, topk);
   return kStatusBytes + kCounterBytes + 2 * kMaxCtas * share_floats(t) * sizeof(float) +
-         operand(t, hidden, kStageK).bytes + operand(rows * kActParts, inter, kKStep).bytes;
+         operand(t, hidden, kHalfK).bytes + operand(rows * kActParts, inter, kKStep).bytes;
 }
 
 bool few_supported(int tokens, int topk, int num_experts, int hidden, int inter) {
