@@ -15,7 +15,7 @@
 //   * two threads copy the stages into a shared-memory ring (bulk copies);
 //     they run through both products without waiting for the activation, so
 //     the ring is full of down weights when the activation is complete;
-//   * sixteen warps feed the codes to m16n8k16 MMAs of FP16 operands: the bits
+//   * eight warps feed the codes to m16n8k16 MMAs of FP16 operands: the bits
 //     000qqqq and 000qqqq0000 are subnormal FP16 numbers, q * 2^-24 and
 //     q * 2^-20, so a word of eight codes becomes four MMA registers with one
 //     shift and four ANDs. The 8 that every code is too large comes off as the
@@ -57,7 +57,9 @@ namespace w4a16 {
 namespace {
 
 constexpr int kGroups = 4;                   // warpgroups; group g takes every fourth stage
-constexpr int kComputeWarps = 4 * kGroups;
+constexpr int kGroupWarps = 2;               // of 64 weight rows each
+constexpr int kComputeWarps = kGroupWarps * kGroups;
+constexpr int kMt = 4;                       // 16-row MMA tiles of a warp
 constexpr int kComputeThreads = 32 * kComputeWarps;
 // Two warps issue the weight copies by turns: one thread gets round its loop
 // (wait for the slot, announce the bytes, copy) only every 620 cycles, 4.4 TB/s
@@ -201,7 +203,7 @@ __device__ __forceinline__ uint4 load16(const void* from) {
   return *reinterpret_cast<const uint4*>(from);
 }
 
-// kG groups of 32 k of one 64-k step: 32 weight rows of this warp (two 16-row
+// kG groups of 32 k of one 64-k step: 64 weight rows of this warp (four 16-row
 // MMA tiles) times eight columns, of which a thread keeps the even one or
 // both; acc += scale * sum of every group.
 // k order inside a group: thread t of a quad holds word t of each weight row
@@ -211,14 +213,17 @@ __device__ __forceinline__ uint4 load16(const void* from) {
 // whose addresses repeat two 16-byte runs.
 template <int kCols, int kG>
 __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const uint4& b0,
-                                         const uint4& b1,
-                                         float (&acc)[2][2 * kCols]) {
+                                         const uint4& b1, float (&acc)[kMt][2 * kCols]) {
   constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
   const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};
-  uint32_t w[kG][4], sc[4];
+  uint32_t w[kG][kMt / 2][4], sc[kMt / 2][4];
 #pragma unroll
-  for (int g = 0; g < kG; ++g) ldmatrix_x4(codes + g * (kTileRows * 16), w[g]);
-  ldmatrix_x4_trans(scales, sc);
+  for (int g = 0; g < kG; ++g)
+#pragma unroll
+    for (int h = 0; h < kMt / 2; ++h)
+      ldmatrix_x4(codes + g * (kTileRows * 16) + h * 512, w[g][h]);
+#pragma unroll
+  for (int h = 0; h < kMt / 2; ++h) ldmatrix_x4_trans(scales + h * 64, sc[h]);
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
     const uint4 b = g == 0 ? b0 : b1;
@@ -226,14 +231,15 @@ __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const 
     mma16816(i, minus8, b.x, b.y, 0.f, 0.f, 0.f, 0.f);
     mma16816(i, minus8, b.z, b.w, i[0], i[1], i[2], i[3]);
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t w0 = w[g][2 * mt], w1 = w[g][2 * mt + 1], v0 = w0 >> 8, v1 = w1 >> 8;
+    for (int mt = 0; mt < kMt; ++mt) {
+      const uint32_t w0 = w[g][mt >> 1][2 * (mt & 1)], w1 = w[g][mt >> 1][2 * (mt & 1) + 1];
+      const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
       const uint32_t a0[4] = {w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh};
       const uint32_t a1[4] = {v0 & kLow, v1 & kLow, v0 & kHigh, v1 & kHigh};
       float c[4];
       mma16816(c, a0, b.x, b.y, i[0], i[1], i[2], i[3]);
       mma16816(c, a1, b.z, b.w, c[0], c[1], c[2], c[3]);
-      const uint32_t pair = sc[2 * g + mt];
+      const uint32_t pair = sc[mt >> 1][2 * g + (mt & 1)];
       const float s0 = __uint_as_float(pair << 16), s1 = __uint_as_float(pair & 0xFFFF0000u);
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
@@ -251,10 +257,10 @@ __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const 
 template <int kCols>
 __device__ __forceinline__ void half_mma(int valid, uint32_t codes, uint32_t scales, Cols& x,
                                          float2 factor, const uint8_t* next, int next_valid,
-                                         float (&acc)[2][2 * kCols]) {
+                                         float (&acc)[kMt][2 * kCols]) {
   const auto step = [&](auto st, int n, int next_n) {
     constexpr int kS = decltype(st)::value;
-    float part[2][2 * kCols] = {};
+    float part[kMt][2 * kCols] = {};
     if (n >= 2)
       step_mma<kCols, 2>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
                          x.b[2 * kS + 1], part);
@@ -263,7 +269,7 @@ __device__ __forceinline__ void half_mma(int valid, uint32_t codes, uint32_t sca
                          x.b[2 * kS + 1], part);
     const float f = kS == 0 ? factor.x : factor.y;
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int i = 0; i < 2 * kCols; ++i) acc[mt][i] = fmaf(f, part[mt][i], acc[mt][i]);
     if (next_n > 0) x.b[2 * kS] = load16(next + kS * 128);
@@ -282,7 +288,7 @@ __device__ __forceinline__ void half_mma(int valid, uint32_t codes, uint32_t sca
 template <int kCols>
 __device__ __forceinline__ void stage_mma(int valid, uint32_t codes, uint32_t scales, Cols& x,
                                           float4 factor, const uint8_t* here, const uint8_t* next,
-                                          int next_valid, float (&acc)[2][2 * kCols]) {
+                                          int next_valid, float (&acc)[kMt][2 * kCols]) {
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     half_mma<kCols>(valid, codes, scales, x, make_float2(factor.x, factor.y),
@@ -303,6 +309,24 @@ __device__ __forceinline__ bool few_wait(uint32_t bar, uint32_t parity, volatile
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait_sleep(bar, parity, 1000000)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > timeout) {
+      *abort_flag = 1;
+      atomicCAS(status, 0, 0x1000 | where);
+      return false;
+    }
+  }
+}
+
+// Until the counter that other CTAs raise has reached `want`; false if the
+// wait gave up.
+__device__ __forceinline__ bool wait_count(const int* counter, int want, volatile int* abort_flag,
+                                           int* status, int where, long long timeout) {
+  const long long t0 = clock64();
+  while (true) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+    if (v >= want) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > timeout) {
       *abort_flag = 1;
@@ -378,7 +402,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
 
   const uint32_t bar_w = smem_u32(smem), bar_e = bar_w + 8 * kMaxSlots;  // slots full, slots free
   const uint32_t bar_sf = bar_w + 16 * kMaxSlots, bar_se = bar_sf + 16;  // sums full, free
-  const uint32_t bar_act = bar_se + 16, bar_rows = bar_act + 8;  // activation, rows in FP16
+  const uint32_t bar_act = bar_se + 16;  // activation complete
   int* scalars = reinterpret_cast<int*>(smem + 16 * kMaxSlots + 64);
   volatile int* abort_flag = scalars;
   int* last_arrival = scalars + 1;
@@ -409,7 +433,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   if (warp == kFewThreads / 32 - 1) {
     if (lane < sm.slots) {
       mbar_init(bar_w + 8 * lane, 1);
-      mbar_init(bar_e + 8 * lane, 4);
+      mbar_init(bar_e + 8 * lane, kGroupWarps);
     }
     if (lane < 2) {
       mbar_init(bar_sf + 8 * lane, kComputeWarps);
@@ -417,7 +441,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     }
     if (lane == 0) {
       mbar_init(bar_act, 1);
-      mbar_init(bar_rows, 1);
       *abort_flag = 0;
     }
     fence_mbar_init();
@@ -480,33 +503,30 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
       if (l16 == 0)
         reinterpret_cast<float*>(x_op + xo.factors)[tok * xo.blocks + kb] = out_factor;
     }
-    asm volatile("bar.sync 2, %0;" ::"n"(kFewThreads - kComputeThreads) : "memory");
-    if (tid == kComputeThreads) {
-      __threadfence();
-      atomicAdd(&counters->rows_done, 1);
-    }
   }
-  if (a.logits != nullptr) {
-    for (int t = warp; t < a.tokens && warp < kComputeWarps; t += kComputeWarps) {
+  // ... and of the routing: one warp a token, so that a call of many tokens
+  // waits for one token's routing only
+  if (a.logits != nullptr && warp == 0)
+    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
       if (a.num_global <= 512)
         route_token<16>(a.logits, a.bf16_logits, t, a.num_global, a.topk, a.renormalize,
-                        a.expert_offset, a.num_experts, s_ids, s_weights);
+                        a.expert_offset, a.num_experts, a.topk_ids, a.topk_weights);
       else
         route_token<32>(a.logits, a.bf16_logits, t, a.num_global, a.topk, a.renormalize,
-                        a.expert_offset, a.num_experts, s_ids, s_weights);
+                        a.expert_offset, a.num_experts, a.topk_ids, a.topk_weights);
     }
-  } else {
-    for (int i = tid; i < rows_cap; i += kFewThreads) {
-      s_ids[i] = a.topk_ids[i];
-      s_weights[i] = a.topk_weights[i];
-    }
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    atomicAdd(&counters->rows_done, 1);
+    wait_count(&counters->rows_done, gridDim.x, abort_flag, status, kWhereRows, a.timeout_cycles);
   }
   __syncthreads();
-  if (a.logits != nullptr && blockIdx.x == 0)
-    for (int i = tid; i < rows_cap; i += kFewThreads) {
-      a.topk_ids[i] = s_ids[i];
-      a.topk_weights[i] = s_weights[i];
-    }
+  for (int i = tid; i < rows_cap; i += kFewThreads) {
+    s_ids[i] = __ldcg(a.topk_ids + i);
+    s_weights[i] = __ldcg(a.topk_weights + i);
+  }
+  __syncthreads();
   // bit t of an expert's mask: token t goes there
   for (int i = tid; i < rows_cap; i += kFewThreads) {
     const int e = s_ids[i];
@@ -514,19 +534,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   }
   __syncthreads();
   // running sums over the experts of (rows, passes of up to four rows):
-  // thread i of the first 512 holds experts 2i and 2i + 1
+  // thread i of the compute warps holds kOwn experts from kOwn * i on
   const auto rows_and_passes = [](uint32_t mask) {
     const uint32_t n = __popc(mask);
     return n | (n + kRowsPerPass - 1) / kRowsPerPass << 16;
   };
-  uint32_t mine[2] = {0u, 0u}, own[2] = {0u, 0u}, incl = 0u;
+  constexpr int kOwn = 1024 / kComputeThreads;
+  uint32_t mine[kOwn] = {}, own = 0u, incl = 0u;
   if (warp < kComputeWarps) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      mine[i] = 2 * tid + i < a.num_experts ? s_mask[2 * tid + i] : 0u;
-      own[i] = rows_and_passes(mine[i]);
+    for (int i = 0; i < kOwn; ++i) {
+      mine[i] = kOwn * tid + i < a.num_experts ? s_mask[kOwn * tid + i] : 0u;
+      own += rows_and_passes(mine[i]);
     }
-    incl = own[0] + own[1];
+    incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -538,11 +559,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   if (warp < kComputeWarps) {
     const uint32_t v = lane < kComputeWarps ? static_cast<uint32_t>(warp_sums[lane]) : 0u;
     const uint32_t all = __reduce_add_sync(0xffffffffu, v);
-    uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0u) + incl - own[0] - own[1];
+    uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0u) + incl - own;
     if (tid == 0) *num_chunks_p = static_cast<int>(all >> 16);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = 2 * tid + i, n = __popc(mine[i]);
+    for (int i = 0; i < kOwn; ++i) {
+      const int e = kOwn * tid + i, n = __popc(mine[i]);
       if (n > 0) {
         const int row = static_cast<int>(before & 0xFFFFu);
         int c = static_cast<int>(before >> 16);
@@ -553,7 +574,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
                         static_cast<uint32_t>(min(kRowsPerPass, n - r) - 1) << 10 |
                         static_cast<uint32_t>(row + r) << 16;
       }
-      before += own[i];
+      before += rows_and_passes(mine[i]);
     }
   }
   __syncthreads();
@@ -666,8 +687,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     // After a wait gave up every warp still walks its stages (on whatever the
     // ring holds), so that the epilogue warps and the other CTAs meet all the
     // arrivals they count on.
-    const int grp = warp >> 2;
-    const int m0 = (warp & 3) * 32;  // this warp's weight rows in a tile
+    const int grp = warp / kGroupWarps;
+    const int m0 = (warp % kGroupWarps) * 64;  // this warp's weight rows in a tile
     const int g = lane >> 2, t = lane & 3;
     int slot = grp;                  // slot and phase of this group's next stage
     uint32_t phase = 0;
@@ -697,9 +718,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
 
     if (gu_count > 0) {
       const int S = gu.stages;
-      if (live)
-        live = __all_sync(0xffffffffu, few_wait(bar_rows, 0, abort_flag, status, kWhereRows,
-                                                a.timeout_cycles));
       // thread t of a quad accumulates row t of the pass, as MMA column 2t
       // (column 2t + 1 is a copy; rows past the last repeat it)
       const auto token_of = [&](int q, int r) {
@@ -727,7 +745,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
       const int q_end = (gu_end - 1) / S;
       for (int q = gu_begin / S; q <= q_end; ++q) {
         // item q: this group's stages of it, then its sums to the epilogue
-        float acc[2][2] = {};
+        float acc[kMt][2] = {};
 #pragma unroll 1
         while (next_q == q && at < gu_end) {
           const int valid = groups0 - 8 * next_s;
@@ -756,7 +774,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         wait_sums(bar_se + 8 * buf, buf ? uses1 : uses0);
         float* my = sums + buf * kItemSums + grp * (kRowsPerPass * kSumPitch) + t * kSumPitch + m0 + g;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) my[mt * 16 + h * 8] = acc[mt][h] * kCodeScale;
         __syncwarp();
@@ -806,13 +824,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         // this group's stages of the tile, expert by expert: the passes' rows
         // are added to their tokens
         wait_sums(bar_se, uses0);
-        for (int tok = 0; tok < a.tokens; ++tok) my[tok * kSumPitch + lane] = 0.f;
+        for (int tok = 0; tok < a.tokens; ++tok) my[tok * kSumPitch + lane] = my[tok * kSumPitch + 32 + lane] = 0.f;
         __syncwarp();
         const int stop = min(dn_end, (tile + 1) * tile_stages);
         while (at < stop) {
           const uint32_t ch = chunks[next_c];
           const int last = static_cast<int>(ch >> 10 & 7u), row = static_cast<int>(ch >> 16) + t;
-          float acc[2][4] = {};
+          float acc[kMt][4] = {};
           bool more = true;  // own stages left in this pass
 #pragma unroll 1
           while (more) {
@@ -843,7 +861,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
             const float w = row_weight[row] * kCodeScale;
             float* dst = my + row_token[row] * kSumPitch + g;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float v = fmaf(acc[mt][2 * h + 1], 1.f / kPartScale, acc[mt][2 * h]);
@@ -862,27 +880,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     const int etid = tid - 32 * kWarpEpilogue0;
     bool live = true;
     uint32_t items = 0;  // sums taken, the two buffers by turns
-    // every CTA's arrivals at a counter, then one at a barrier of this CTA
-    const auto pass_on = [&](int* counter, int want, uint32_t bar, int where) {
-      const long long t0 = clock64();
-      while (true) {
-        int v;
-        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-        if (v >= want) {
-          mbar_arrive(bar);
-          break;
-        }
-        if (*abort_flag) break;
-        if (clock64() - t0 > a.timeout_cycles) {
-          *abort_flag = 1;
-          atomicCAS(status, 0, 0x1000 | where);
-          break;
-        }
-      }
-    };
-    if (gu_count > 0 && etid == 0)
-      pass_on(&counters->rows_done, static_cast<int>(gridDim.x), bar_rows, kWhereRows);
-    __syncwarp();
     if (gu_count > 0) {
       const int S = gu.stages;
       int q = gu_begin / S, at = gu_begin;
@@ -987,8 +984,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         ++q;
       }
     }
-    if (dn_end > dn_begin && etid == 0)  // every gate_up item of every CTA is out
-      pass_on(&counters->act_done, num_chunks * tiles0, bar_act, kWhereAct);
+    // every gate_up item of every CTA is out: the activation is complete
+    if (dn_end > dn_begin && etid == 0 &&
+        wait_count(&counters->act_done, num_chunks * tiles0, abort_flag, status, kWhereAct,
+                   a.timeout_cycles))
+      mbar_arrive(bar_act);
     __syncwarp();
     if (dn_end > dn_begin) {
       const int tile_stages = num_chunks * dn.stages;
