@@ -623,65 +623,76 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   const int gu_count = gu_end - gu_begin;
 
   if (warp >= kWarpWeights0 && warp < kWarpEpilogue0) {
-    // ---- weight copies (one thread of each warp) ----
-    if (lane == 0) {
-      const uint64_t policy = policy_evict_first();
-      const int first = warp - kWarpWeights0;
-      int slot = first;
-      uint32_t phase = 0;
-      int next = first;  // stage of this CTA, over both products
-      bool ok = true;
+    // ---- weight copies, by lane 0; lanes 16 to 31 bring the lines of the rows
+    // that the stage will meet into L1 (four rows of four lines) ----
+    const uint64_t policy = policy_evict_first();
+    const int first = warp - kWarpWeights0;
+    int slot = first;
+    uint32_t phase = 0;
+    int next = first;  // stage of this CTA, over both products
+    bool ok = true;
 #pragma unroll
-      for (int ph = 0; ph < 2; ++ph) {
-        const int begin = ph == 0 ? gu_begin : dn_begin - gu_count;
-        const int end = ph == 0 ? gu_end : dn_end;
-        if (!ok || begin + next >= end) continue;
-        const int S = ph == 0 ? gu.stages : dn.stages;
-        const int steps = ph == 0 ? steps0 : steps1;
-        const int inner_n = ph == 0 ? tiles0 : num_chunks;
-        const int q = (begin + next) / S;
-        int s = begin + next - q * S, outer = q / inner_n, inner = q - outer * inner_n;
-        const uint8_t* base = ph == 0 ? a.gate_up : a.down;
-        const long long expert_bytes = ph == 0 ? a.gate_up_expert_bytes : a.down_expert_bytes;
-        const uint8_t* src = nullptr;
-        bool fresh = true;
-        for (; begin + next < end; next += kWeightWarps) {
-          if (fresh) {
-            const int c = ph == 0 ? outer : inner, tile = ph == 0 ? inner : outer;
-            src = base + (chunks[c] & 1023u) * expert_bytes +
-                  static_cast<long long>(tile) * steps * kStepBytes;
-            fresh = false;
+    for (int ph = 0; ph < 2; ++ph) {
+      const int begin = ph == 0 ? gu_begin : dn_begin - gu_count;
+      const int end = ph == 0 ? gu_end : dn_end;
+      if (!ok || begin + next >= end) continue;
+      const int S = ph == 0 ? gu.stages : dn.stages;
+      const int steps = ph == 0 ? steps0 : steps1;
+      const int inner_n = ph == 0 ? tiles0 : num_chunks;
+      const int q = (begin + next) / S;
+      int s = begin + next - q * S, outer = q / inner_n, inner = q - outer * inner_n;
+      const uint8_t* base = ph == 0 ? a.gate_up : a.down;
+      const long long expert_bytes = ph == 0 ? a.gate_up_expert_bytes : a.down_expert_bytes;
+      const uint8_t* src = nullptr;
+      const uint8_t* line = nullptr;
+      bool fresh = true;
+      for (; begin + next < end; next += kWeightWarps) {
+        if (fresh) {
+          const uint32_t ch = chunks[ph == 0 ? outer : inner];
+          const int tile = ph == 0 ? inner : outer;
+          src = base + (ch & 1023u) * expert_bytes +
+                static_cast<long long>(tile) * steps * kStepBytes;
+          if (ph == 0) {
+            const int r = min((lane >> 2) & 3, static_cast<int>(ch >> 10 & 7u));
+            line = x_op +
+                   static_cast<long long>(row_token[static_cast<int>(ch >> 16) + r]) * a.hidden * 2 +
+                   (lane & 3) * 128;
           }
-          if (!few_wait(bar_e + 8 * slot, phase ^ 1u, abort_flag, status, kWhereRing,
-                        a.timeout_cycles)) {
-            ok = false;
-            break;
-          }
+          fresh = false;
+        }
+        if (!__all_sync(0xffffffffu, few_wait(bar_e + 8 * slot, phase ^ 1u, abort_flag, status,
+                                              kWhereRing, a.timeout_cycles))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
           const uint32_t bytes = min(4, steps - 4 * s) * kStepBytes;
           mbar_arrive_expect_tx(bar_w + 8 * slot, bytes);
           bulk_g2s(ring + slot * kWStage, src + static_cast<long long>(s) * kWStage, bytes,
                    bar_w + 8 * slot, policy);
-          slot_next(slot, phase, kWeightWarps, sm.slots);
-          s += kWeightWarps;
-          while (s >= S) {
-            s -= S;
-            fresh = true;
-            if (++inner == inner_n) {
-              inner = 0;
-              ++outer;
-            }
+        } else if (ph == 0 && lane >= 16 && s * (2 * kStageK) + (lane & 3) * 128 < a.hidden * 2) {
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(line + s * (2 * kStageK)));
+        }
+        slot_next(slot, phase, kWeightWarps, sm.slots);
+        s += kWeightWarps;
+        while (s >= S) {
+          s -= S;
+          fresh = true;
+          if (++inner == inner_n) {
+            inner = 0;
+            ++outer;
           }
         }
       }
-      if (!ok)  // copies in flight land before the CTA ends
-        for (int u = first; u < next; u += kWeightWarps) {
-          if (u < next - sm.slots) continue;
-          const long long t0 = clock64();
-          while (!mbar_try_wait(bar_w + 8 * (u % sm.slots), (u / sm.slots) & 1) &&
-                 clock64() - t0 < kFewDrainCycles) {
-          }
-        }
     }
+    if (!ok && lane == 0)  // copies in flight land before the CTA ends
+      for (int u = first; u < next; u += kWeightWarps) {
+        if (u < next - sm.slots) continue;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar_w + 8 * (u % sm.slots), (u / sm.slots) & 1) &&
+               clock64() - t0 < kFewDrainCycles) {
+        }
+      }
   } else if (warp < kComputeWarps) {
     // ---- compute: warpgroup `grp` takes the stages u % 4 == grp ----
     // After a wait gave up every warp still walks its stages (on whatever the
