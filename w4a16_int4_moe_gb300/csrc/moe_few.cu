@@ -123,12 +123,22 @@ constexpr int kItemSums = kGroups * kRowsPerPass * kSumPitch;
 inline int sum_floats(int tokens) { return std::max(2 * kItemSums, kGroups * tokens * kSumPitch); }
 
 // Shared memory of a call, all offsets in bytes.
+// Up to kLocalTokens tokens every CTA routes and converts all rows for itself,
+// into shared memory; more are shared out, one exchange between the CTAs later.
+constexpr int kLocalTokens = 2;
+constexpr size_t kLocalBytes = 32 << 10;
+inline bool few_local(int tokens, int hidden) {
+  return tokens <= kLocalTokens && operand(tokens, hidden, kHalfK).bytes <= kLocalBytes;
+}
+
 struct FewSmem {
   int slots, ring;
+  int local, rows;  // whether the rows lie here, and where
   int sums, ids, weights, mask, base, row_token, row_weight, chunks, total;
 };
-FewSmem few_smem(int tokens, int topk, int num_experts) {
+FewSmem few_smem(int tokens, int topk, int num_experts, int hidden) {
   FewSmem s;
+  s.local = few_local(tokens, hidden);
   const int rows = max_rows(tokens, topk);
   int at = 1024;  // barriers and scalars
   auto take = [&at](size_t bytes) {
@@ -144,6 +154,7 @@ FewSmem few_smem(int tokens, int topk, int num_experts) {
   s.row_token = take(4 * static_cast<size_t>(rows));
   s.row_weight = take(4 * static_cast<size_t>(rows));
   s.chunks = take(4 * static_cast<size_t>(rows));
+  s.rows = take(s.local ? operand(tokens, hidden, kHalfK).bytes : 0);
   s.ring = at;
   s.slots = std::min(kMaxSlots, (kFewMaxSmem - at) / kWStage);
   s.total = at + s.slots * kWStage;
@@ -318,6 +329,10 @@ __device__ __forceinline__ bool few_wait(uint32_t bar, uint32_t parity, volatile
   }
 }
 
+// Orders this thread's (and, behind a barrier, its CTA's) accesses before and
+// after it for the whole GPU.
+__device__ __forceinline__ void gpu_fence() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 // Until the counter that other CTAs raise has reached `want`; false if the
 // wait gave up.
 __device__ __forceinline__ bool wait_count(const int* counter, int want, volatile int* abort_flag,
@@ -354,9 +369,9 @@ __device__ __forceinline__ void epilogue_sync() {
 __device__ __forceinline__ bool epilogue_arrive(int* counter, int last, int* flag, int etid) {
   epilogue_sync();
   if (etid == 0) {
-    __threadfence();
+    gpu_fence();
     *flag = atomicAdd(counter, 1) == last;
-    __threadfence();
+    gpu_fence();
   }
   epilogue_sync();
   return *flag != 0;
@@ -409,6 +424,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   int* num_chunks_p = scalars + 2;
   int* warp_sums = scalars + 4;  // [16]
   uint32_t* block_top = reinterpret_cast<uint32_t*>(scalars + 20);  // [2][kRowsPerPass]
+  volatile int* act_ready = scalars + 3;
   float* sums = reinterpret_cast<float*>(smem + sm.sums);
   int* s_ids = reinterpret_cast<int*>(smem + sm.ids);
   float* s_weights = reinterpret_cast<float*>(smem + sm.weights);
@@ -424,9 +440,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   float* shares = reinterpret_cast<float*>(a.workspace + kStatusBytes + kCounterBytes);
   const size_t share = share_floats(a.tokens);
   // the two operands: the rows, and the activation's parts (row r, part p: row 2r + p)
-  uint8_t* x_op = reinterpret_cast<uint8_t*>(shares + 2 * kMaxCtas * share);
   const Operand xo = operand(a.tokens, a.hidden, kHalfK);
-  uint8_t* act_op = x_op + xo.bytes;
+  uint8_t* act_op = reinterpret_cast<uint8_t*>(shares + 2 * kMaxCtas * share) + xo.bytes;
+  uint8_t* x_op = sm.local ? smem + sm.rows : act_op - xo.bytes;
   const Operand ao = operand(static_cast<size_t>(rows_cap) * kActParts, a.inter, kKStep);
 
   // ---- setup: barriers, routing, the rows of every expert ----
@@ -442,17 +458,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     if (lane == 0) {
       mbar_init(bar_act, 1);
       *abort_flag = 0;
+      *act_ready = 0;
     }
     fence_mbar_init();
   }
   for (int e = tid; e < a.num_experts; e += kFewThreads) s_mask[e] = 0u;
-  if (warp >= kComputeWarps) {
-    // this CTA's share of the rows into FP16: sixteen lanes a block of 128
-    const int half = (tid - kComputeThreads) >> 4, l16 = lane & 15;
-    constexpr int kHalves = (kFewThreads - kComputeThreads) / 16;
+  grid_dependency_wait();  // what follows reads what earlier launches wrote
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // the rows into FP16, all of them or this CTA's share: sixteen lanes a block
+  // of 128
+  {
+    constexpr int kHalves = kFewThreads / 16;
+    const int half = tid >> 4, l16 = lane & 15;
     const int row_blocks = (a.hidden + kHalfK - 1) / kHalfK;  // of the input's scales too
     const int blocks = a.tokens * row_blocks;
-    for (int b0 = blockIdx.x * kHalves; b0 < blocks; b0 += gridDim.x * kHalves) {
+    for (int b0 = sm.local ? 0 : blockIdx.x * kHalves; b0 < blocks;
+         b0 += sm.local ? kHalves : gridDim.x * kHalves) {
       const int blk = min(b0 + half, blocks - 1);  // (the last ones may repeat a block)
       const int tok = blk / row_blocks, kb = blk - tok * row_blocks, k0 = kb * kHalfK + l16 * 8;
       const long long at = static_cast<long long>(tok) * a.hidden + k0;
@@ -504,29 +525,53 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         reinterpret_cast<float*>(x_op + xo.factors)[tok * xo.blocks + kb] = out_factor;
     }
   }
-  // ... and of the routing: one warp a token, so that a call of many tokens
-  // waits for one token's routing only
-  if (a.logits != nullptr && warp == 0)
-    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-      if (a.num_global <= 512)
-        route_token<16>(a.logits, a.bf16_logits, t, a.num_global, a.topk, a.renormalize,
-                        a.expert_offset, a.num_experts, a.topk_ids, a.topk_weights);
-      else
-        route_token<32>(a.logits, a.bf16_logits, t, a.num_global, a.topk, a.renormalize,
-                        a.expert_offset, a.num_experts, a.topk_ids, a.topk_weights);
+  // the routing: of all tokens, or one CTA a token, so that a call of many
+  // waits for one only
+  int32_t* ids = sm.local ? s_ids : a.topk_ids;
+  float* weights = sm.local ? s_weights : a.topk_weights;
+  if (a.logits != nullptr)
+    for (int t = sm.local ? 0 : blockIdx.x; t < a.tokens; t += sm.local ? 1 : gridDim.x)
+      route_token_cta<kFewThreads / 32>(a.logits, a.bf16_logits, t, a.num_global, a.topk,
+                                        a.renormalize, a.expert_offset, a.num_experts, ids,
+                                        weights, sums);
+  __syncthreads();
+  if (!sm.local) {
+    if (tid == 0) {
+      gpu_fence();
+      atomicAdd(&counters->rows_done, 1);
+      wait_count(&counters->rows_done, gridDim.x, abort_flag, status, kWhereRows,
+                 a.timeout_cycles);
     }
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    atomicAdd(&counters->rows_done, 1);
-    wait_count(&counters->rows_done, gridDim.x, abort_flag, status, kWhereRows, a.timeout_cycles);
+    __syncthreads();
   }
-  __syncthreads();
-  for (int i = tid; i < rows_cap; i += kFewThreads) {
-    s_ids[i] = __ldcg(a.topk_ids + i);
-    s_weights[i] = __ldcg(a.topk_weights + i);
+  if (!sm.local || a.logits == nullptr) {
+    for (int i = tid; i < rows_cap; i += kFewThreads) {
+      s_ids[i] = __ldcg(a.topk_ids + i);
+      s_weights[i] = __ldcg(a.topk_weights + i);
+    }
+    __syncthreads();
+  } else if (blockIdx.x == 0) {
+    for (int i = tid; i < rows_cap; i += kFewThreads) {
+      a.topk_ids[i] = s_ids[i];
+      a.topk_weights[i] = s_weights[i];
+    }
   }
-  __syncthreads();
+  if (a.tokens == 1) {
+    // one token: every local pick is a row and a pass of its own, in slot order
+    if (warp == 0) {
+      const int e = lane < a.topk ? s_ids[lane] : -1;
+      const bool local = e >= 0 && e < a.num_experts;
+      const uint32_t all = __ballot_sync(0xffffffffu, local);
+      const int row = __popc(all & ((1u << lane) - 1u));
+      if (local) {
+        row_token[row] = 0;
+        row_weight[row] = s_weights[lane];
+        chunks[row] = static_cast<uint32_t>(e) | static_cast<uint32_t>(row) << 16;
+      }
+      if (lane == 0) *num_chunks_p = __popc(all);
+    }
+    __syncthreads();
+  } else {
   // bit t of an expert's mask: token t goes there
   for (int i = tid; i < rows_cap; i += kFewThreads) {
     const int e = s_ids[i];
@@ -593,6 +638,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     row_weight[row] = w;
   }
   __syncthreads();
+  }
 
   const int num_chunks = *num_chunks_p;
   if (num_chunks == 0) {  // no row for this GPU's experts
@@ -602,7 +648,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
            i += static_cast<long long>(gridDim.x) * kFewThreads)
         a.out[i] = 0.f;
     if (tid == 0) {
-      __threadfence();
+      gpu_fence();
       if (atomicAdd(&counters->exits, 1) == static_cast<int>(gridDim.x) - 1) {
         counters->rows_done = 0;
         counters->exits = 0;
@@ -623,8 +669,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   const int gu_count = gu_end - gu_begin;
 
   if (warp >= kWarpWeights0 && warp < kWarpEpilogue0) {
-    // ---- weight copies, by lane 0; lanes 16 to 31 bring the lines of the rows
-    // that the stage will meet into L1 (four rows of four lines) ----
+    // ---- weight copies, by lane 0; the lanes bring the lines that the stage
+    // will meet into L1: four lines of four rows, or, once the activation is
+    // complete, of four rows' two parts ----
     const uint64_t policy = policy_evict_first();
     const int first = warp - kWarpWeights0;
     int slot = first;
@@ -652,12 +699,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
           const int tile = ph == 0 ? inner : outer;
           src = base + (ch & 1023u) * expert_bytes +
                 static_cast<long long>(tile) * steps * kStepBytes;
-          if (ph == 0) {
-            const int r = min((lane >> 2) & 3, static_cast<int>(ch >> 10 & 7u));
-            line = x_op +
-                   static_cast<long long>(row_token[static_cast<int>(ch >> 16) + r]) * a.hidden * 2 +
-                   (lane & 3) * 128;
-          }
+          const int last = static_cast<int>(ch >> 10 & 7u), row0 = static_cast<int>(ch >> 16);
+          line = ph == 0 ? x_op + static_cast<long long>(row_token[row0 + min(lane >> 2 & 3, last)]) *
+                                      a.hidden * 2
+                         : act_op + (static_cast<long long>(row0 + min(lane >> 3, last)) * kActParts +
+                                     (lane >> 2 & 1)) *
+                                        a.inter * 2;
+          line += (lane & 3) * 128;
           fresh = false;
         }
         if (!__all_sync(0xffffffffu, few_wait(bar_e + 8 * slot, phase ^ 1u, abort_flag, status,
@@ -670,9 +718,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
           mbar_arrive_expect_tx(bar_w + 8 * slot, bytes);
           bulk_g2s(ring + slot * kWStage, src + static_cast<long long>(s) * kWStage, bytes,
                    bar_w + 8 * slot, policy);
-        } else if (ph == 0 && lane >= 16 && s * (2 * kStageK) + (lane & 3) * 128 < a.hidden * 2) {
-          asm volatile("prefetch.global.L1 [%0];" ::"l"(line + s * (2 * kStageK)));
         }
+        if ((ph == 0 ? lane < 16 && !sm.local : *act_ready != 0) &&
+            s * (2 * kStageK) + (lane & 3) * 128 < 2 * (ph == 0 ? a.hidden : a.inter))
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(line + s * (2 * kStageK)));
         slot_next(slot, phase, kWeightWarps, sm.slots);
         s += kWeightWarps;
         while (s >= S) {
@@ -986,7 +1035,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
           put_act(c, gate, up);
           epilogue_sync();
           if (etid == 0) {
-            __threadfence();
+            gpu_fence();
             atomicAdd(&counters->act_done, 1);
           }
         }
@@ -998,8 +1047,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     // every gate_up item of every CTA is out: the activation is complete
     if (dn_end > dn_begin && etid == 0 &&
         wait_count(&counters->act_done, num_chunks * tiles0, abort_flag, status, kWhereAct,
-                   a.timeout_cycles))
+                   a.timeout_cycles)) {
+      *act_ready = 1;
       mbar_arrive(bar_act);
+    }
     __syncwarp();
     if (dn_end > dn_begin) {
       const int tile_stages = num_chunks * dn.stages;
@@ -1084,18 +1135,29 @@ bool few_supported(int tokens, int topk, int num_experts, int hidden, int inter)
       static_cast<long long>((hidden + kTileRows - 1) / kTileRows) *
           ((inter + kStageK - 1) / kStageK));
   if (rows * stages >= (1LL << 30)) return false;
-  return rows <= 1024 && few_smem(tokens, topk, num_experts).slots >= kMinSlots;
+  return rows <= 1024 && few_smem(tokens, topk, num_experts, hidden).slots >= kMinSlots;
 }
 
 cudaError_t launch_moe_few(const FewArgs& args, int sms, cudaStream_t stream) {
   FewParams p;
   p.a = args;
-  p.s = few_smem(args.tokens, args.topk, args.num_experts);
+  p.s = few_smem(args.tokens, args.topk, args.num_experts, args.hidden);
   const cudaError_t e = cudaFuncSetAttribute(
       w4a16_moe_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem);
   if (e != cudaSuccess) return e;
-  w4a16_moe_few_kernel<<<std::min(sms, kMaxCtas), kFewThreads, p.s.total, stream>>>(p);
-  return cudaGetLastError();
+  // a programmatic dependent of the launch before: it starts while that one
+  // ends, and waits for its end before it reads anything
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(sms, kMaxCtas)));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.s.total);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, w4a16_moe_few_kernel, p);
 }
 
 }  // namespace w4a16

@@ -107,4 +107,124 @@ __device__ __forceinline__ void route_token(const void* __restrict__ logits, int
   }
 }
 
+// The same by a whole CTA of kWarps warps (all threads take part), for one
+// token at a time: the shortest way through when there are few. Warp w takes
+// the experts of the rows 32 i .. 32 i + 31, i = w, w + kWarps, ..., and sorts
+// out its topk best; warp 0 merges the lists. Results, to the bit, as above
+// (the exponentials are added in the same order). scratch: 32 * 32 + 2 *
+// kWarps * 32 + kWarps words of shared memory; ids and weights may be shared
+// memory too.
+template <int kWarps>
+__device__ __forceinline__ void route_token_cta(const void* __restrict__ logits, int bf16_logits,
+                                                int t, int num_experts, int topk, int renormalize,
+                                                int expert_offset, int num_local, int32_t* ids,
+                                                float* weights, float* scratch) {
+  constexpr int kRows = (32 + kWarps - 1) / kWarps;
+  float* exps = scratch;  // [32][32]
+  uint32_t* list_key = reinterpret_cast<uint32_t*>(scratch + 32 * 32);  // [kWarps][32]
+  int* list_id = reinterpret_cast<int*>(list_key + kWarps * 32);
+  float* tops = reinterpret_cast<float*>(list_id + kWarps * 32);  // [kWarps]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = (num_experts + 31) / 32;
+  const long long row = static_cast<long long>(t) * num_experts;
+  float v[kRows];
+  uint32_t key[kRows];
+  float mx = -FLT_MAX;
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int e = min(32 * (warp + j * kWarps) + lane, num_experts - 1);
+    v[j] = bf16_logits ? __uint_as_float(static_cast<uint32_t>(
+                                             __ldg(static_cast<const uint16_t*>(logits) + row + e))
+                                         << 16)
+                       : __ldg(static_cast<const float*>(logits) + row + e);
+  }
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    if (32 * (warp + j * kWarps) + lane >= num_experts) v[j] = -FLT_MAX;
+    mx = fmaxf(mx, v[j]);
+    const uint32_t bits = __float_as_uint(v[j] + 0.f);
+    key[j] = v[j] > -FLT_MAX ? ((bits >> 31) != 0 ? ~bits : bits | 0x80000000u) : 0u;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) tops[warp] = mx;
+  // this warp's topk best, largest first, ties to the lower expert
+  uint32_t my_key = 0u;
+  int my_id = -1;
+#pragma unroll 1
+  for (int s = 0; s < topk; ++s) {
+    uint32_t best = 0u;
+    int best_j = 0;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        best_j = j;
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    if (top == 0u) break;
+    const int e = static_cast<int>(__reduce_min_sync(
+        0xffffffffu,
+        best == top ? static_cast<uint32_t>(32 * (warp + best_j * kWarps) + lane) : 0xffffffffu));
+    if ((e & 31) == lane && best == top)
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        if (j == best_j) key[j] = 0u;
+    if (lane == s) {
+      my_key = top;
+      my_id = e;
+    }
+  }
+  list_key[warp * 32 + lane] = my_key;
+  list_id[warp * 32 + lane] = my_id;
+  __syncthreads();
+  mx = -FLT_MAX;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, tops[w]);
+#pragma unroll
+  for (int j = 0; j < kRows; ++j)
+    if (warp + j * kWarps < rows)
+      exps[(warp + j * kWarps) * 32 + lane] =
+          32 * (warp + j * kWarps) + lane < num_experts ? expf(v[j] - mx) : 0.f;
+  __syncthreads();
+  if (warp == 0) {
+    float sum = 0.f;
+    for (int i = 0; i < rows; ++i) sum += exps[i * 32 + lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // lane w walks list w
+    int pos = 0;
+    uint32_t head = lane < kWarps ? list_key[lane * 32] : 0u;
+    int head_id = lane < kWarps ? list_id[lane * 32] : -1;
+    float my_v = 0.f;
+    my_id = -1;
+#pragma unroll 1
+    for (int s = 0; s < topk; ++s) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, head);
+      if (top == 0u) break;
+      const int e = static_cast<int>(__reduce_min_sync(
+          0xffffffffu, head == top ? static_cast<uint32_t>(head_id) : 0xffffffffu));
+      if (lane == s) {
+        my_v = __uint_as_float((top >> 31) != 0 ? top & 0x7FFFFFFFu : ~top);
+        my_id = e;
+      }
+      if (head == top && head_id == e) {
+        ++pos;
+        head = pos < topk ? list_key[lane * 32 + pos] : 0u;
+        head_id = pos < topk ? list_id[lane * 32 + pos] : -1;
+      }
+    }
+    const float my_p = my_id >= 0 ? expf(my_v - mx) / sum : 0.f;
+    float sel_sum = 0.f;
+    for (int s = 0; s < topk; ++s) sel_sum += __shfl_sync(0xffffffffu, my_p, s);
+    if (lane < topk) {
+      const int loc = my_id - expert_offset;
+      const long long at = static_cast<long long>(t) * topk + lane;
+      ids[at] = (my_id >= 0 && loc >= 0 && loc < num_local) ? loc : -1;
+      weights[at] = renormalize ? (sel_sum > 0.f ? my_p / sel_sum : 0.f) : my_p;
+    }
+  }
+  __syncthreads();  // scratch is free again
+}
+
 }  // namespace w4a16
