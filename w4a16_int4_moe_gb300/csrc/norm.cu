@@ -6,18 +6,24 @@
 //   scale = max(amax |y|, 1e-10) / 448 of a 128-column group or of the row
 //   (448 is the largest e4m3 value; the floor keeps the scale a normal number,
 //   so that an all-zero group divides to zero).
+//
+// Bound by memory for many rows, by latency for few. A row is read once into
+// registers (eight columns a thread and chunk: 16-byte loads), its sum of
+// squares joined over the threads of the row, and everything is written from
+// registers. A block of 16 lanes holds the 128 columns of a group of the 8-bit
+// form, so a group's largest value needs four shuffles and no shared memory.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace w4a16 {
 
 namespace {
 
-constexpr int kNormThreads = 256;
 constexpr float kAmaxFloor = 1e-10f;
 constexpr float kE4m3Max = 448.f;
 
@@ -28,67 +34,162 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// eight quotients by the scale, rounded to e4m3 (the division is exact, so
+// that a value on a border falls as its quotient does)
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float scale) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(y[4 * i], scale), __fdiv_rn(y[4 * i + 1], scale)), __NV_SATFINITE,
+        __NV_E4M3);
+    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(y[4 * i + 2], scale), __fdiv_rn(y[4 * i + 3], scale)),
+        __NV_SATFINITE, __NV_E4M3);
+    w[i] = static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Joins a value over the kThreads threads of a row (all of the CTA).
+template <int kThreads, typename Op>
+__device__ __forceinline__ float row_join(float v, float* part, Op op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if constexpr (kThreads > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) v = op(v, part[i]);
+  }
+  return v;
+}
+
 }  // namespace
 
-// One CTA per row; the row is read again for each step.
-__global__ void __launch_bounds__(kNormThreads) w4a16_add_rms_norm_kernel(const NormArgs a) {
-  __shared__ float part[kNormThreads / 32];
-  extern __shared__ float y_row[];
+// One row per CTA of kThreads threads; chunk c of thread t holds the columns
+// 8 (c * kThreads + t) .. + 7, kChunks chunks.
+template <int kThreads, int kChunks>
+__global__ void __launch_bounds__(kThreads) w4a16_add_rms_norm_kernel(const NormArgs a) {
+  __shared__ float part[2][kThreads / 32];
   const int row = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const __nv_bfloat16* x =
-      reinterpret_cast<const __nv_bfloat16*>(a.x) + static_cast<long long>(row) * a.x_stride;
-  const __nv_bfloat16* r =
-      a.residual == nullptr ? nullptr
-                            : reinterpret_cast<const __nv_bfloat16*>(a.residual) +
-                                  static_cast<long long>(row) * a.residual_stride;
-  const __nv_bfloat16* w = reinterpret_cast<const __nv_bfloat16*>(a.weight);
   const long long at = static_cast<long long>(row) * a.hidden;
-  float ss = 0.f;
-  for (int c = threadIdx.x; c < a.hidden; c += kNormThreads) {
-    float h = __bfloat162float(x[c]);
-    if (r != nullptr) {
-      h += __bfloat162float(r[c]);
-      reinterpret_cast<__nv_bfloat16*>(a.residual_out)[at + c] = __float2bfloat16_rn(h);
+  const uint16_t* x = a.x + static_cast<long long>(row) * a.x_stride;
+  float h[kChunks][8];
+  uint4 w[kChunks];
+  // the weight is the caller's own; the rows may come from the launch before
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int k = 8 * (c * kThreads + static_cast<int>(threadIdx.x));
+    w[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (k < a.hidden) w[c] = __ldg(reinterpret_cast<const uint4*>(a.weight + k));
+  }
+  uint4 in[kChunks], res[kChunks];
+  const uint16_t* r = a.residual == nullptr
+                          ? nullptr
+                          : a.residual + static_cast<long long>(row) * a.residual_stride;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int k = 8 * (c * kThreads + static_cast<int>(threadIdx.x));
+    in[c] = res[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (k < a.hidden) {
+      in[c] = *reinterpret_cast<const uint4*>(x + k);
+      if (r != nullptr) res[c] = *reinterpret_cast<const uint4*>(r + k);
     }
-    y_row[c] = h;
-    ss += h * h;
   }
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (lane == 0) part[warp] = ss;
-  __syncthreads();
-  ss = 0.f;
-  for (int i = 0; i < kNormThreads / 32; ++i) ss += part[i];
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    unpack8(in[c], h[c]);
+    if (r != nullptr) {
+      float f[8];
+      unpack8(res[c], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[c][i] += f[i];
+      const int k = 8 * (c * kThreads + static_cast<int>(threadIdx.x));
+      if (k < a.hidden) *reinterpret_cast<uint4*>(a.residual_out + at + k) = pack8(h[c]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(h[c][i], h[c][i], ss);
+  }
+  ss = row_join<kThreads>(ss, part[0], [](float p, float q) { return p + q; });
   const float inv = rsqrtf(ss / static_cast<float>(a.hidden) + a.eps);
-  for (int c = threadIdx.x; c < a.hidden; c += kNormThreads) {
-    const float y = y_row[c] * inv * __bfloat162float(w[c]);
-    y_row[c] = y;
-    if (a.out != nullptr) reinterpret_cast<__nv_bfloat16*>(a.out)[at + c] = __float2bfloat16_rn(y);
+  float amax = kAmaxFloor;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int k = 8 * (c * kThreads + static_cast<int>(threadIdx.x));
+    float f[8];
+    unpack8(w[c], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[c][i] = h[c][i] * inv * f[i];
+    if (a.out != nullptr && k < a.hidden) *reinterpret_cast<uint4*>(a.out + at + k) = pack8(h[c]);
+    if (a.fp8_group == W4A16_FP8_NONE) continue;
+    // (columns past the row are 0, or NaN in a row that has a NaN norm)
+    float top = kAmaxFloor;
+    if (k < a.hidden) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(h[c][i]));
+    }
+    if (a.fp8_group == W4A16_FP8_ROW) {
+      amax = max_nan(amax, top);
+      continue;
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float scale = __fdiv_rn(top, kE4m3Max);
+    if (k < a.hidden) {
+      *reinterpret_cast<uint2*>(a.out_fp8 + at + k) = codes8(h[c], scale);
+      if ((threadIdx.x & 15) == 0)
+        a.scales[static_cast<long long>(row) * ((a.hidden + 127) / 128) + k / 128] = scale;
+    }
   }
-  if (a.fp8_group == W4A16_FP8_NONE) return;
-  __syncthreads();
-  const int group = a.fp8_group == W4A16_FP8_ROW ? a.hidden : a.fp8_group;
-  const int groups = (a.hidden + group - 1) / group;
-  for (int g = warp; g < groups; g += kNormThreads / 32) {
-    const int end = min(a.hidden, (g + 1) * group);
-    float amax = kAmaxFloor;
-    for (int c = g * group + lane; c < end; c += 32) amax = max_nan(amax, fabsf(y_row[c]));
-    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float scale = amax / kE4m3Max;
-    if (lane == 0) a.scales[static_cast<long long>(row) * groups + g] = scale;
-    for (int c = g * group + lane; c < end; c += 32)
-      a.out_fp8[at + c] = __nv_cvt_float_to_fp8(y_row[c] / scale, __NV_SATFINITE, __NV_E4M3);
+  if (a.fp8_group != W4A16_FP8_ROW) return;
+  amax = row_join<kThreads>(amax, part[1], [](float p, float q) { return max_nan(p, q); });
+  const float scale = __fdiv_rn(amax, kE4m3Max);
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int k = 8 * (c * kThreads + static_cast<int>(threadIdx.x));
+    if (k < a.hidden) *reinterpret_cast<uint2*>(a.out_fp8 + at + k) = codes8(h[c], scale);
   }
+  if (threadIdx.x == 0) a.scales[row] = scale;
 }
 
 cudaError_t launch_add_rms_norm(const NormArgs& args, int sms, cudaStream_t stream) {
   (void)sms;
-  const size_t smem = static_cast<size_t>(args.hidden) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(w4a16_add_rms_norm_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kNormMaxHidden * static_cast<int>(sizeof(float)));
-  if (e != cudaSuccess) return e;
-  w4a16_add_rms_norm_kernel<<<args.rows, kNormThreads, smem, stream>>>(args);
+  const int rows = args.rows;
+  const int need = (args.hidden + 7) / 8;  // threads of one chunk
+  if (need <= 32)
+    w4a16_add_rms_norm_kernel<32, 1><<<rows, 32, 0, stream>>>(args);
+  else if (need <= 128)
+    w4a16_add_rms_norm_kernel<128, 1><<<rows, 128, 0, stream>>>(args);
+  else if (need <= 256)
+    w4a16_add_rms_norm_kernel<256, 1><<<rows, 256, 0, stream>>>(args);
+  else if (need <= 512)
+    w4a16_add_rms_norm_kernel<256, 2><<<rows, 256, 0, stream>>>(args);
+  else if (need <= 1024)
+    w4a16_add_rms_norm_kernel<256, 4><<<rows, 256, 0, stream>>>(args);
+  else
+    w4a16_add_rms_norm_kernel<512, 4><<<rows, 512, 0, stream>>>(args);
   return cudaGetLastError();
 }
 
