@@ -398,14 +398,14 @@ def w4a16_silu_and_mul(x: torch.Tensor, out: Optional[torch.Tensor] = None, stre
 # pass plain integers: no ctypes object is built per pointer, and the current
 # stream is read without making a Stream object.
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
 def _raw_stream(device, stream):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index or 0)
+    return _current_stream(device.index)
+
+
+def _current_stream(index):
+    return torch._C._cuda_getCurrentRawStream(0 if index is None else index)
 
 
 def _refuse(fn: str, why: str):
@@ -413,19 +413,23 @@ def _refuse(fn: str, why: str):
 
 
 def _need(fn: str, what: str, t: torch.Tensor, dtype, shape):
-    """t is a contiguous tensor of this type and shape, else W4A16_ERR_INVALID_ARG."""
-    if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
-            or not t.is_cuda):
+    """The address of t, a contiguous GPU tensor of this type and shape (else
+    W4A16_ERR_INVALID_ARG)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, "
                     f"not contiguous {dtype} {tuple(shape)} on a GPU")
+    return t.data_ptr()
 
 
 def _rows(fn: str, what: str, t: torch.Tensor):
-    """t is BF16 [rows, columns] with adjacent columns; returns its row stride."""
-    if (t.dtype != torch.bfloat16 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)
-            or not t.is_cuda):
-        _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} of strides {t.stride()} on {t.device}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    """t is BF16 [rows, columns] on a GPU with adjacent columns; returns
+    (address, rows, columns, row stride)."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
+        _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}")
+    (rows, columns), (pitch, step) = t.shape, t.stride()
+    if step != 1 and columns > 1:
+        _refuse(fn, f"{what}: strides {t.stride()}")
+    return t.data_ptr(), rows, columns, pitch if rows > 1 else max(pitch, columns)
 
 
 def w4a16_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -440,37 +444,32 @@ def w4a16_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     written, and the third entry may be the residual itself). x and residual
     BF16 [T, H], rows may be strided."""
     fn = "w4a16_add_rms_norm"
-    x_stride = _rows(fn, "x", x)
-    rows, hidden = x.shape
-    r_stride = 0
-    _need(fn, "weight", weight, torch.bfloat16, (hidden,))
+    x_at, rows, hidden, x_stride = _rows(fn, "x", x)
+    w_at = _need(fn, "weight", weight, torch.bfloat16, (hidden,))
+    r_at, r_stride = None, 0
     if residual is not None:
-        r_stride = _rows(fn, "residual", residual)
-        if residual.shape != x.shape:
+        r_at, r_rows, r_cols, r_stride = _rows(fn, "residual", residual)
+        if r_rows != rows or r_cols != hidden:
             _refuse(fn, f"residual {tuple(residual.shape)} for x {tuple(x.shape)}")
     if fp8_group not in (W4A16_FP8_NONE, W4A16_FP8_ROW, W4A16_FP8_GROUP):
         raise W4A16Error(fn, W4A16_ERR_UNSUPPORTED, f"fp8_group {fp8_group}")
-    groups = 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP)
+    shape = (rows, hidden)
+    groups = (rows, 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP))
     if out is None:
-        def new(dtype, *shape):
-            return torch.empty(shape, dtype=dtype, device=x.device)
-        out = (new(torch.bfloat16, rows, hidden) if bf16_out else None,
-               new(torch.bfloat16, rows, hidden) if residual is not None else None,
-               new(torch.float8_e4m3fn, rows, hidden) if fp8_group else None,
-               new(torch.float32, rows, groups) if fp8_group else None)
-    else:
-        for what, t, dtype, shape in (
-                ("out", out[0], torch.bfloat16, (rows, hidden)),
-                ("residual_out", out[1], torch.bfloat16, (rows, hidden)),
-                ("out_fp8", out[2], torch.float8_e4m3fn, (rows, hidden)),
-                ("scales", out[3], torch.float32, (rows, groups))):
-            if t is not None:
-                _need(fn, what, t, dtype, shape)
+        out = (torch.empty(shape, dtype=torch.bfloat16, device=x.device) if bf16_out else None,
+               torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+               if residual is not None else None,
+               torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+               if fp8_group else None,
+               torch.empty(groups, dtype=torch.float32, device=x.device) if fp8_group else None)
     y, res_out, y8, scales = out
     _check(fn, load_library().w4a16_add_rms_norm(
-        x.data_ptr(), x_stride, _addr(residual), r_stride, weight.data_ptr(), eps, rows, hidden,
-        _addr(y), _addr(res_out), _addr(y8), _addr(scales), fp8_group,
-        _raw_stream(x.device, stream)))
+        x_at, x_stride, r_at, r_stride, w_at, eps, rows, hidden,
+        None if y is None else _need(fn, "out", y, torch.bfloat16, shape),
+        None if res_out is None else _need(fn, "residual_out", res_out, torch.bfloat16, shape),
+        None if y8 is None else _need(fn, "out_fp8", y8, torch.float8_e4m3fn, shape),
+        None if scales is None else _need(fn, "scales", scales, torch.float32, groups),
+        fp8_group, _raw_stream(x.device, stream)))
     return out
 
 
@@ -478,17 +477,14 @@ def w4a16_router_logits(x: torch.Tensor, weight: torch.Tensor,
                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """x BF16 [T, H] (rows may be strided), weight BF16 [E, H] -> FP32 [T, E]."""
     fn = "w4a16_router_logits"
-    x_stride = _rows(fn, "x", x)
-    tokens, hidden = x.shape
+    x_at, tokens, hidden, x_stride = _rows(fn, "x", x)
     experts = weight.shape[0]
-    _need(fn, "weight", weight, torch.bfloat16, (experts, hidden))
+    w_at = _need(fn, "weight", weight, torch.bfloat16, (experts, hidden))
     if out is None:
         out = torch.empty((tokens, experts), dtype=torch.float32, device=x.device)
-    else:
-        _need(fn, "out", out, torch.float32, (tokens, experts))
     _check(fn, load_library().w4a16_router_logits(
-        x.data_ptr(), x_stride, weight.data_ptr(), tokens, hidden, experts, out.data_ptr(),
-        _raw_stream(x.device, stream)))
+        x_at, x_stride, w_at, tokens, hidden, experts,
+        _need(fn, "out", out, torch.float32, (tokens, experts)), _raw_stream(x.device, stream)))
     return out
 
 
@@ -508,32 +504,32 @@ def w4a16_moe_few_tokens(packed_gate_up: torch.Tensor, packed_down: torch.Tensor
     logits, topk_ids and topk_weights [T, topk] are the routing; with logits
     (FP32 or BF16 [T, E_global]) they receive it."""
     fn = "w4a16_moe_few_tokens"
-    tokens, topk = topk_ids.shape
+    tokens, topk = picks = topk_ids.shape
     fp8 = x_scales is not None
-    _need(fn, "x", x, torch.float8_e4m3fn if fp8 else torch.bfloat16, (tokens, hidden))
-    _need(fn, "topk_ids", topk_ids, torch.int32, (tokens, topk))
-    _need(fn, "topk_weights", topk_weights, torch.float32, (tokens, topk))
+    x_at = _need(fn, "x", x, torch.float8_e4m3fn if fp8 else torch.bfloat16, (tokens, hidden))
+    s_at = None
     if fp8:
-        _need(fn, "x_scales", x_scales, torch.float32,
-              (tokens, -(-hidden // W4A16_FP8_GROUP)))
-    lg_type, experts = W4A16_DTYPE_F32, 0
+        s_at = _need(fn, "x_scales", x_scales, torch.float32,
+                     (tokens, -(-hidden // W4A16_FP8_GROUP)))
+    lg_at, lg_type, experts = None, W4A16_DTYPE_F32, 0
     if logits is not None:
-        if logits.dtype == torch.bfloat16:
+        dtype = logits.dtype
+        if dtype is torch.bfloat16:
             lg_type = W4A16_DTYPE_BF16
+        else:
+            dtype = torch.float32
         experts = logits.shape[1]
-        _need(fn, "logits", logits,
-              torch.bfloat16 if lg_type == W4A16_DTYPE_BF16 else torch.float32,
-              (tokens, experts))
+        lg_at = _need(fn, "logits", logits, dtype, (tokens, experts))
     if out is None:
         out = torch.empty((tokens, hidden), dtype=torch.float32, device=x.device)
-    else:
-        _need(fn, "out", out, torch.float32, (tokens, hidden))
     _check(fn, load_library().w4a16_moe_few_tokens(
-        packed_gate_up.data_ptr(), packed_down.data_ptr(), num_experts, hidden, inter,
-        x.data_ptr(), W4A16_DTYPE_FP8 if fp8 else W4A16_DTYPE_BF16, _addr(x_scales), tokens, topk,
-        _addr(logits), lg_type, experts, 1 if renormalize else 0, expert_offset,
-        topk_ids.data_ptr(), topk_weights.data_ptr(), out.data_ptr(), flags,
-        workspace.data_ptr(), workspace.numel(), _raw_stream(x.device, stream)))
+        packed_gate_up.data_ptr(), packed_down.data_ptr(), num_experts, hidden, inter, x_at,
+        W4A16_DTYPE_FP8 if fp8 else W4A16_DTYPE_BF16, s_at, tokens, topk, lg_at, lg_type, experts,
+        1 if renormalize else 0, expert_offset,
+        _need(fn, "topk_ids", topk_ids, torch.int32, picks),
+        _need(fn, "topk_weights", topk_weights, torch.float32, picks),
+        _need(fn, "out", out, torch.float32, (tokens, hidden)), flags, workspace.data_ptr(),
+        workspace.numel(), _raw_stream(x.device, stream)))
     return out
 
 
