@@ -154,6 +154,9 @@ bool tmem_accumulators(int block_m, int k_steps, int* d_cols, int* parts, int* d
 bool early_epilogue(int block_m, int out_mode, bool pair);
 // 2-D map of BF16 [rows, k] (box 64 x box_rows, 128-byte swizzle).
 bool encode_act_tmap(CUtensorMap* map, const void* act, long long rows, int k, int box_rows);
+// The same with rows `stride` elements apart (a multiple of 8).
+bool encode_rows_tmap(CUtensorMap* map, const void* rows_at, long long rows, int k,
+                      long long stride, int box_rows);
 // 3-D map of the permuted rows [rows, k_pad]: dims (64 columns, rows, k_pad /
 // 64 chunks), box 64 x box_rows x box_steps (1 or 2 k steps), 128-byte swizzle.
 bool encode_permuted_tmap(CUtensorMap* map, const void* act, long long rows, int k_pad,
@@ -200,6 +203,28 @@ cudaError_t launch_topk_softmax(const void* logits, int bf16_logits, int tokens,
                                 int topk, int renormalize, int expert_offset, int num_local,
                                 int32_t* topk_ids, float* topk_weights, int sms,
                                 cudaStream_t stream);
+
+// A launch as a programmatic dependent of the launch before: its CTAs may start
+// while that one ends, so the kernel calls grid_dependency_wait() before it
+// reads anything. cluster: CTAs of a cluster (1: none).
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, size_t smem,
+                             int cluster, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 
 // The residual's addition and the RMS norm (norm.cu).
 struct NormArgs {

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   }
   for (int e = tid; e < a.num_experts; e += kFewThreads) s_mask[e] = 0u;
   grid_dependency_wait();  // what follows reads what earlier launches wrote
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dependents_go();
   // the rows into FP16, all of them or this CTA's share: sixteen lanes a block
   // of 128
   {
@@ -1145,19 +1145,8 @@ cudaError_t launch_moe_few(const FewArgs& args, int sms, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(
       w4a16_moe_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem);
   if (e != cudaSuccess) return e;
-  // a programmatic dependent of the launch before: it starts while that one
-  // ends, and waits for its end before it reads anything
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(sms, kMaxCtas)));
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.s.total);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w4a16_moe_few_kernel, p);
+  return launch_dependent(w4a16_moe_few_kernel, std::min(sms, kMaxCtas), kFewThreads,
+                          static_cast<size_t>(p.s.total), 1, stream, p);
 }
 
 }  // namespace w4a16

@@ -1617,6 +1617,11 @@ bool tmem_accumulators(int block_m, int k_steps, int* d_cols, int* parts, int* d
 }
 
 bool encode_act_tmap(CUtensorMap* map, const void* act, long long rows, int k, int box_rows) {
+  return encode_rows_tmap(map, act, rows, k, k, box_rows);
+}
+
+bool encode_rows_tmap(CUtensorMap* map, const void* act, long long rows, int k, long long stride,
+                      int box_rows) {
   using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
   static EncodeFn encode = nullptr;
   static std::once_flag once;
@@ -1630,7 +1635,7 @@ bool encode_act_tmap(CUtensorMap* map, const void* act, long long rows, int k, i
   });
   if (encode == nullptr || rows <= 0 || rows > (1LL << 31) || k <= 0) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k) * 2};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(kKStep), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(act), dims, strides,

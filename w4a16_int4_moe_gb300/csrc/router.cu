@@ -1,42 +1,323 @@
 // router.cu -- the router's product: logits = x . weight^T, BF16 operands,
 // FP32 sums.
+//
+// Two kernels, by the number of tokens:
+//
+//   * up to kFewTokens: the weight (5.5 MB for 384 experts of hidden 7168) is
+//     read once and every token with it. A cluster of eight CTAs shares
+//     sixteen experts, each CTA an eighth of the columns, so that all SMs read
+//     a part of the weight at once; m16n8k16 MMAs straight from global memory
+//     (no operand is used twice by an SM), partial sums joined through the
+//     cluster's shared memory;
+//   * more: a dense product on tcgen05, 128 tokens x up to 256 experts a tile,
+//     both operands by TMA, accumulators in TMEM. Where the tiles are fewer
+//     than the SMs, a cluster of up to eight CTAs splits the columns of one.
+//
+// The order of the additions follows from the sizes alone.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace w4a16 {
 
-// One warp per (token, expert).
-__global__ void __launch_bounds__(256)
-    w4a16_router_logits_kernel(const uint16_t* __restrict__ x, long long x_stride,
-                               const uint16_t* __restrict__ weight, int tokens, int hidden,
-                               int num_experts, float* __restrict__ logits) {
-  const int lane = threadIdx.x & 31;
-  const long long total = static_cast<long long>(tokens) * num_experts;
-  const long long warps = static_cast<long long>(gridDim.x) * 8;
-  for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < total;
-       i += warps) {
-    const long long t = i / num_experts, e = i % num_experts;
-    const __nv_bfloat16* xr = reinterpret_cast<const __nv_bfloat16*>(x) + t * x_stride;
-    const __nv_bfloat16* wr = reinterpret_cast<const __nv_bfloat16*>(weight) + e * hidden;
-    float acc = 0.f;
-    for (int c = lane; c < hidden; c += 32)
-      acc = fmaf(__bfloat162float(xr[c]), __bfloat162float(wr[c]), acc);
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) logits[i] = acc;
+namespace {
+
+// ----------------------------------------------------------- few tokens ---
+
+constexpr int kFewTokens = 64;
+constexpr int kFewCluster = 8;
+constexpr int kFewWarps = 8;
+constexpr int kFewExperts = 16;  // of a cluster (MMA M)
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+}  // namespace
+
+// kNt tiles of eight tokens. Columns go in blocks of 32: thread t of a quad
+// takes columns 8t .. 8t + 7 of a block, of both operands alike, so one 16-byte
+// load a row feeds two MMAs whatever order the MMA gives its k.
+template <int kNt>
+__global__ void __launch_bounds__(kFewWarps * 32)
+    w4a16_router_few_kernel(const uint16_t* __restrict__ x, long long x_stride,
+                            const uint16_t* __restrict__ weight, int tokens, int hidden,
+                            int num_experts, float* __restrict__ logits) {
+  __shared__ float part[kFewWarps][kFewExperts * 8 * kNt];
+  __shared__ float sums[kFewExperts * 8 * kNt];  // [token][expert]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int e0 = static_cast<int>(blockIdx.x) / kFewCluster * kFewExperts;
+  grid_dependency_wait();
+  grid_dependents_go();
+  const int blocks = (hidden + 31) / 32;
+  const int first = blocks * rank / kFewCluster, last = blocks * (rank + 1) / kFewCluster;
+  const uint16_t* a0 = weight + static_cast<long long>(min(e0 + g, num_experts - 1)) * hidden;
+  const uint16_t* a1 = weight + static_cast<long long>(min(e0 + g + 8, num_experts - 1)) * hidden;
+  const uint16_t* b[kNt];
+#pragma unroll
+  for (int n = 0; n < kNt; ++n) b[n] = x + min(8 * n + g, tokens - 1) * x_stride;
+  float acc[kNt][4] = {};
+  constexpr int kUnroll = kNt <= 2 ? 4 : 2;  // blocks in flight
+  for (int blk = first + warp; blk < last; blk += kFewWarps * kUnroll) {
+    uint4 va[kUnroll][2], vb[kUnroll][kNt];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int k = (blk + u * kFewWarps) * 32 + t * 8;
+      const bool in = blk + u * kFewWarps < last && k < hidden;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      va[u][0] = in ? __ldg(reinterpret_cast<const uint4*>(a0 + k)) : zero;
+      va[u][1] = in ? __ldg(reinterpret_cast<const uint4*>(a1 + k)) : zero;
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+        vb[u][n] = in ? __ldg(reinterpret_cast<const uint4*>(b[n] + k)) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (int n = 0; n < kNt; ++n) {
+        mma_bf16(acc[n], va[u][0].x, va[u][1].x, va[u][0].y, va[u][1].y, vb[u][n].x, vb[u][n].y);
+        mma_bf16(acc[n], va[u][0].z, va[u][1].z, va[u][0].w, va[u][1].w, vb[u][n].z, vb[u][n].w);
+      }
   }
+#pragma unroll
+  for (int n = 0; n < kNt; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      part[warp][(8 * n + 2 * t + (i & 1)) * kFewExperts + g + (i >> 1) * 8] = acc[n][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kFewExperts * 8 * kNt; i += kFewWarps * 32) {
+    float v = part[0][i];
+#pragma unroll
+    for (int w = 1; w < kFewWarps; ++w) v += part[w][i];
+    sums[i] = v;
+  }
+  cluster_sync_all();
+  // every CTA of the cluster writes an eighth of the outputs
+  for (int i = rank * kFewWarps * 32 + static_cast<int>(threadIdx.x); i < kFewExperts * tokens;
+       i += kFewCluster * kFewWarps * 32) {
+    const int tok = i / kFewExperts, e = e0 + i % kFewExperts;
+    const uint32_t at = smem_u32(sums + i);
+    float v = 0.f;
+#pragma unroll
+    for (int c = 0; c < kFewCluster; ++c)
+      v += ld_cluster_f32(map_to_cta(at, static_cast<uint32_t>(c)));
+    if (e < num_experts) logits[static_cast<long long>(tok) * num_experts + e] = v;
+  }
+  cluster_sync_all();  // the sums stay until all have read them
+}
+
+namespace {
+
+// ---------------------------------------------------------- many tokens ---
+
+constexpr int kTileM = 128;        // tokens of a tile (MMA M)
+constexpr int kMaxTileN = 256;     // experts of a tile (MMA N)
+constexpr int kMaxSplit = 8;
+constexpr int kMaxRing = 8;
+constexpr int kRingBytes = 200 << 10;  // 4 slots of k = 64 at N = 256, 5 at 192
+constexpr int kDenseThreads = 192;  // four epilogue warps, a copy warp, an MMA warp
+constexpr int kSumRow = kTileM + 1; // sums [expert][token], rows on different banks
+constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
+
+struct DenseArgs {
+  CUtensorMap x, weight;
+  float* logits;
+  int tokens, num_experts, k_steps;
+  int tile_n, n_tiles, split, slots, tmem_cols;
+};
+
+int dense_slots(int tile_n) {
+  return std::min(kMaxRing, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
+}
+// the ring, whose memory the sums take over; the swizzle needs 1024 bytes
+size_t dense_smem(int tile_n) {
+  const size_t ring = static_cast<size_t>(dense_slots(tile_n)) * (kTileM + tile_n) * kKStep * 2;
+  const size_t sums = static_cast<size_t>(tile_n) * kSumRow * 4;
+  return 2048 + std::max(ring, sums);
+}
+
+__device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*failed) return false;
+    if (clock64() - t0 > kGiveUpCycles) {
+      *failed = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+}  // namespace
+
+// A wait that gives up (none does unless the hardware fails) ends the CTA's
+// work in order and leaves NaN in its logits.
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    w4a16_router_dense_kernel(const __grid_constant__ DenseArgs a) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t bars[2 * kMaxRing + 1];
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed_word;
+  volatile int* failed = &failed_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxRing, done = full + 16 * kMaxRing;
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.tile_n) * kKStep * 2;
+  const uint32_t slot_bytes = a_bytes + b_bytes;
+  const int rank = static_cast<int>(blockIdx.x) % a.split;
+  const int tile = static_cast<int>(blockIdx.x) / a.split;
+  const int m0 = tile / a.n_tiles * kTileM, n0 = tile % a.n_tiles * a.tile_n;
+  const int k0 = a.k_steps * rank / a.split, k1 = a.k_steps * (rank + 1) / a.split;
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&tmem_at), static_cast<uint32_t>(a.tmem_cols));
+    tmem_relinquish();
+    if (lane == 0) {
+      for (int i = 0; i < a.slots; ++i) {
+        mbar_init(full + 8 * i, 1);
+        mbar_init(empty + 8 * i, 1);
+      }
+      mbar_init(done, 1);
+      *failed = 0;
+      fence_mbar_init();
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_dependents_go();
+  const uint32_t tmem = tmem_at;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      bool ok = true;
+      int issued = 0;
+      for (int k = k0; k < k1 && ok; ++k, ++issued) {
+        const int slot = issued % a.slots;
+        ok = dense_wait(empty + 8 * slot, (issued / a.slots & 1) ^ 1, failed);
+        if (!ok) break;
+        mbar_arrive_expect_tx(full + 8 * slot, slot_bytes);
+        tma_load_2d(ring + slot * slot_bytes, &a.x, k * kKStep, m0, full + 8 * slot);
+        tma_load_2d(ring + slot * slot_bytes + a_bytes, &a.weight, k * kKStep, n0,
+                    full + 8 * slot);
+      }
+      if (!ok)  // copies in flight land before the CTA ends
+        for (int i = max(0, issued - a.slots); i < issued; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(full + 8 * (i % a.slots), i / a.slots & 1) &&
+                 clock64() - t0 < kGiveUpCycles) {
+          }
+        }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_m128(static_cast<uint32_t>(a.tile_n));
+      for (int k = k0; k < k1; ++k) {
+        const int i = k - k0, slot = i % a.slots;
+        if (!dense_wait(full + 8 * slot, i / a.slots & 1, failed)) break;
+        tc_fence_after();
+        const uint64_t ad = smem_desc_sw128_kmajor(ring + slot * slot_bytes);
+        const uint64_t bd = smem_desc_sw128_kmajor(ring + slot * slot_bytes + a_bytes);
+#pragma unroll
+        for (int j = 0; j < kKStep / 16; ++j)  // 32 bytes further along k
+          mma_bf16_ss(tmem, ad + 2 * j, bd + 2 * j, idesc, i > 0 || j > 0);
+        tc_commit(empty + 8 * slot);
+      }
+      tc_commit(done);
+    }
+  } else {
+    // lane + 32 warp = token of the tile; the sums take the ring's place
+    bool ok = dense_wait(done, 0, failed);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    float* sums = reinterpret_cast<float*>(smem);
+    const int m = warp * 32 + lane;
+    for (int c = 0; c < a.tile_n; c += 16) {
+      uint32_t v[16];
+      tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        sums[(c + i) * kSumRow + m] = ok ? __uint_as_float(v[i]) : __uint_as_float(0x7FC00000u);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, static_cast<uint32_t>(a.tmem_cols));
+  }
+  if (a.split > 1) cluster_sync_all();
+  // this CTA's share of the tile's tokens, the split's sums in the CTAs' order
+  const int rows = kTileM / a.split;
+  for (int i = threadIdx.x; i < rows * a.tile_n; i += kDenseThreads) {
+    const int m = rank * rows + i / a.tile_n, n = i % a.tile_n;
+    const uint32_t at = ring + static_cast<uint32_t>(n * kSumRow + m) * 4;
+    float v = 0.f;
+    if (a.split == 1)
+      v = *reinterpret_cast<const float*>(smem + (at - ring));
+    else
+      for (int c = 0; c < a.split; ++c)
+        v += ld_cluster_f32(map_to_cta(at, static_cast<uint32_t>(c)));
+    if (m0 + m < a.tokens && n0 + n < a.num_experts)
+      a.logits[static_cast<long long>(m0 + m) * a.num_experts + n0 + n] = v;
+  }
+  if (a.split > 1) cluster_sync_all();
 }
 
 cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
                                  int tokens, int hidden, int num_experts, float* logits, int sms,
                                  cudaStream_t stream) {
-  const long long want = (static_cast<long long>(tokens) * num_experts + 7) / 8;
-  const long long cap = static_cast<long long>(sms) * 8;
-  w4a16_router_logits_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0, stream>>>(
-      x, x_stride, weight, tokens, hidden, num_experts, logits);
-  return cudaGetLastError();
+  if (tokens <= kFewTokens) {
+    const int grid = (num_experts + kFewExperts - 1) / kFewExperts * kFewCluster;
+    const auto run = [&](auto kernel) {
+      return launch_dependent(kernel, grid, kFewWarps * 32, 0, kFewCluster, stream, x, x_stride,
+                              weight, tokens, hidden, num_experts, logits);
+    };
+    if (tokens <= 8) return run(w4a16_router_few_kernel<1>);
+    if (tokens <= 16) return run(w4a16_router_few_kernel<2>);
+    if (tokens <= 32) return run(w4a16_router_few_kernel<4>);
+    return run(w4a16_router_few_kernel<8>);
+  }
+  DenseArgs a;
+  a.logits = logits;
+  a.tokens = tokens;
+  a.num_experts = num_experts;
+  a.k_steps = packed_ksteps(hidden);
+  a.n_tiles = ceil_div(num_experts, kMaxTileN);
+  a.tile_n = std::max(16, ceil_div(ceil_div(num_experts, a.n_tiles), 16) * 16);
+  a.slots = dense_slots(a.tile_n);
+  a.tmem_cols = 32;
+  while (a.tmem_cols < a.tile_n) a.tmem_cols *= 2;
+  const long long tiles = static_cast<long long>(ceil_div(tokens, kTileM)) * a.n_tiles;
+  // as many CTAs as fit, with at least four k steps each
+  a.split = 1;
+  while (a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.k_steps / (a.split * 2) >= 4)
+    a.split *= 2;
+  if (!encode_rows_tmap(&a.x, x, tokens, hidden, x_stride, kTileM) ||
+      !encode_rows_tmap(&a.weight, weight, num_experts, hidden, hidden, a.tile_n))
+    return cudaErrorInvalidValue;
+  if (tiles * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const size_t smem = dense_smem(a.tile_n);
+  const cudaError_t e = cudaFuncSetAttribute(
+      w4a16_router_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 2048);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(w4a16_router_dense_kernel, static_cast<int>(tiles * a.split),
+                          kDenseThreads, smem, a.split, stream, a);
 }
 
 }  // namespace w4a16
