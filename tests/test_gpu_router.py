@@ -37,7 +37,7 @@ def test_router(cuda_dev, tokens, hidden, experts, pitch):
 @pytest.mark.parametrize("tokens,hidden,experts", [
     (1, 8, 1), (3, 8, 1), (130, 8, 2), (5, 24, 3), (140, 40, 1), (33, 72, 17), (129, 200, 257),
     (257, 136, 1024), (2, 1000, 1024), (1, 14336, 129), (300, 14336, 100), (1025, 320, 383),
-    (2049, 64, 16), (4100, 1024, 256),
+    (2049, 64, 16), (4100, 1024, 256), (8192, 7168, 384),
 ])
 def test_router_odd_sizes(cuda_dev, tokens, hidden, experts):
     x, w = _inputs(tokens, hidden, experts, cuda_dev, seed=hidden)

@@ -79,7 +79,8 @@ constexpr float kPartScale = 2048.f;         // the second part is the rest time
 constexpr float kCodeScale = 16777216.f;     // a code is q * 2^-24
 constexpr int kSumPitch = 132;               // FP32 sums [row][128 + 4]
 constexpr int kMaxCtas = 192;
-constexpr int kMinSlots = 4;
+static_assert(kGroups % kWeightWarps == 0, "slots are shared out in turns");
+constexpr int kMinSlots = kGroups;
 constexpr int kMaxSlots = 8;  // 147 KB in flight (more measured slower)
 constexpr int kFewMaxSmem = 232448;
 constexpr long long kFewDrainCycles = 4000000000LL;
@@ -156,7 +157,10 @@ FewSmem few_smem(int tokens, int topk, int num_experts, int hidden) {
   s.chunks = take(4 * static_cast<size_t>(rows));
   s.rows = take(s.local ? operand(tokens, hidden, kHalfK).bytes : 0);
   s.ring = at;
-  s.slots = std::min(kMaxSlots, (kFewMaxSmem - at) / kWStage);
+  // a multiple of the warpgroups and of the copy warps, so that each slot
+  // belongs to one of each: otherwise one of them could come to a slot two
+  // phases ahead of it, which a wait on the phase's parity cannot tell from done
+  s.slots = std::min(kMaxSlots, (kFewMaxSmem - at) / kWStage) / kGroups * kGroups;
   s.total = at + s.slots * kWStage;
   return s;
 }

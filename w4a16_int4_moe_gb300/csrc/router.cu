@@ -125,8 +125,14 @@ constexpr int kTileM = 128;        // tokens of a tile (MMA M)
 constexpr int kMaxTileN = 256;     // experts of a tile (MMA N)
 constexpr int kMaxSplit = 8;
 constexpr int kMaxRing = 8;
-constexpr int kRingBytes = 200 << 10;  // 4 slots of k = 64 at N = 256, 5 at 192
-constexpr int kDenseThreads = 192;  // four epilogue warps, a copy warp, an MMA warp
+constexpr int kRingBytes = 200 << 10;
+// four epilogue warps, then two that copy and two that issue MMAs, by turns:
+// one thread gets round its loop (wait, copy or multiply, report) only every
+// 600 to 1100 cycles, against 384 of a k step at N = 192 (8192 tokens: 67 us
+// with one of each)
+constexpr int kDensePairs = 2;
+constexpr int kDenseThreads = 128 + 2 * 32 * kDensePairs;
+constexpr int kWarpCopy0 = 4, kWarpMma0 = 4 + kDensePairs;
 constexpr int kSumRow = kTileM + 1; // sums [expert][token], rows on different banks
 constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
 
@@ -137,8 +143,13 @@ struct DenseArgs {
   int tile_n, n_tiles, split, slots, tmem_cols;
 };
 
+// Ring slots, a multiple of the threads that take turns: each slot then belongs
+// to one copy and one MMA thread. (In a ring of five a thread could come to a
+// slot two phases ahead of it, which a wait on the phase's parity cannot tell
+// from done.) 4 at N = 256 and 192, up to 8 for narrower tiles.
 int dense_slots(int tile_n) {
-  return std::min(kMaxRing, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
+  const int fit = std::min(kMaxRing, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
+  return fit / kDensePairs * kDensePairs;
 }
 // the ring, whose memory the sums take over; the swizzle needs 1024 bytes
 size_t dense_smem(int tile_n) {
@@ -181,7 +192,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const int tile = static_cast<int>(blockIdx.x) / a.split;
   const int m0 = tile / a.n_tiles * kTileM, n0 = tile % a.n_tiles * a.tile_n;
   const int k0 = a.k_steps * rank / a.split, k1 = a.k_steps * (rank + 1) / a.split;
-  if (warp == 5) {
+  if (warp == kWarpMma0) {
     tmem_alloc(smem_u32(&tmem_at), static_cast<uint32_t>(a.tmem_cols));
     tmem_relinquish();
     if (lane == 0) {
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         mbar_init(full + 8 * i, 1);
         mbar_init(empty + 8 * i, 1);
       }
-      mbar_init(done, 1);
+      mbar_init(done, kDensePairs);
       *failed = 0;
       fence_mbar_init();
     }
@@ -201,12 +212,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   grid_dependents_go();
   const uint32_t tmem = tmem_at;
 
-  if (warp == 4) {
+  if (warp >= kWarpCopy0 && warp < kWarpMma0) {
     if (lane == 0) {
       bool ok = true;
-      int issued = 0;
-      for (int k = k0; k < k1 && ok; ++k, ++issued) {
-        const int slot = issued % a.slots;
+      const int first = warp - kWarpCopy0;
+      int issued = first;  // k step of this CTA
+      for (; k0 + issued < k1; issued += kDensePairs) {
+        const int slot = issued % a.slots, k = k0 + issued;
         ok = dense_wait(empty + 8 * slot, (issued / a.slots & 1) ^ 1, failed);
         if (!ok) break;
         mbar_arrive_expect_tx(full + 8 * slot, slot_bytes);
@@ -215,25 +227,29 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                     full + 8 * slot);
       }
       if (!ok)  // copies in flight land before the CTA ends
-        for (int i = max(0, issued - a.slots); i < issued; ++i) {
+        for (int i = first; i < issued; i += kDensePairs) {
+          if (i < issued - a.slots) continue;
           const long long t0 = clock64();
           while (!mbar_try_wait(full + 8 * (i % a.slots), i / a.slots & 1) &&
                  clock64() - t0 < kGiveUpCycles) {
           }
         }
     }
-  } else if (warp == 5) {
+  } else if (warp >= kWarpMma0) {
+    // each into an accumulator of its own
     if (lane == 0) {
+      const int first = warp - kWarpMma0;
+      const uint32_t d = tmem + static_cast<uint32_t>(first * a.tmem_cols / kDensePairs);
       const uint32_t idesc = idesc_bf16_m128(static_cast<uint32_t>(a.tile_n));
-      for (int k = k0; k < k1; ++k) {
-        const int i = k - k0, slot = i % a.slots;
+      for (int i = first; k0 + i < k1; i += kDensePairs) {
+        const int slot = i % a.slots;
         if (!dense_wait(full + 8 * slot, i / a.slots & 1, failed)) break;
         tc_fence_after();
         const uint64_t ad = smem_desc_sw128_kmajor(ring + slot * slot_bytes);
         const uint64_t bd = smem_desc_sw128_kmajor(ring + slot * slot_bytes + a_bytes);
 #pragma unroll
         for (int j = 0; j < kKStep / 16; ++j)  // 32 bytes further along k
-          mma_bf16_ss(tmem, ad + 2 * j, bd + 2 * j, idesc, i > 0 || j > 0);
+          mma_bf16_ss(d, ad + 2 * j, bd + 2 * j, idesc, i > first || j > 0);
         tc_commit(empty + 8 * slot);
       }
       tc_commit(done);
@@ -246,17 +262,20 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     float* sums = reinterpret_cast<float*>(smem);
     const int m = warp * 32 + lane;
     for (int c = 0; c < a.tile_n; c += 16) {
-      uint32_t v[16];
-      tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
-      tmem_ld_wait();
+      uint32_t v[16], u[16] = {};
+      const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + c;
+      tmem_ld_32x32b_x16(at, v);
+      if (k1 - k0 > 1) tmem_ld_32x32b_x16(at + a.tmem_cols / kDensePairs, u);
+      tmem_ld_wait_for(v, u);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        sums[(c + i) * kSumRow + m] = ok ? __uint_as_float(v[i]) : __uint_as_float(0x7FC00000u);
+        sums[(c + i) * kSumRow + m] =
+            ok ? __uint_as_float(v[i]) + __uint_as_float(u[i]) : __uint_as_float(0x7FC00000u);
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kWarpMma0) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, static_cast<uint32_t>(a.tmem_cols));
@@ -302,7 +321,7 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
   a.tile_n = std::max(16, ceil_div(ceil_div(num_experts, a.n_tiles), 16) * 16);
   a.slots = dense_slots(a.tile_n);
   a.tmem_cols = 32;
-  while (a.tmem_cols < a.tile_n) a.tmem_cols *= 2;
+  while (a.tmem_cols < a.tile_n * kDensePairs) a.tmem_cols *= 2;
   const long long tiles = static_cast<long long>(ceil_div(tokens, kTileM)) * a.n_tiles;
   // as many CTAs as fit, with at least four k steps each
   a.split = 1;
