@@ -281,19 +281,31 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     tmem_dealloc(tmem, static_cast<uint32_t>(a.tmem_cols));
   }
   if (a.split > 1) cluster_sync_all();
-  // this CTA's share of the tile's tokens, the split's sums in the CTAs' order
+  // this CTA's share of the tile's tokens, a token a warp; the split's sums in
+  // the CTAs' order
   const int rows = kTileM / a.split;
-  for (int i = threadIdx.x; i < rows * a.tile_n; i += kDenseThreads) {
-    const int m = rank * rows + i / a.tile_n, n = i % a.tile_n;
-    const uint32_t at = ring + static_cast<uint32_t>(n * kSumRow + m) * 4;
-    float v = 0.f;
-    if (a.split == 1)
-      v = *reinterpret_cast<const float*>(smem + (at - ring));
-    else
-      for (int c = 0; c < a.split; ++c)
-        v += ld_cluster_f32(map_to_cta(at, static_cast<uint32_t>(c)));
-    if (m0 + m < a.tokens && n0 + n < a.num_experts)
-      a.logits[static_cast<long long>(m0 + m) * a.num_experts + n0 + n] = v;
+  const float* sums = reinterpret_cast<const float*>(smem);
+  for (int r = warp; r < rows; r += kDenseThreads / 32) {
+    const int m = rank * rows + r;
+    if (m0 + m >= a.tokens) break;
+    float* out = a.logits + static_cast<long long>(m0 + m) * a.num_experts + n0;
+    const int n_end = min(a.tile_n, a.num_experts - n0);
+    if (a.split == 1) {
+#pragma unroll 4
+      for (int n = lane; n < n_end; n += 32) out[n] = sums[n * kSumRow + m];
+    } else {
+      for (int n = lane; n < n_end; n += 32) {
+        const uint32_t at = ring + static_cast<uint32_t>(n * kSumRow + m) * 4;
+        float v[kMaxSplit];
+#pragma unroll
+        for (int c = 0; c < kMaxSplit; ++c)
+          v[c] = c < a.split ? ld_cluster_f32(map_to_cta(at, static_cast<uint32_t>(c))) : 0.f;
+        float sum = v[0];
+#pragma unroll
+        for (int c = 1; c < kMaxSplit; ++c) sum += v[c];
+        out[n] = sum;
+      }
+    }
   }
   if (a.split > 1) cluster_sync_all();
 }
