@@ -30,6 +30,7 @@ namespace {
 // ----------------------------------------------------------- few tokens ---
 
 constexpr int kFewTokens = 64;
+constexpr int kFewBlock = 64;  // tokens of a CTA at most
 constexpr int kFewCluster = 8;
 constexpr int kFewWarps = 8;
 constexpr int kFewExperts = 16;  // of a cluster (MMA M)
@@ -57,7 +58,13 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int e0 = static_cast<int>(blockIdx.x) / kFewCluster * kFewExperts;
+  const int tile = static_cast<int>(blockIdx.x) / kFewCluster;
+  const int e_tiles = (num_experts + kFewExperts - 1) / kFewExperts;
+  const int e0 = tile % e_tiles * kFewExperts;
+  const int t0 = tile / e_tiles * (8 * kNt);
+  x += t0 * x_stride;
+  logits += static_cast<long long>(t0) * num_experts;
+  tokens = min(tokens - t0, 8 * kNt);
   grid_dependency_wait();
   grid_dependents_go();
   const int blocks = (hidden + 31) / 32;
@@ -133,7 +140,7 @@ constexpr int kRingBytes = 200 << 10;
 constexpr int kDensePairs = 2;
 constexpr int kDenseThreads = 128 + 2 * 32 * kDensePairs;
 constexpr int kWarpCopy0 = 4, kWarpMma0 = 4 + kDensePairs;
-constexpr int kSumRow = kTileM + 1; // sums [expert][token], rows on different banks
+constexpr int kSplitTileN = 128;   // of a tile whose columns are split
 constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
 
 struct DenseArgs {
@@ -151,10 +158,16 @@ int dense_slots(int tile_n) {
   const int fit = std::min(kMaxRing, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
   return fit / kDensePairs * kDensePairs;
 }
-// the ring, whose memory the sums take over; the swizzle needs 1024 bytes
-size_t dense_smem(int tile_n) {
+// The ring's memory, which the swizzle wants at 1024 bytes, is later the tile's
+// sums [token][expert], four floats between rows so that they start on
+// different banks, and behind them what the other CTAs of a split send.
+__host__ __device__ inline int sum_pitch(int tile_n) { return tile_n + 4; }
+__host__ __device__ inline int tile_sums_bytes(int tile_n) {
+  return kTileM * sum_pitch(tile_n) * 4;
+}
+size_t dense_smem(int tile_n, int split) {
   const size_t ring = static_cast<size_t>(dense_slots(tile_n)) * (kTileM + tile_n) * kKStep * 2;
-  const size_t sums = static_cast<size_t>(tile_n) * kSumRow * 4;
+  const size_t sums = static_cast<size_t>(tile_sums_bytes(tile_n)) * (split > 1 ? 2 : 1);
   return 2048 + std::max(ring, sums);
 }
 
@@ -179,12 +192,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bars[2 * kMaxRing + 1];
+  __shared__ uint64_t bars[2 * kMaxRing + 2];
   __shared__ uint32_t tmem_at;
   __shared__ int failed_word;
   volatile int* failed = &failed_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxRing, done = full + 16 * kMaxRing;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxRing, done = full + 16 * kMaxRing,
+                 received = done + 8;
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.tile_n) * kKStep * 2;
   const uint32_t slot_bytes = a_bytes + b_bytes;
@@ -201,6 +215,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         mbar_init(empty + 8 * i, 1);
       }
       mbar_init(done, kDensePairs);
+      mbar_init(received, 1);
       *failed = 0;
       fence_mbar_init();
     }
@@ -259,8 +274,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     bool ok = dense_wait(done, 0, failed);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    float* sums = reinterpret_cast<float*>(smem);
-    const int m = warp * 32 + lane;
+    float* row = reinterpret_cast<float*>(smem) + (warp * 32 + lane) * sum_pitch(a.tile_n);
     for (int c = 0; c < a.tile_n; c += 16) {
       uint32_t v[16], u[16] = {};
       const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + c;
@@ -268,10 +282,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       if (k1 - k0 > 1) tmem_ld_32x32b_x16(at + a.tmem_cols / kDensePairs, u);
       tmem_ld_wait_for(v, u);
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        sums[(c + i) * kSumRow + m] =
-            ok ? __uint_as_float(v[i]) + __uint_as_float(u[i]) : __uint_as_float(0x7FC00000u);
+      for (int i = 0; i < 4; ++i) {
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          f[j] = ok ? __uint_as_float(v[4 * i + j]) + __uint_as_float(u[4 * i + j])
+                    : __uint_as_float(0x7FC00000u);
+        *reinterpret_cast<float4*>(row + c + 4 * i) = make_float4(f[0], f[1], f[2], f[3]);
+      }
     }
+    fence_proxy_async_smem();  // a bulk copy sends them on
     tc_fence_before();
   }
   __syncthreads();
@@ -280,41 +300,48 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, static_cast<uint32_t>(a.tmem_cols));
   }
-  if (a.split > 1) cluster_sync_all();
-  // this CTA's share of the tile's tokens, a token a warp; the split's sums in
-  // the CTAs' order
-  const int rows = kTileM / a.split;
+  // a split: every CTA finishes a share of the tokens, whose sums the others
+  // send it, one bulk copy each
+  const int rows = kTileM / a.split, pitch = sum_pitch(a.tile_n);
+  const uint32_t share = static_cast<uint32_t>(rows * pitch * 4);
+  const uint32_t inbox = ring + static_cast<uint32_t>(tile_sums_bytes(a.tile_n));
+  bool whole = true;
+  if (a.split > 1) {
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(received, share * (a.split - 1));
+    cluster_sync_all();  // everybody's ring is done with, and expects
+    if (static_cast<int>(threadIdx.x) < a.split && static_cast<int>(threadIdx.x) != rank) {
+      const uint32_t to = threadIdx.x;
+      asm volatile(
+          "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes "
+          "[%0], [%1], %2, [%3];" ::"r"(map_to_cta(inbox + rank * share, to)),
+          "r"(ring + to * share), "r"(share), "r"(map_to_cta(received, to))
+          : "memory");
+    }
+    whole = dense_wait(received, 0, failed);
+  }
   const float* sums = reinterpret_cast<const float*>(smem);
+  const float* others = reinterpret_cast<const float*>(smem + (inbox - ring));
+  const int n_end = min(a.tile_n, a.num_experts - n0);
   for (int r = warp; r < rows; r += kDenseThreads / 32) {
     const int m = rank * rows + r;
     if (m0 + m >= a.tokens) break;
     float* out = a.logits + static_cast<long long>(m0 + m) * a.num_experts + n0;
-    const int n_end = min(a.tile_n, a.num_experts - n0);
-    if (a.split == 1) {
 #pragma unroll 4
-      for (int n = lane; n < n_end; n += 32) out[n] = sums[n * kSumRow + m];
-    } else {
-      for (int n = lane; n < n_end; n += 32) {
-        const uint32_t at = ring + static_cast<uint32_t>(n * kSumRow + m) * 4;
-        float v[kMaxSplit];
-#pragma unroll
-        for (int c = 0; c < kMaxSplit; ++c)
-          v[c] = c < a.split ? ld_cluster_f32(map_to_cta(at, static_cast<uint32_t>(c))) : 0.f;
-        float sum = v[0];
-#pragma unroll
-        for (int c = 1; c < kMaxSplit; ++c) sum += v[c];
-        out[n] = sum;
-      }
+    for (int n = lane; n < n_end; n += 32) {
+      float v = 0.f;
+      for (int c = 0; c < a.split; ++c)  // in the CTAs' order
+        v += c == rank ? sums[m * pitch + n] : others[(c * rows + r) * pitch + n];
+      out[n] = whole ? v : __uint_as_float(0x7FC00000u);
     }
   }
-  if (a.split > 1) cluster_sync_all();
+  if (a.split > 1) cluster_sync_all();  // the sums stay until all are sent
 }
 
 cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
                                  int tokens, int hidden, int num_experts, float* logits, int sms,
                                  cudaStream_t stream) {
   if (tokens <= kFewTokens) {
-    const int grid = (num_experts + kFewExperts - 1) / kFewExperts * kFewCluster;
+    const int grid = ceil_div(num_experts, kFewExperts) * ceil_div(tokens, kFewBlock) * kFewCluster;
     const auto run = [&](auto kernel) {
       return launch_dependent(kernel, grid, kFewWarps * 32, 0, kFewCluster, stream, x, x_stride,
                               weight, tokens, hidden, num_experts, logits);
@@ -329,21 +356,26 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
   a.tokens = tokens;
   a.num_experts = num_experts;
   a.k_steps = packed_ksteps(hidden);
+  // tiles as wide as can be; narrower ones where these leave half the SMs idle,
+  // and then as many CTAs on the columns of a tile as there are SMs for, with
+  // at least four k steps each
+  const int m_tiles = ceil_div(tokens, kTileM);
   a.n_tiles = ceil_div(num_experts, kMaxTileN);
+  const bool narrow = static_cast<long long>(m_tiles) * a.n_tiles * 2 <= sms;
+  if (narrow) a.n_tiles = ceil_div(num_experts, kSplitTileN);
   a.tile_n = std::max(16, ceil_div(ceil_div(num_experts, a.n_tiles), 16) * 16);
   a.slots = dense_slots(a.tile_n);
   a.tmem_cols = 32;
   while (a.tmem_cols < a.tile_n * kDensePairs) a.tmem_cols *= 2;
-  const long long tiles = static_cast<long long>(ceil_div(tokens, kTileM)) * a.n_tiles;
-  // as many CTAs as fit, with at least four k steps each
+  const long long tiles = static_cast<long long>(m_tiles) * a.n_tiles;
   a.split = 1;
-  while (a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.k_steps / (a.split * 2) >= 4)
+  while (narrow && a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.k_steps / (a.split * 2) >= 4)
     a.split *= 2;
   if (!encode_rows_tmap(&a.x, x, tokens, hidden, x_stride, kTileM) ||
       !encode_rows_tmap(&a.weight, weight, num_experts, hidden, hidden, a.tile_n))
     return cudaErrorInvalidValue;
   if (tiles * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const size_t smem = dense_smem(a.tile_n);
+  const size_t smem = dense_smem(a.tile_n, a.split);
   const cudaError_t e = cudaFuncSetAttribute(
       w4a16_router_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 2048);
   if (e != cudaSuccess) return e;
