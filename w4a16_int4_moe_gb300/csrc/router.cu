@@ -29,8 +29,10 @@ namespace {
 
 // ----------------------------------------------------------- few tokens ---
 
+// (at 65 tokens x 384 experts x 7168 columns the two kernels take 10 us each,
+// at 64 tokens this one 6.5)
 constexpr int kFewTokens = 64;
-constexpr int kFewBlock = 64;  // tokens of a CTA at most
+constexpr int kFewBlock = 32;  // tokens of a CTA at most (64: 9.9 us for 48 tokens, 32: 6.5)
 constexpr int kFewCluster = 8;
 constexpr int kFewWarps = 8;
 constexpr int kFewExperts = 16;  // of a cluster (MMA M)
@@ -326,7 +328,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const int m = rank * rows + r;
     if (m0 + m >= a.tokens) break;
     float* out = a.logits + static_cast<long long>(m0 + m) * a.num_experts + n0;
-#pragma unroll 4
+    if (a.split == 1) {
+#pragma unroll 8
+      for (int n = lane; n < n_end; n += 32) out[n] = sums[m * pitch + n];
+      continue;
+    }
     for (int n = lane; n < n_end; n += 32) {
       float v = 0.f;
       for (int c = 0; c < a.split; ++c)  // in the CTAs' order
@@ -348,8 +354,7 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
     };
     if (tokens <= 8) return run(w4a16_router_few_kernel<1>);
     if (tokens <= 16) return run(w4a16_router_few_kernel<2>);
-    if (tokens <= 32) return run(w4a16_router_few_kernel<4>);
-    return run(w4a16_router_few_kernel<8>);
+    return run(w4a16_router_few_kernel<kFewBlock / 8>);
   }
   DenseArgs a;
   a.logits = logits;
