@@ -390,23 +390,28 @@ __device__ __forceinline__ void slot_next(int& slot, uint32_t& phase, int step, 
 }
 
 // The stages of one product, cut into equal runs: CTA b of `grid` owns
-// [begin(b), begin(b + 1)), `base` stages each and one more for the first
-// `extra` CTAs (the host keeps the total below 2^30).
+// [begin(b), begin(b + 1)), `base` units each and one more for the first
+// `extra` CTAs (the host keeps the total below 2^30). A unit is a stage, or a
+// whole item where items are so short (two stages for each warpgroup) that the
+// exchange of shares, some 2.5 us, takes longer than they do.
+constexpr int kWholeItem = 2 * kGroups;
 struct Split {
-  int stages;  // of one item
-  int grid, base, extra;
-  __device__ __forceinline__ Split(int items, int item_stages, int ctas) {
-    const int total = items * item_stages;
-    stages = item_stages;
+  int stages;  // of one pass over an expert's tile
+  int unit, grid, base, extra;
+  // `items` items of item_stages stages
+  __device__ __forceinline__ Split(int items, int item_stages, int pass_stages, int ctas) {
+    stages = pass_stages;
+    unit = item_stages <= kWholeItem ? item_stages : 1;
+    const int total = items * (item_stages / unit);
     grid = min(ctas, total);
     base = total / grid;
     extra = total - base * grid;
   }
-  __device__ __forceinline__ int begin(int b) const { return b * base + min(b, extra); }
+  __device__ __forceinline__ int begin(int b) const { return (b * base + min(b, extra)) * unit; }
   // the CTA that owns stage `at`
   __device__ __forceinline__ int owner(int at) const {
-    const int longer = extra * (base + 1);
-    return at < longer ? at / (base + 1) : extra + (at - longer) / base;
+    const int u = at / unit, longer = extra * (base + 1);
+    return u < longer ? u / (base + 1) : extra + (u - longer) / base;
   }
 };
 
@@ -469,6 +474,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   for (int e = tid; e < a.num_experts; e += kFewThreads) s_mask[e] = 0u;
   grid_dependency_wait();  // what follows reads what earlier launches wrote
   grid_dependents_go();
+  if (a.logits != nullptr && (sm.local || static_cast<int>(blockIdx.x) < a.tokens)) {
+    // the logits of the (first) token that this CTA routes, into L1 meanwhile
+    const int bytes = a.num_global * (a.bf16_logits ? 2 : 4);
+    const uint8_t* row = static_cast<const uint8_t*>(a.logits) +
+                         (sm.local ? 0 : static_cast<long long>(blockIdx.x) * bytes);
+    if (tid * 128 < bytes) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + tid * 128));
+  }
   // the rows into FP16, all of them or this CTA's share: sixteen lanes a block
   // of 128
   {
@@ -665,8 +677,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
   const int steps0 = (a.hidden + kKStep - 1) / kKStep, steps1 = (a.inter + kKStep - 1) / kKStep;
   const int groups0 = a.hidden / kGroup, groups1 = a.inter / kGroup;
   const int tiles0 = a.inter / 64, tiles1 = (a.hidden + kTileRows - 1) / kTileRows;
-  const Split gu(num_chunks * tiles0, (steps0 + 3) / 4, gridDim.x);
-  const Split dn(num_chunks * tiles1, (steps1 + 3) / 4, gridDim.x);
+  const Split gu(num_chunks * tiles0, (steps0 + 3) / 4, (steps0 + 3) / 4, gridDim.x);
+  const Split dn(tiles1, num_chunks * ((steps1 + 3) / 4), (steps1 + 3) / 4, gridDim.x);
   const int cta = blockIdx.x;
   const int gu_begin = cta < gu.grid ? gu.begin(cta) : 0, gu_end = cta < gu.grid ? gu.begin(cta + 1) : 0;
   const int dn_begin = cta < dn.grid ? dn.begin(cta) : 0, dn_end = cta < dn.grid ? dn.begin(cta + 1) : 0;
@@ -944,6 +956,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     const int etid = tid - 32 * kWarpEpilogue0;
     bool live = true;
     uint32_t items = 0;  // sums taken, the two buffers by turns
+    // This CTA has used the counters for the last time (the first warp calls
+    // it); the last one to say so leaves them zero for the next call.
+    const auto leave = [&]() {
+      if (etid >= 32) return;
+      int last = 0;
+      if (etid == 0)
+        last = atomicAdd(&counters->exits, 1) == static_cast<int>(gridDim.x) - 1;
+      if (!__shfl_sync(0xffffffffu, last, 0)) return;
+      for (int i = etid; i < 2 * kMaxCtas; i += 32) counters->item[0][i] = 0;
+      if (etid == 0) {
+        counters->act_done = 0;
+        counters->rows_done = 0;
+        counters->exits = 0;
+      }
+    };
     if (gu_count > 0) {
       const int S = gu.stages;
       int q = gu_begin / S, at = gu_begin;
@@ -1087,8 +1114,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_se);
-        if (cta0 != cta1 &&
-            epilogue_arrive(&counters->item[1][cta0], cta1 - cta0, last_arrival, etid)) {
+        const int next_at = min(dn_end, tile0 + tile_stages);
+        const bool join = cta0 != cta1 && epilogue_arrive(&counters->item[1][cta0], cta1 - cta0,
+                                                          last_arrival, etid);
+        if (next_at == dn_end) leave();
+        if (join) {
           // the shares in the CTAs' order, eight quads of a thread at a time
           for (int i0 = etid; i0 < quads; i0 += 8 * kEpilogueThreads) {
             float4 v[8] = {};
@@ -1105,18 +1135,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
               if (i0 + j * kEpilogueThreads < quads) put_out(i0 + j * kEpilogueThreads, v[j]);
           }
         }
-        at = min(dn_end, tile0 + tile_stages);
+        at = next_at;
       }
     }
-    // the last CTA out leaves the counters zero for the next call
-    if (epilogue_arrive(&counters->exits, static_cast<int>(gridDim.x) - 1, last_arrival, etid)) {
-      for (int i = etid; i < 2 * kMaxCtas; i += kEpilogueThreads) counters->item[0][i] = 0;
-      if (etid == 0) {
-        counters->act_done = 0;
-        counters->rows_done = 0;
-        counters->exits = 0;
-      }
-    }
+    if (dn_end == dn_begin) leave();
   }
 }
 
