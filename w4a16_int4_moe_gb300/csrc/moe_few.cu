@@ -15,20 +15,22 @@
 //   * two threads copy the stages into a shared-memory ring (bulk copies);
 //     they run through both products without waiting for the activation, so
 //     the ring is full of down weights when the activation is complete;
-//   * eight warps feed the codes to m16n8k16 MMAs of FP16 operands: the bits
-//     000qqqq and 000qqqq0000 are subnormal FP16 numbers, q * 2^-24 and
-//     q * 2^-20, so a word of eight codes becomes four MMA registers with one
-//     shift and four ANDs. The 8 that every code is too large comes off as the
-//     number that a group's sums start from, -8 times the columns, from two
-//     more MMAs a group. Weights are the M side, the rows of an
-//     expert (at most four per pass over its weights) the N side; the scale of
-//     a group of 32 is applied to the group's FP32 sum, so no weight is
-//     rounded. The codes never leave registers: through TMEM, as the tcgen05
-//     kernel of the large batches needs them, the same stream reaches 0.4 of
-//     the copy bandwidth, and as BF16 pairs q - 8 for BF16 MMAs 0.55 (430
-//     instructions a stage and warp, 190 of them on the half-rate integer
-//     pipe). e4m3 MMAs, for which the code bytes would do as they are, cost
-//     more: mma.sync converts their operands;
+//   * eight warps feed the codes to m16n8k16 MMAs of FP16 operands: a code in
+//     bits 7 to 10 of a half word is the FP16 number q * 2^-17 (bits 0 to 9 of
+//     a subnormal and the lowest exponent bit above them count on without a
+//     step), so a word of eight codes becomes four MMA registers with four
+//     shifts and four ANDs. (In bits 0 to 7 three of the shifts would go, but
+//     the tensor core lines products up by their exponents and a subnormal's
+//     leading zeros are lost precision: 3.6e-6 against 3e-7 of the output.)
+//     The 8 that every code is too large comes off as the number that a group's
+//     sums start from, -8 times the columns, from two more MMAs a group.
+//     Weights are the M side, the rows of an expert (at most four per pass over
+//     its weights) the N side; the scale of a group of 32 is applied to the
+//     group's FP32 sum, so no weight is rounded. The codes never leave
+//     registers: through TMEM, as the tcgen05 kernel of the large batches needs
+//     them, the same stream reaches 0.4 of the copy bandwidth, and as BF16
+//     pairs q - 8 for BF16 MMAs 0.55. e4m3 MMAs, for which the code bytes would
+//     do as they are, cost more: mma.sync converts their operands;
 //   * the rows are put into FP16 first, times a power of two per block of 128
 //     columns (a BF16 value fits exactly down to 2^-32 of its block's largest;
 //     rows in e4m3 fit as they are); the FP32 activation goes into two FP16
@@ -76,7 +78,7 @@ constexpr int kHalfK = kStageK / 2;          // columns that a lane holds at a t
 constexpr int kRowsPerPass = 4;              // rows of an expert per pass over its weights
 constexpr int kActParts = 2;                 // FP16 parts of an activation value
 constexpr float kPartScale = 2048.f;         // the second part is the rest times this
-constexpr float kCodeScale = 16777216.f;     // a code is q * 2^-24
+constexpr float kCodeScale = 131072.f;       // a code is q * 2^-17
 constexpr int kSumPitch = 132;               // FP32 sums [row][128 + 4]
 constexpr int kMaxCtas = 192;
 static_assert(kGroups % kWeightWarps == 0, "slots are shared out in turns");
@@ -201,10 +203,6 @@ __device__ __forceinline__ float block_factor(uint32_t max_bits) {
   return __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
 }
 
-// Value k of a row as the MMAs take it: the codes k = 2, 3 of every four lie
-// four bits higher in their word, times 16.
-__device__ __forceinline__ float column_value(int k, float y) { return k & 2 ? y * 0.0625f : y; }
-
 // The columns of half a stage in a lane's registers: thread t of a quad holds
 // k = 8t .. 8t + 7 of each of the four groups of its MMA column. They come
 // straight from L1 or L2, right after the same groups of the half before were
@@ -229,8 +227,8 @@ __device__ __forceinline__ uint4 load16(const void* from) {
 template <int kCols, int kG>
 __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const uint4& b0,
                                          const uint4& b1, float (&acc)[kMt][2 * kCols]) {
-  constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
-  const uint32_t minus8[4] = {0x80088008u, 0x80088008u, 0x80808080u, 0x80808080u};
+  constexpr uint32_t kCode = 0x07800780u, kMinus8 = 0x84008400u;
+  const uint32_t minus8[4] = {kMinus8, kMinus8, kMinus8, kMinus8};
   uint32_t w[kG][kMt / 2][4], sc[kMt / 2][4];
 #pragma unroll
   for (int g = 0; g < kG; ++g)
@@ -248,9 +246,8 @@ __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const 
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt) {
       const uint32_t w0 = w[g][mt >> 1][2 * (mt & 1)], w1 = w[g][mt >> 1][2 * (mt & 1) + 1];
-      const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
-      const uint32_t a0[4] = {w0 & kLow, w1 & kLow, w0 & kHigh, w1 & kHigh};
-      const uint32_t a1[4] = {v0 & kLow, v1 & kLow, v0 & kHigh, v1 & kHigh};
+      const uint32_t a0[4] = {w0 << 7 & kCode, w1 << 7 & kCode, w0 << 3 & kCode, w1 << 3 & kCode};
+      const uint32_t a1[4] = {w0 >> 1 & kCode, w1 >> 1 & kCode, w0 >> 5 & kCode, w1 >> 5 & kCode};
       float c[4];
       mma16816(c, a0, b.x, b.y, i[0], i[1], i[2], i[3]);
       mma16816(c, a1, b.z, b.w, c[0], c[1], c[2], c[3]);
@@ -530,8 +527,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
       uint32_t packed[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(column_value(2 * i, y[2 * i]),
-                                            column_value(2 * i + 1, y[2 * i + 1]));
+        const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
         packed[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
       if (in)
@@ -1011,12 +1007,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
               // (0 beside an infinity or a NaN)
               float rest = (y - __half2float(hi)) * kPartScale;
               if (!(fabsf(y) < INFINITY)) rest = 0.f;
-              const float value[kActParts] = {__half2float(hi), __half2float(__float2half_rn(rest))};
+              const __half value[kActParts] = {hi, __float2half_rn(rest)};
               const long long row = static_cast<long long>(row0 + r) * kActParts;
 #pragma unroll
               for (int p = 0; p < kActParts; ++p) {
                 reinterpret_cast<__half*>(act_op)[(row + p) * a.inter + inner * 64 + c] =
-                    __float2half_rn(column_value(c, value[p]));
+                    value[p];
               }
               if (etid == 0)
                 reinterpret_cast<float*>(act_op + ao.factors)[row * ao.blocks + inner] =
