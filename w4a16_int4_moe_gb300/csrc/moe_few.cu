@@ -16,12 +16,14 @@
 //     they run through both products without waiting for the activation, so
 //     the ring is full of down weights when the activation is complete;
 //   * eight warps feed the codes to m16n8k16 MMAs of FP16 operands: a code in
-//     bits 7 to 10 of a half word is the FP16 number q * 2^-17 (bits 0 to 9 of
-//     a subnormal and the lowest exponent bit above them count on without a
-//     step), so a word of eight codes becomes four MMA registers with four
-//     shifts and four ANDs. (In bits 0 to 7 three of the shifts would go, but
-//     the tensor core lines products up by their exponents and a subnormal's
-//     leading zeros are lost precision: 3.6e-6 against 3e-7 of the output.)
+//     bits 3 to 6 or 7 to 10 of a half word is the FP16 number q * 2^-21 or
+//     q * 2^-17 (bits 0 to 9 of a subnormal and the lowest exponent bit above
+//     them count on without a step), so a word of eight codes becomes four MMA
+//     registers with two shifts and four ANDs. (In bits 0 to 7 one shift would
+//     do, but the tensor core lines products up by their exponents, and a
+//     subnormal's leading zeros are lost precision: 3.6e-6 of the output,
+//     against 3e-7 with all codes in the highest bits, four shifts and 6 per
+//     cent of the time.)
 //     The 8 that every code is too large comes off as the number that a group's
 //     sums start from, -8 times the columns, from two more MMAs a group.
 //     Weights are the M side, the rows of an expert (at most four per pass over
@@ -78,7 +80,7 @@ constexpr int kHalfK = kStageK / 2;          // columns that a lane holds at a t
 constexpr int kRowsPerPass = 4;              // rows of an expert per pass over its weights
 constexpr int kActParts = 2;                 // FP16 parts of an activation value
 constexpr float kPartScale = 2048.f;         // the second part is the rest times this
-constexpr float kCodeScale = 131072.f;       // a code is q * 2^-17
+constexpr float kCodeScale = 2097152.f;      // a code is q * 2^-21
 constexpr int kSumPitch = 132;               // FP32 sums [row][128 + 4]
 constexpr int kMaxCtas = 192;
 static_assert(kGroups % kWeightWarps == 0, "slots are shared out in turns");
@@ -203,6 +205,10 @@ __device__ __forceinline__ float block_factor(uint32_t max_bits) {
   return __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
 }
 
+// Value k of a row as the MMAs take it: of every four codes of a row the last
+// two lie four bits higher in their half words, times 16.
+__device__ __forceinline__ float column_value(int k, float y) { return k & 2 ? y * 0.0625f : y; }
+
 // The columns of half a stage in a lane's registers: thread t of a quad holds
 // k = 8t .. 8t + 7 of each of the four groups of its MMA column. They come
 // straight from L1 or L2, right after the same groups of the half before were
@@ -227,8 +233,8 @@ __device__ __forceinline__ uint4 load16(const void* from) {
 template <int kCols, int kG>
 __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const uint4& b0,
                                          const uint4& b1, float (&acc)[kMt][2 * kCols]) {
-  constexpr uint32_t kCode = 0x07800780u, kMinus8 = 0x84008400u;
-  const uint32_t minus8[4] = {kMinus8, kMinus8, kMinus8, kMinus8};
+  constexpr uint32_t kLow = 0x00780078u, kHigh = 0x07800780u;
+  const uint32_t minus8[4] = {0x80408040u, 0x80408040u, 0x84008400u, 0x84008400u};
   uint32_t w[kG][kMt / 2][4], sc[kMt / 2][4];
 #pragma unroll
   for (int g = 0; g < kG; ++g)
@@ -246,8 +252,9 @@ __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const 
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt) {
       const uint32_t w0 = w[g][mt >> 1][2 * (mt & 1)], w1 = w[g][mt >> 1][2 * (mt & 1) + 1];
-      const uint32_t a0[4] = {w0 << 7 & kCode, w1 << 7 & kCode, w0 << 3 & kCode, w1 << 3 & kCode};
-      const uint32_t a1[4] = {w0 >> 1 & kCode, w1 >> 1 & kCode, w0 >> 5 & kCode, w1 >> 5 & kCode};
+      const uint32_t u0 = w0 << 3, u1 = w1 << 3, v0 = w0 >> 5, v1 = w1 >> 5;
+      const uint32_t a0[4] = {u0 & kLow, u1 & kLow, u0 & kHigh, u1 & kHigh};
+      const uint32_t a1[4] = {v0 & kLow, v1 & kLow, v0 & kHigh, v1 & kHigh};
       float c[4];
       mma16816(c, a0, b.x, b.y, i[0], i[1], i[2], i[3]);
       mma16816(c, a1, b.z, b.w, c[0], c[1], c[2], c[3]);
@@ -527,7 +534,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
       uint32_t packed[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+        const __half2 h = __floats2half2_rn(column_value(2 * i, y[2 * i]),
+                                            column_value(2 * i + 1, y[2 * i + 1]));
         packed[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
       if (in)
@@ -1012,7 +1020,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
 #pragma unroll
               for (int p = 0; p < kActParts; ++p) {
                 reinterpret_cast<__half*>(act_op)[(row + p) * a.inter + inner * 64 + c] =
-                    value[p];
+                    __float2half_rn(column_value(c, __half2float(value[p])));
               }
               if (etid == 0)
                 reinterpret_cast<float*>(act_op + ao.factors)[row * ao.blocks + inner] =
