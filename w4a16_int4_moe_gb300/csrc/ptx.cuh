@@ -315,19 +315,12 @@ __device__ __forceinline__ void tmem_ld_wait() {
 }
 
 // The same for arithmetic on what was loaded: the wait passes the registers on,
-// so that no use of them (which would also let others take them while the load
-// is under way) can be placed before it.
-__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[16], uint32_t (&u)[16]) {
+// so that no use of them can be placed before it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
                  "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
                  "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-               :
-               : "memory");
-  asm volatile(""
-               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]),
-                 "+r"(u[6]), "+r"(u[7]), "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]),
-                 "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15])
                :
                : "memory");
 }

@@ -135,13 +135,20 @@ constexpr int kMaxTileN = 256;     // experts of a tile (MMA N)
 constexpr int kMaxSplit = 8;
 constexpr int kMaxRing = 8;
 constexpr int kRingBytes = 200 << 10;
-// four epilogue warps, then two that copy and two that issue MMAs, by turns:
+// Eight epilogue warps, then two that copy and two that issue MMAs, by turns:
 // one thread gets round its loop (wait, copy or multiply, report) only every
 // 600 to 1100 cycles, against 384 of a k step at N = 192 (8192 tokens: 67 us
-// with one of each)
+// with one of each).
 constexpr int kDensePairs = 2;
-constexpr int kDenseThreads = 128 + 2 * 32 * kDensePairs;
-constexpr int kWarpCopy0 = 4, kWarpMma0 = 4 + kDensePairs;
+constexpr int kSumWarps = 8;       // two a TMEM quarter, half of the columns each
+constexpr int kDenseThreads = 32 * (kSumWarps + 2 * kDensePairs);
+constexpr int kWarpCopy0 = kSumWarps, kWarpMma0 = kSumWarps + kDensePairs;
+// The tensor core cuts its sums off instead of rounding them, which over the
+// 224 additions that 7168 columns are to each of two accumulators came to
+// 3.8e-6 of the logits. So after eight k steps (32 additions) an MMA thread
+// hands its accumulator to the epilogue warps, which add it to FP32 sums in
+// registers, and begins at zero: 4.8e-7, for 2 us of 50.
+constexpr int kChunk = 8;
 constexpr int kSplitTileN = 128;   // of a tile whose columns are split
 constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
 
@@ -194,13 +201,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bars[2 * kMaxRing + 2];
+  __shared__ uint64_t bars[2 * kMaxRing + 2 * kDensePairs + 1];
   __shared__ uint32_t tmem_at;
   __shared__ int failed_word;
   volatile int* failed = &failed_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxRing, done = full + 16 * kMaxRing,
-                 received = done + 8;
+                 drained = done + 8 * kDensePairs, received = drained + 8 * kDensePairs;
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.tile_n) * kKStep * 2;
   const uint32_t slot_bytes = a_bytes + b_bytes;
@@ -216,7 +223,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         mbar_init(full + 8 * i, 1);
         mbar_init(empty + 8 * i, 1);
       }
-      mbar_init(done, kDensePairs);
+      for (int i = 0; i < kDensePairs; ++i) {
+        mbar_init(done + 8 * i, 1);
+        mbar_init(drained + 8 * i, kSumWarps);
+      }
       mbar_init(received, 1);
       *failed = 0;
       fence_mbar_init();
@@ -258,43 +268,68 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       const int first = warp - kWarpMma0;
       const uint32_t d = tmem + static_cast<uint32_t>(first * a.tmem_cols / kDensePairs);
       const uint32_t idesc = idesc_bf16_m128(static_cast<uint32_t>(a.tile_n));
-      for (int i = first; k0 + i < k1; i += kDensePairs) {
+      int n = 0;  // steps of this thread
+      for (int i = first; k0 + i < k1; i += kDensePairs, ++n) {
         const int slot = i % a.slots;
+        if (n > 0 && n % kChunk == 0) {
+          tc_commit(done + 8 * first);
+          if (!dense_wait(drained + 8 * first, (n / kChunk - 1) & 1, failed)) break;
+          tc_fence_after();
+        }
         if (!dense_wait(full + 8 * slot, i / a.slots & 1, failed)) break;
         tc_fence_after();
         const uint64_t ad = smem_desc_sw128_kmajor(ring + slot * slot_bytes);
         const uint64_t bd = smem_desc_sw128_kmajor(ring + slot * slot_bytes + a_bytes);
 #pragma unroll
         for (int j = 0; j < kKStep / 16; ++j)  // 32 bytes further along k
-          mma_bf16_ss(d, ad + 2 * j, bd + 2 * j, idesc, i > first || j > 0);
+          mma_bf16_ss(d, ad + 2 * j, bd + 2 * j, idesc, n % kChunk != 0 || j > 0);
         tc_commit(empty + 8 * slot);
       }
-      tc_commit(done);
+      if (n > 0) tc_commit(done + 8 * first);
     }
   } else {
-    // lane + 32 warp = token of the tile; the sums take the ring's place
-    bool ok = dense_wait(done, 0, failed);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
-    float* row = reinterpret_cast<float*>(smem) + (warp * 32 + lane) * sum_pitch(a.tile_n);
-    for (int c = 0; c < a.tile_n; c += 16) {
-      uint32_t v[16], u[16] = {};
-      const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + c;
-      tmem_ld_32x32b_x16(at, v);
-      if (k1 - k0 > 1) tmem_ld_32x32b_x16(at + a.tmem_cols / kDensePairs, u);
-      tmem_ld_wait_for(v, u);
+    // lane + 32 (warp % 4) = token of the tile, half of the experts; in the end
+    // the sums take the ring's place
+    const int half = (a.tile_n / 2 + 15) / 16 * 16;
+    const int c0 = warp < 4 ? 0 : half, cols = warp < 4 ? half : a.tile_n - half;
+    const uint32_t at = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + c0;
+    float sum[kMaxTileN / 2] = {};
+    bool ok = true;
+    for (int c = 0; ok; ++c) {
+      bool any = false;
+      for (int j = 0; j < kDensePairs && ok; ++j) {
+        // chunk c of MMA thread j, which has the steps j, j + kDensePairs, ...
+        if (j + c * kChunk * kDensePairs >= k1 - k0) continue;
+        any = true;
+        ok = __all_sync(0xffffffffu, dense_wait(done + 8 * j, c & 1, failed));
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[4];
+        for (int p = 0; p < kMaxTileN / 32; ++p)
+          if (16 * p < cols) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(at + j * (a.tmem_cols / kDensePairs) + 16 * p, v);
+            tmem_ld_wait_for(v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          f[j] = ok ? __uint_as_float(v[4 * i + j]) + __uint_as_float(u[4 * i + j])
-                    : __uint_as_float(0x7FC00000u);
-        *reinterpret_cast<float4*>(row + c + 4 * i) = make_float4(f[0], f[1], f[2], f[3]);
+            for (int i = 0; i < 16; ++i) sum[16 * p + i] += __uint_as_float(v[i]);
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(drained + 8 * j);
       }
+      if (!any) break;
     }
+    ok = __all_sync(0xffffffffu, ok && !*failed);
+    // (nothing reads the ring any more: all of its copies were multiplied)
+    float* row = reinterpret_cast<float*>(smem) + (warp % 4 * 32 + lane) * sum_pitch(a.tile_n) + c0;
+#pragma unroll
+    for (int p = 0; p < kMaxTileN / 8; ++p)
+      if (4 * p < cols)
+        *reinterpret_cast<float4*>(row + 4 * p) =
+            ok ? make_float4(sum[4 * p], sum[4 * p + 1], sum[4 * p + 2], sum[4 * p + 3])
+               : make_float4(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u),
+                             __uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
     fence_proxy_async_smem();  // a bulk copy sends them on
-    tc_fence_before();
   }
   __syncthreads();
   if (warp == kWarpMma0) {
