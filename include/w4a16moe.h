@@ -448,7 +448,8 @@ enum { W4A16_FP8_NONE = 0, W4A16_FP8_ROW = -1, W4A16_FP8_GROUP = 128 };
  *   out = bf16(y)
  *   scales = max(amax(|y|), 1e-10) / 448, over each group of 128 columns
  *            (W4A16_FP8_GROUP; the last group may be shorter) or over the row
- *            (W4A16_FP8_ROW);  out_fp8 = e4m3(y / scale), round to nearest.
+ *            (W4A16_FP8_ROW);  out_fp8 = e4m3(y * (1 / scale)), to nearest
+ *            (the reciprocal and the product are FP32).
  * The 8-bit form is what w4a16_moe_few_tokens takes with W4A16_DTYPE_FP8.
  *   x        BF16 [rows, hidden], row stride x_stride elements;
  *   residual BF16 [rows, hidden], row stride residual_stride, or NULL;
@@ -502,9 +503,13 @@ size_t w4a16_moe_few_tokens_workspace_size(int tokens, int topk, int hidden, int
  *   out[t, :] = sum over s of topk_weights[t, s] *
  *               (silu(x[t] . Wgate_e^T) * (x[t] . Wup_e^T)) . Wdown_e^T,
  * e = topk_ids[t, s], over the picks of this GPU's experts. Unlike the indexed
- * GEMMs it keeps weights (q - 8) * scale, the activation and every sum in
- * FP32 (no BF16 rounding in between), and adds in an order that depends only
- * on the sizes and the routing: repeated calls give the same bits.
+ * GEMMs it rounds nothing to BF16 in between: sums are FP32, the weights are
+ * (q - 8) times the scale applied in FP32, and the operands of the products
+ * are FP16 numbers times a power of two per block: x exactly down to 2^-28 of
+ * its 128-column block's largest value, the activation in two parts, 22 bits
+ * from its 64-column block's largest. It adds in an order that depends only on
+ * the sizes and the routing: repeated calls give the same bits. An expert's
+ * weights are read once per four of its rows.
  *   packed_gate_up  [num_experts, 2*inter, hidden], W4A16_LAYOUT_KTILE64_GLU16;
  *   packed_down     [num_experts, hidden, inter], W4A16_LAYOUT_KTILE64;
  *   x, x_dtype      BF16 [tokens, hidden] (W4A16_DTYPE_BF16, x_scales NULL), or
@@ -523,7 +528,8 @@ size_t w4a16_moe_few_tokens_workspace_size(int tokens, int topk, int hidden, int
  * topk * hidden * inter < 2^43, tokens <= W4A16_FEW_TOKENS_MAX, topk <= 32
  * (and <= num_global_experts with logits), num_experts and
  * num_global_experts <= 1024 (else W4A16_ERR_UNSUPPORTED); packed weights, x
- * and out 16-byte aligned (else W4A16_ERR_INVALID_ARG); ws_bytes >=
+ * and out 16-byte aligned, the other arrays by their elements (else
+ * W4A16_ERR_INVALID_ARG); ws_bytes >=
  * w4a16_moe_few_tokens_workspace_size(tokens, topk, hidden, inter) (else
  * W4A16_ERR_WORKSPACE). No host synchronisation: graph-capturable. A
  * device-side wait that gives up is reported by w4a16_read_device_status.

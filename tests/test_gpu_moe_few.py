@@ -290,3 +290,33 @@ def test_expired_waits_are_reported_and_the_next_call_is_right(cuda_dev, monkeyp
     assert st == ops.W4A16_ERR_TIMEOUT and 0x1021 <= word <= 0x1025, hex(word)
     monkeypatch.delenv("W4A16_WAIT_TIMEOUT_CYCLES")
     assert torch.equal(_run(p, cuda_dev, packed=packed, ws=ws), want)
+
+
+def test_first_call_inside_a_capture_that_is_never_replayed(cuda_dev):
+    # the layer's workspace is zero from its construction on
+    p = wl.uniform_problem(6, 512, 256, 8, 2, seed=15)
+    gu, dn = _packed(p, cuda_dev)
+    layer = moe_mod.W4A16MoE(
+        moe_mod.PackedExperts(gu, 8, 512, 512, ops.W4A16_LAYOUT_KTILE64_GLU16),
+        moe_mod.PackedExperts(dn, 8, 512, 256), 2, 32, device=cuda_dev)
+    x = bf16_tensor(p.x, cuda_dev)
+    ids, w = dev(p.topk_ids, cuda_dev), dev(p.topk_weights, cuda_dev)
+    out = torch.zeros(6, 512, device=cuda_dev)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.few_tokens(x, ids, w, out=out)
+    assert not layer.few_workspace.any()
+    _close(layer.few_tokens(x, ids, w), oracle.bf16_bits_to_f64(p.x), p.topk_ids, p.topk_weights, p)
+    graph.replay()
+    assert torch.equal(out, layer.few_tokens(x, ids, w))
+
+
+def test_short_weights_and_foreign_workspaces_are_refused(cuda_dev):
+    # on the host: nothing is launched
+    p = wl.uniform_problem(4, 256, 128, 3, 2, seed=5)
+    (gu, dn), ws = _packed(p, cuda_dev), _workspace(p, cuda_dev)
+    for packed, space in (((gu[:-1], dn), ws), ((gu, dn[:-1]), ws), ((gu.cpu(), dn), ws),
+                          ((gu, dn), ws.cpu()), ((gu, dn), ws[:-1]), ((gu, dn), ws[16:])):
+        with pytest.raises(ops.W4A16Error):
+            _run(p, cuda_dev, packed=packed, ws=space)

@@ -94,3 +94,13 @@ def test_tensors_of_the_wrong_kind_are_refused(lib):
         with pytest.raises(ops.W4A16Error):
             ops.w4a16_moe_few_tokens(blob, blob, 8, 256, 128, x_, ids, wt, blob, **kw)
 
+
+def test_few_tokens_alignment(lib):
+    need = ops.w4a16_moe_few_tokens_workspace_size(4, 2, 256, 128)
+    base = dict(xt=ops.W4A16_DTYPE_FP8, xs=P, lg=P, lt=ops.W4A16_DTYPE_F32, ids=P, w=P)
+    for bad in (dict(xs=P + 2), dict(lg=P + 2), dict(lg=P + 1, lt=ops.W4A16_DTYPE_BF16),
+                dict(ids=P + 1), dict(w=P + 2)):
+        a = dict(base, **bad)
+        assert lib.w4a16_moe_few_tokens(P, P, 8, 256, 128, P, a["xt"], a["xs"], 4, 2, a["lg"],
+                                        a["lt"], 16, 1, 0, a["ids"], a["w"], P, 0, P, need,
+                                        None) == INV, bad

@@ -829,11 +829,9 @@ w4a16_status w4a16_add_rms_norm(const uint16_t* x, long long x_stride, const uin
       !aligned16(residual_out) || (reinterpret_cast<uintptr_t>(out_fp8) & 7u) != 0 ||
       (reinterpret_cast<uintptr_t>(scales) & 3u) != 0)
     return W4A16_ERR_INVALID_ARG;
-  const int sms = current_sm_count();
-  if (sms <= 0) return W4A16_ERR_CUDA;
   NormArgs a = {x,    x_stride, residual, residual_stride, weight, eps,      rows,
                 hidden, out,    residual_out, out_fp8,     scales, fp8_group};
-  return cuda_status(launch_add_rms_norm(a, sms, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_add_rms_norm(a, static_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status w4a16_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
@@ -885,6 +883,12 @@ w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed
     return W4A16_ERR_INVALID_ARG;
   if ((x_dtype == W4A16_DTYPE_FP8) != (x_scales != nullptr)) return W4A16_ERR_INVALID_ARG;
   if (!aligned16(packed_gate_up) || !aligned16(packed_down) || !aligned16(x) || !aligned16(out))
+    return W4A16_ERR_INVALID_ARG;
+  const uintptr_t words = reinterpret_cast<uintptr_t>(topk_ids) |
+                          reinterpret_cast<uintptr_t>(topk_weights) |
+                          reinterpret_cast<uintptr_t>(x_scales);
+  if (words % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(logits) % (logits_dtype == W4A16_DTYPE_BF16 ? 2 : 4) != 0)
     return W4A16_ERR_INVALID_ARG;
   if (workspace == nullptr ||
       ws_bytes < w4a16_moe_few_tokens_workspace_size(tokens, topk, hidden, inter))

