@@ -91,6 +91,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int c
       : "memory");
 }
 
+// The same for a CTA pair: bar (address from map_to_cta) may be the other
+// CTA's, dst is this CTA's own memory.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, int col, int row,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(col), "r"(row), "r"(bar)
+      : "memory");
+}
+
 // One box of a 3-D tensor map at (c0, c1, c2).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2,
                                             uint32_t bar) {
@@ -244,7 +255,20 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// The same over a CTA pair (cta_group::2, M = 256): A rows 0..127 from this
+// mma_bf16_ss over a CTA pair (cta_group::2, M = 256): A rows 0..127, B columns
+// 0..N/2-1 and D rows 0..127 lie in this CTA, the rest in the peer, at the same
+// addresses. Issued by the pair's even-ranked CTA.
+__device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// mma_bf16_ts over a CTA pair (cta_group::2, M = 256): A rows 0..127 from this
 // CTA's TMEM and rows 128..255 from the peer's, at the same column address;
 // B columns 0..N/2-1 from this CTA's shared memory and N/2..N-1 from the
 // peer's, at the same address; D rows split like A. Issued by the pair's

@@ -140,7 +140,7 @@ constexpr int kTileM = 128;        // tokens of a tile (MMA M)
 constexpr int kMaxTileN = 256;     // experts of a tile (MMA N)
 constexpr int kMaxSplit = 8;
 constexpr int kMaxRing = 8;
-constexpr int kRingBytes = 200 << 10;
+constexpr int kRingBytes = 224 << 10;
 // Eight epilogue warps, then two that copy and two that issue MMAs, by turns:
 // one thread gets round its loop (wait, copy or multiply, report) only every
 // 600 to 1100 cycles, against 384 of a k step at N = 192 (8192 tokens: 67 us
@@ -162,15 +162,15 @@ struct DenseArgs {
   CUtensorMap x, weight;
   float* logits;
   int tokens, num_experts, k_steps;
-  int tile_n, n_tiles, split, slots, tmem_cols;
+  int tile_n, b_rows, n_tiles, split, slots, tmem_cols;
 };
 
 // Ring slots, a multiple of the threads that take turns: each slot then belongs
 // to one copy and one MMA thread. (In a ring of five a thread could come to a
 // slot two phases ahead of it, which a wait on the phase's parity cannot tell
-// from done.) 4 at N = 256 and 192, up to 8 for narrower tiles.
-int dense_slots(int tile_n) {
-  const int fit = std::min(kMaxRing, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
+// from done.) 8 in a pair at N = 192, 6 at N = 256, 6 or 8 in a split.
+int dense_slots(int b_rows) {
+  const int fit = std::min(kMaxRing, kRingBytes / ((kTileM + b_rows) * kKStep * 2));
   return fit / kDensePairs * kDensePairs;
 }
 // The ring's memory, which the swizzle wants at 1024 bytes, is later the tile's
@@ -180,15 +180,17 @@ __host__ __device__ inline int sum_pitch(int tile_n) { return tile_n + 4; }
 __host__ __device__ inline int tile_sums_bytes(int tile_n) {
   return kTileM * sum_pitch(tile_n) * 4;
 }
-size_t dense_smem(int tile_n, int split) {
-  const size_t ring = static_cast<size_t>(dense_slots(tile_n)) * (kTileM + tile_n) * kKStep * 2;
+size_t dense_smem(int tile_n, int b_rows, int split) {
+  const size_t ring = static_cast<size_t>(dense_slots(b_rows)) * (kTileM + b_rows) * kKStep * 2;
   const size_t sums = static_cast<size_t>(tile_sums_bytes(tile_n)) * (split > 1 ? 2 : 1);
   return 2048 + std::max(ring, sums);
 }
 
+// kRemote: threads of the other CTA of a pair arrive as well.
+template <bool kRemote = false>
 __device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!(kRemote ? mbar_try_wait_cluster_now(bar, parity) : mbar_try_wait(bar, parity))) {
     if (*failed) return false;
     if (clock64() - t0 > kGiveUpCycles) {
       *failed = 1;
@@ -200,8 +202,14 @@ __device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volati
 
 }  // namespace
 
+// kPair: the two CTAs of a cluster multiply a tile of 256 tokens together. Each
+// copies its own 128 tokens and half of the experts, 28 KB a k step at N = 192
+// instead of 40, all copies report to the first CTA, whose MMA threads issue
+// for both, and every CTA keeps the sums of its tokens. Otherwise a.split CTAs
+// of a cluster share a tile of 128 tokens by its columns.
 // A wait that gives up (none does unless the hardware fails) ends the CTA's
 // work in order and leaves NaN in its logits.
+template <bool kPair>
 __global__ void __launch_bounds__(kDenseThreads, 1)
     w4a16_router_dense_kernel(const __grid_constant__ DenseArgs a) {
   extern __shared__ uint8_t raw[];
@@ -215,15 +223,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxRing, done = full + 16 * kMaxRing,
                  drained = done + 8 * kDensePairs, received = drained + 8 * kDensePairs;
   const uint32_t ring = smem_u32(smem);
-  const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.tile_n) * kKStep * 2;
+  const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.b_rows) * kKStep * 2;
   const uint32_t slot_bytes = a_bytes + b_bytes;
-  const int rank = static_cast<int>(blockIdx.x) % a.split;
-  const int tile = static_cast<int>(blockIdx.x) / a.split;
-  const int m0 = tile / a.n_tiles * kTileM, n0 = tile % a.n_tiles * a.tile_n;
-  const int k0 = a.k_steps * rank / a.split, k1 = a.k_steps * (rank + 1) / a.split;
+  const int ctas = kPair ? 2 : a.split;  // of a tile
+  const int rank = static_cast<int>(blockIdx.x) % ctas;
+  const int tile = static_cast<int>(blockIdx.x) / ctas;
+  const int m0 = (kPair ? tile / a.n_tiles * 2 + rank : tile / a.n_tiles) * kTileM;
+  const int n0 = tile % a.n_tiles * a.tile_n;
+  const int k0 = kPair ? 0 : a.k_steps * rank / a.split;
+  const int k1 = kPair ? a.k_steps : a.k_steps * (rank + 1) / a.split;
   if (warp == kWarpMma0) {
-    tmem_alloc(smem_u32(&tmem_at), static_cast<uint32_t>(a.tmem_cols));
-    tmem_relinquish();
     if (lane == 0) {
       for (int i = 0; i < a.slots; ++i) {
         mbar_init(full + 8 * i, 1);
@@ -231,15 +240,24 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       }
       for (int i = 0; i < kDensePairs; ++i) {
         mbar_init(done + 8 * i, 1);
-        mbar_init(drained + 8 * i, kSumWarps);
+        mbar_init(drained + 8 * i, kPair ? 2 * kSumWarps : kSumWarps);
       }
       mbar_init(received, 1);
       *failed = 0;
       fence_mbar_init();
     }
+    __syncwarp();
+    if constexpr (kPair) {
+      tmem_alloc_pair(smem_u32(&tmem_at), static_cast<uint32_t>(a.tmem_cols));
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&tmem_at), static_cast<uint32_t>(a.tmem_cols));
+      tmem_relinquish();
+    }
     tc_fence_before();
   }
   __syncthreads();
+  if constexpr (kPair) cluster_sync_all();  // the other's barriers and TMEM are there
   tc_fence_after();
   grid_dependency_wait();
   grid_dependents_go();
@@ -254,12 +272,19 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int slot = issued % a.slots, k = k0 + issued;
         ok = dense_wait(empty + 8 * slot, (issued / a.slots & 1) ^ 1, failed);
         if (!ok) break;
-        mbar_arrive_expect_tx(full + 8 * slot, slot_bytes);
-        tma_load_2d(ring + slot * slot_bytes, &a.x, k * kKStep, m0, full + 8 * slot);
-        tma_load_2d(ring + slot * slot_bytes + a_bytes, &a.weight, k * kKStep, n0,
-                    full + 8 * slot);
+        const uint32_t to = ring + slot * slot_bytes;
+        if constexpr (kPair) {
+          const uint32_t bar = map_to_cta(full + 8 * slot, 0);
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * slot, 2 * slot_bytes);
+          tma_load_2d_pair(to, &a.x, k * kKStep, m0, bar);
+          tma_load_2d_pair(to + a_bytes, &a.weight, k * kKStep, n0 + rank * a.b_rows, bar);
+        } else {
+          mbar_arrive_expect_tx(full + 8 * slot, slot_bytes);
+          tma_load_2d(to, &a.x, k * kKStep, m0, full + 8 * slot);
+          tma_load_2d(to + a_bytes, &a.weight, k * kKStep, n0, full + 8 * slot);
+        }
       }
-      if (!ok)  // copies in flight land before the CTA ends
+      if (!ok && (!kPair || rank == 0))  // copies in flight land before the CTAs end
         for (int i = first; i < issued; i += kDensePairs) {
           if (i < issued - a.slots) continue;
           const long long t0 = clock64();
@@ -270,28 +295,42 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     }
   } else if (warp >= kWarpMma0) {
     // each into an accumulator of its own
-    if (lane == 0) {
+    if (lane == 0 && (!kPair || rank == 0)) {
+      const auto report = [](uint32_t bar) {
+        if constexpr (kPair)
+          tc_commit_pair_mc(bar, 3);
+        else
+          tc_commit(bar);
+      };
       const int first = warp - kWarpMma0;
       const uint32_t d = tmem + static_cast<uint32_t>(first * a.tmem_cols / kDensePairs);
-      const uint32_t idesc = idesc_bf16_m128(static_cast<uint32_t>(a.tile_n));
+      const uint32_t idesc = idesc_bf16(kPair ? 2 * kTileM : kTileM, static_cast<uint32_t>(a.tile_n));
+      bool ok = true;
       int n = 0;  // steps of this thread
       for (int i = first; k0 + i < k1; i += kDensePairs, ++n) {
         const int slot = i % a.slots;
         if (n > 0 && n % kChunk == 0) {
-          tc_commit(done + 8 * first);
-          if (!dense_wait(drained + 8 * first, (n / kChunk - 1) & 1, failed)) break;
+          report(done + 8 * first);
+          ok = dense_wait<kPair>(drained + 8 * first, (n / kChunk - 1) & 1, failed);
+          if (!ok) break;
           tc_fence_after();
         }
-        if (!dense_wait(full + 8 * slot, i / a.slots & 1, failed)) break;
+        ok = dense_wait(full + 8 * slot, i / a.slots & 1, failed);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t ad = smem_desc_sw128_kmajor(ring + slot * slot_bytes);
         const uint64_t bd = smem_desc_sw128_kmajor(ring + slot * slot_bytes + a_bytes);
 #pragma unroll
-        for (int j = 0; j < kKStep / 16; ++j)  // 32 bytes further along k
-          mma_bf16_ss(d, ad + 2 * j, bd + 2 * j, idesc, n % kChunk != 0 || j > 0);
-        tc_commit(empty + 8 * slot);
+        for (int j = 0; j < kKStep / 16; ++j) {  // 32 bytes further along k
+          const uint32_t add = n % kChunk != 0 || j > 0;
+          if constexpr (kPair)
+            mma_bf16_ss_pair(d, ad + 2 * j, bd + 2 * j, idesc, add);
+          else
+            mma_bf16_ss(d, ad + 2 * j, bd + 2 * j, idesc, add);
+        }
+        report(empty + 8 * slot);
       }
-      if (n > 0) tc_commit(done + 8 * first);
+      if (n > 0 && ok) report(done + 8 * first);
     }
   } else {
     // lane + 32 (warp % 4) = token of the tile, half of the experts; in the end
@@ -321,7 +360,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(drained + 8 * j);
+        if (lane == 0) {
+          if constexpr (kPair)
+            mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * j, 0));
+          else
+            mbar_arrive(drained + 8 * j);
+        }
       }
       if (!any) break;
     }
@@ -337,15 +381,20 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                              __uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
     fence_proxy_async_smem();  // a bulk copy sends them on
   }
+  tc_fence_before();
+  __syncwarp();
   __syncthreads();
+  if constexpr (kPair) cluster_sync_all();  // nothing reaches across any more
   if (warp == kWarpMma0) {
-    __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, static_cast<uint32_t>(a.tmem_cols));
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, static_cast<uint32_t>(a.tmem_cols));
+    else
+      tmem_dealloc(tmem, static_cast<uint32_t>(a.tmem_cols));
   }
   // a split: every CTA finishes a share of the tokens, whose sums the others
   // send it, one bulk copy each
-  const int rows = kTileM / a.split, pitch = sum_pitch(a.tile_n);
+  const int rows = kPair ? kTileM : kTileM / a.split, pitch = sum_pitch(a.tile_n);
   const uint32_t share = static_cast<uint32_t>(rows * pitch * 4);
   const uint32_t inbox = ring + static_cast<uint32_t>(tile_sums_bytes(a.tile_n));
   bool whole = true;
@@ -366,7 +415,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const float* others = reinterpret_cast<const float*>(smem + (inbox - ring));
   const int n_end = min(a.tile_n, a.num_experts - n0);
   for (int r = warp; r < rows; r += kDenseThreads / 32) {
-    const int m = rank * rows + r;
+    const int m = kPair ? r : rank * rows + r;
     if (m0 + m >= a.tokens) break;
     float* out = a.logits + static_cast<long long>(m0 + m) * a.num_experts + n0;
     if (a.split == 1) {
@@ -402,31 +451,34 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
   a.tokens = tokens;
   a.num_experts = num_experts;
   a.k_steps = packed_ksteps(hidden);
-  // tiles as wide as can be; narrower ones where these leave half the SMs idle,
-  // and then as many CTAs on the columns of a tile as there are SMs for, with
-  // at least four k steps each
+  // tiles as wide as can be, of 256 tokens by two CTAs; narrower ones of 128
+  // where these would leave half the SMs idle, and then as many CTAs on the
+  // columns of a tile as there are SMs for, with at least four k steps each
   const int m_tiles = ceil_div(tokens, kTileM);
   a.n_tiles = ceil_div(num_experts, kMaxTileN);
-  const bool narrow = static_cast<long long>(m_tiles) * a.n_tiles * 2 <= sms;
-  if (narrow) a.n_tiles = ceil_div(num_experts, kSplitTileN);
-  a.tile_n = std::max(16, ceil_div(ceil_div(num_experts, a.n_tiles), 16) * 16);
-  a.slots = dense_slots(a.tile_n);
+  const bool pair = static_cast<long long>(m_tiles) * a.n_tiles * 2 > sms;
+  if (!pair) a.n_tiles = ceil_div(num_experts, kSplitTileN);
+  const int step = pair ? 32 : 16;  // of an MMA's N
+  a.tile_n = ceil_div(ceil_div(num_experts, a.n_tiles), step) * step;
+  a.b_rows = pair ? a.tile_n / 2 : a.tile_n;
+  a.slots = dense_slots(a.b_rows);
   a.tmem_cols = 32;
   while (a.tmem_cols < a.tile_n * kDensePairs) a.tmem_cols *= 2;
-  const long long tiles = static_cast<long long>(m_tiles) * a.n_tiles;
+  const long long tiles = static_cast<long long>(pair ? ceil_div(m_tiles, 2) : m_tiles) * a.n_tiles;
   a.split = 1;
-  while (narrow && a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.k_steps / (a.split * 2) >= 4)
+  while (!pair && a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.k_steps / (a.split * 2) >= 4)
     a.split *= 2;
   if (!encode_rows_tmap(&a.x, x, tokens, hidden, x_stride, kTileM) ||
-      !encode_rows_tmap(&a.weight, weight, num_experts, hidden, hidden, a.tile_n))
+      !encode_rows_tmap(&a.weight, weight, num_experts, hidden, hidden, a.b_rows))
     return cudaErrorInvalidValue;
-  if (tiles * a.split > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const size_t smem = dense_smem(a.tile_n, a.split);
+  const int ctas = pair ? 2 : a.split;
+  if (tiles * ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const auto kernel = pair ? w4a16_router_dense_kernel<true> : w4a16_router_dense_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(
-      w4a16_router_dense_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 2048);
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 2048);
   if (e != cudaSuccess) return e;
-  return launch_dependent(w4a16_router_dense_kernel, static_cast<int>(tiles * a.split),
-                          kDenseThreads, smem, a.split, stream, a);
+  return launch_dependent(kernel, static_cast<int>(tiles * ctas), kDenseThreads,
+                          dense_smem(a.tile_n, a.b_rows, a.split), ctas, stream, a);
 }
 
 }  // namespace w4a16
