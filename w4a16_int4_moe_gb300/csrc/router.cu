@@ -151,26 +151,28 @@ constexpr int kDenseThreads = 32 * (kSumWarps + 2 * kDensePairs);
 constexpr int kWarpCopy0 = kSumWarps, kWarpMma0 = kSumWarps + kDensePairs;
 // The tensor core cuts its sums off instead of rounding them, which over the
 // 224 additions that 7168 columns are to each of two accumulators came to
-// 3.8e-6 of the logits. So after eight k steps (32 additions) an MMA thread
+// 3.8e-6 of the logits. So after 512 columns (32 additions) an MMA thread
 // hands its accumulator to the epilogue warps, which add it to FP32 sums in
 // registers, and begins at zero: 4.8e-7, for 2 us of 50.
-constexpr int kChunk = 8;
+constexpr int kChunk = 8;  // times kKStep columns
 constexpr int kSplitTileN = 128;   // of a tile whose columns are split
 constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
 
 struct DenseArgs {
   CUtensorMap x, weight;
   float* logits;
-  int tokens, num_experts, k_steps;
+  int tokens, num_experts;
+  int k_steps, sub;  // steps of sub * kKStep columns
   int tile_n, b_rows, n_tiles, split, slots, tmem_cols;
 };
 
 // Ring slots, a multiple of the threads that take turns: each slot then belongs
 // to one copy and one MMA thread. (In a ring of five a thread could come to a
 // slot two phases ahead of it, which a wait on the phase's parity cannot tell
-// from done.) 8 in a pair at N = 192, 6 at N = 256, 6 or 8 in a split.
-int dense_slots(int b_rows) {
-  const int fit = std::min(kMaxRing, kRingBytes / ((kTileM + b_rows) * kKStep * 2));
+// from done.) 4 of 128 columns in a pair at N = 192, 6 of 64 at N = 256, 6 or 8
+// of 64 in a split.
+int dense_slots(int b_rows, int sub) {
+  const int fit = std::min(kMaxRing, kRingBytes / ((kTileM + b_rows) * sub * kKStep * 2));
   return fit / kDensePairs * kDensePairs;
 }
 // The ring's memory, which the swizzle wants at 1024 bytes, is later the tile's
@@ -180,9 +182,9 @@ __host__ __device__ inline int sum_pitch(int tile_n) { return tile_n + 4; }
 __host__ __device__ inline int tile_sums_bytes(int tile_n) {
   return kTileM * sum_pitch(tile_n) * 4;
 }
-size_t dense_smem(int tile_n, int b_rows, int split) {
-  const size_t ring = static_cast<size_t>(dense_slots(b_rows)) * (kTileM + b_rows) * kKStep * 2;
-  const size_t sums = static_cast<size_t>(tile_sums_bytes(tile_n)) * (split > 1 ? 2 : 1);
+size_t dense_smem(const DenseArgs& a) {
+  const size_t ring = static_cast<size_t>(a.slots) * (kTileM + a.b_rows) * a.sub * kKStep * 2;
+  const size_t sums = static_cast<size_t>(tile_sums_bytes(a.tile_n)) * (a.split > 1 ? 2 : 1);
   return 2048 + std::max(ring, sums);
 }
 
@@ -224,8 +226,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                  drained = done + 8 * kDensePairs, received = drained + 8 * kDensePairs;
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.b_rows) * kKStep * 2;
-  const uint32_t slot_bytes = a_bytes + b_bytes;
+  const uint32_t sub_bytes = a_bytes + b_bytes, slot_bytes = sub_bytes * a.sub;
   const int ctas = kPair ? 2 : a.split;  // of a tile
+  const int chunk = kChunk / a.sub;
   const int rank = static_cast<int>(blockIdx.x) % ctas;
   const int tile = static_cast<int>(blockIdx.x) / ctas;
   const int m0 = (kPair ? tile / a.n_tiles * 2 + rank : tile / a.n_tiles) * kTileM;
@@ -272,16 +275,19 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int slot = issued % a.slots, k = k0 + issued;
         ok = dense_wait(empty + 8 * slot, (issued / a.slots & 1) ^ 1, failed);
         if (!ok) break;
-        const uint32_t to = ring + slot * slot_bytes;
-        if constexpr (kPair) {
-          const uint32_t bar = map_to_cta(full + 8 * slot, 0);
-          if (rank == 0) mbar_arrive_expect_tx(full + 8 * slot, 2 * slot_bytes);
-          tma_load_2d_pair(to, &a.x, k * kKStep, m0, bar);
-          tma_load_2d_pair(to + a_bytes, &a.weight, k * kKStep, n0 + rank * a.b_rows, bar);
-        } else {
-          mbar_arrive_expect_tx(full + 8 * slot, slot_bytes);
-          tma_load_2d(to, &a.x, k * kKStep, m0, full + 8 * slot);
-          tma_load_2d(to + a_bytes, &a.weight, k * kKStep, n0, full + 8 * slot);
+        if (!kPair || rank == 0)
+          mbar_arrive_expect_tx(full + 8 * slot, kPair ? 2 * slot_bytes : slot_bytes);
+        for (int j = 0; j < a.sub; ++j) {
+          const uint32_t to = ring + slot * slot_bytes + j * sub_bytes;
+          const int column = (k * a.sub + j) * kKStep;
+          if constexpr (kPair) {
+            const uint32_t bar = map_to_cta(full + 8 * slot, 0);
+            tma_load_2d_pair(to, &a.x, column, m0, bar);
+            tma_load_2d_pair(to + a_bytes, &a.weight, column, n0 + rank * a.b_rows, bar);
+          } else {
+            tma_load_2d(to, &a.x, column, m0, full + 8 * slot);
+            tma_load_2d(to + a_bytes, &a.weight, column, n0, full + 8 * slot);
+          }
         }
       }
       if (!ok && (!kPair || rank == 0))  // copies in flight land before the CTAs end
@@ -309,24 +315,27 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       int n = 0;  // steps of this thread
       for (int i = first; k0 + i < k1; i += kDensePairs, ++n) {
         const int slot = i % a.slots;
-        if (n > 0 && n % kChunk == 0) {
+        if (n > 0 && n % chunk == 0) {
           report(done + 8 * first);
-          ok = dense_wait<kPair>(drained + 8 * first, (n / kChunk - 1) & 1, failed);
+          ok = dense_wait<kPair>(drained + 8 * first, (n / chunk - 1) & 1, failed);
           if (!ok) break;
           tc_fence_after();
         }
         ok = dense_wait(full + 8 * slot, i / a.slots & 1, failed);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ad = smem_desc_sw128_kmajor(ring + slot * slot_bytes);
-        const uint64_t bd = smem_desc_sw128_kmajor(ring + slot * slot_bytes + a_bytes);
+        for (int u = 0; u < a.sub; ++u) {
+          const uint32_t from = ring + slot * slot_bytes + u * sub_bytes;
+          const uint64_t ad = smem_desc_sw128_kmajor(from);
+          const uint64_t bd = smem_desc_sw128_kmajor(from + a_bytes);
 #pragma unroll
-        for (int j = 0; j < kKStep / 16; ++j) {  // 32 bytes further along k
-          const uint32_t add = n % kChunk != 0 || j > 0;
-          if constexpr (kPair)
-            mma_bf16_ss_pair(d, ad + 2 * j, bd + 2 * j, idesc, add);
-          else
-            mma_bf16_ss(d, ad + 2 * j, bd + 2 * j, idesc, add);
+          for (int j = 0; j < kKStep / 16; ++j) {  // 32 bytes further along k
+            const uint32_t add = n % chunk != 0 || u > 0 || j > 0;
+            if constexpr (kPair)
+              mma_bf16_ss_pair(d, ad + 2 * j, bd + 2 * j, idesc, add);
+            else
+              mma_bf16_ss(d, ad + 2 * j, bd + 2 * j, idesc, add);
+          }
         }
         report(empty + 8 * slot);
       }
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       bool any = false;
       for (int j = 0; j < kDensePairs && ok; ++j) {
         // chunk c of MMA thread j, which has the steps j, j + kDensePairs, ...
-        if (j + c * kChunk * kDensePairs >= k1 - k0) continue;
+        if (j + c * chunk * kDensePairs >= k1 - k0) continue;
         any = true;
         ok = __all_sync(0xffffffffu, dense_wait(done + 8 * j, c & 1, failed));
         if (!ok) break;
@@ -450,7 +459,6 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
   a.logits = logits;
   a.tokens = tokens;
   a.num_experts = num_experts;
-  a.k_steps = packed_ksteps(hidden);
   // tiles as wide as can be, of 256 tokens by two CTAs; narrower ones of 128
   // where these would leave half the SMs idle, and then as many CTAs on the
   // columns of a tile as there are SMs for, with at least four k steps each
@@ -461,7 +469,11 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
   const int step = pair ? 32 : 16;  // of an MMA's N
   a.tile_n = ceil_div(ceil_div(num_experts, a.n_tiles), step) * step;
   a.b_rows = pair ? a.tile_n / 2 : a.tile_n;
-  a.slots = dense_slots(a.b_rows);
+  // 128 columns a step where four fit: the copy and MMA threads get round their
+  // loops fast enough then (8192 tokens x 384 experts: 42 us with 64 columns)
+  a.sub = pair && dense_slots(a.b_rows, 2) >= 4 ? 2 : 1;
+  a.k_steps = ceil_div(hidden, a.sub * kKStep);
+  a.slots = dense_slots(a.b_rows, a.sub);
   a.tmem_cols = 32;
   while (a.tmem_cols < a.tile_n * kDensePairs) a.tmem_cols *= 2;
   const long long tiles = static_cast<long long>(pair ? ceil_div(m_tiles, 2) : m_tiles) * a.n_tiles;
@@ -478,7 +490,7 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 2048);
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, static_cast<int>(tiles * ctas), kDenseThreads,
-                          dense_smem(a.tile_n, a.b_rows, a.split), ctas, stream, a);
+                          dense_smem(a), ctas, stream, a);
 }
 
 }  // namespace w4a16
