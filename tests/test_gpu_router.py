@@ -80,3 +80,18 @@ def test_in_a_graph_on_a_side_stream(cuda_dev):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("tokens,hidden,experts,pitch", [
+    # pairs of CTAs, their columns split by four, by two and not at all, with a
+    # last pair of one CTA's tokens, a last step outside the columns, padding
+    (1500, 7168, 384, 0), (1450, 2056, 250, 2064), (3000, 4104, 384, 0), (4096, 7168, 384, 0),
+    (2100, 7168, 64, 0), (6000, 520, 383, 528), (8100, 136, 70, 0), (700, 7168, 384, 0),
+])
+def test_router_many_tokens(cuda_dev, tokens, hidden, experts, pitch):
+    x, w = _inputs(tokens, hidden, experts, cuda_dev, pitch, tokens)
+    g = Guarded((tokens, experts), torch.float32, cuda_dev)
+    ops.w4a16_router_logits(x, w, out=g.t)
+    g.check("logits")
+    _check(g.t, x, w)
+    assert torch.equal(ops.w4a16_router_logits(x, w), g.t)

@@ -9,22 +9,26 @@
 //     a part of the weight at once; m16n8k16 MMAs straight from global memory
 //     (no operand is used twice by an SM), partial sums joined through the
 //     cluster's shared memory;
-//   * more: a dense product on tcgen05, 128 tokens x up to 256 experts a tile,
-//     both operands by TMA, accumulators in TMEM. Where the tiles are fewer
-//     than the SMs, a cluster of up to eight CTAs splits the columns of one.
+//   * more: a dense product on tcgen05, 128 tokens (256 of a CTA pair) x up to
+//     256 experts a tile, both operands by TMA, accumulators in TMEM. Where the
+//     tiles are fewer than the SMs, a cluster of up to eight CTAs splits the
+//     columns of one.
 //
 // The order of the additions follows from the sizes alone.
 //
 // 384 experts of hidden 7168, in a graph: 1 token 3.2 us, 48 tokens 6.5 us, both
 // latency (launch, one round of loads, the cluster's exchange; the weight alone
-// is 0.8 us of the copy rate). 8192 tokens: 50 us, 0.9 PFLOP/s, 0.47 of a
-// library product's rate: bound by the operands' way from L2 into the ring
-// (40 KB a k step and SM; the tensor cores work 37 per cent of the time).
+// is 0.8 us of the copy rate). 8192 tokens: 41 us, 1.1 PFLOP/s, 0.57 of a
+// library product's rate, on 128 of 152 SMs: 7 us are launch, first loads and
+// the logits' way out, the rest is bound by the operands' way into an SM
+// (28 KB of 64 columns at 50 bytes a cycle, against 384 cycles of MMAs).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -155,7 +159,6 @@ constexpr int kWarpCopy0 = kSumWarps, kWarpMma0 = kSumWarps + kDensePairs;
 // hands its accumulator to the epilogue warps, which add it to FP32 sums in
 // registers, and begins at zero: 4.8e-7, for 2 us of 50.
 constexpr int kChunk = 8;  // times kKStep columns
-constexpr int kSplitTileN = 128;   // of a tile whose columns are split
 constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
 
 struct DenseArgs {
@@ -204,11 +207,11 @@ __device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volati
 
 }  // namespace
 
-// kPair: the two CTAs of a cluster multiply a tile of 256 tokens together. Each
-// copies its own 128 tokens and half of the experts, 28 KB a k step at N = 192
-// instead of 40, all copies report to the first CTA, whose MMA threads issue
-// for both, and every CTA keeps the sums of its tokens. Otherwise a.split CTAs
-// of a cluster share a tile of 128 tokens by its columns.
+// kPair: two CTAs multiply a tile of 256 tokens together. Each copies its own
+// 128 tokens and half of the experts, 28 KB of 64 columns at N = 192 instead of
+// 40, all copies report to the first CTA, whose MMA threads issue for both, and
+// every CTA keeps the sums of its tokens. Otherwise a tile has 128 tokens and
+// one CTA. a.split CTAs or pairs of a cluster share a tile by its columns.
 // A wait that gives up (none does unless the hardware fails) ends the CTA's
 // work in order and leaves NaN in its logits.
 template <bool kPair>
@@ -227,14 +230,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.b_rows) * kKStep * 2;
   const uint32_t sub_bytes = a_bytes + b_bytes, slot_bytes = sub_bytes * a.sub;
-  const int ctas = kPair ? 2 : a.split;  // of a tile
+  const int ctas = (kPair ? 2 : 1) * a.split;  // of a tile
+  const int id = static_cast<int>(blockIdx.x) % ctas;  // in the cluster
+  const int half = kPair ? id & 1 : 0, rank = kPair ? id >> 1 : id;  // of the tokens, columns
+  const uint32_t leader = static_cast<uint32_t>(kPair ? id & ~1 : id);
   const int chunk = kChunk / a.sub;
-  const int rank = static_cast<int>(blockIdx.x) % ctas;
   const int tile = static_cast<int>(blockIdx.x) / ctas;
-  const int m0 = (kPair ? tile / a.n_tiles * 2 + rank : tile / a.n_tiles) * kTileM;
+  const int m0 = (kPair ? tile / a.n_tiles * 2 + half : tile / a.n_tiles) * kTileM;
   const int n0 = tile % a.n_tiles * a.tile_n;
-  const int k0 = kPair ? 0 : a.k_steps * rank / a.split;
-  const int k1 = kPair ? a.k_steps : a.k_steps * (rank + 1) / a.split;
+  const int k0 = a.k_steps * rank / a.split, k1 = a.k_steps * (rank + 1) / a.split;
   if (warp == kWarpMma0) {
     if (lane == 0) {
       for (int i = 0; i < a.slots; ++i) {
@@ -275,22 +279,22 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int slot = issued % a.slots, k = k0 + issued;
         ok = dense_wait(empty + 8 * slot, (issued / a.slots & 1) ^ 1, failed);
         if (!ok) break;
-        if (!kPair || rank == 0)
+        if (half == 0)
           mbar_arrive_expect_tx(full + 8 * slot, kPair ? 2 * slot_bytes : slot_bytes);
         for (int j = 0; j < a.sub; ++j) {
           const uint32_t to = ring + slot * slot_bytes + j * sub_bytes;
           const int column = (k * a.sub + j) * kKStep;
           if constexpr (kPair) {
-            const uint32_t bar = map_to_cta(full + 8 * slot, 0);
+            const uint32_t bar = map_to_cta(full + 8 * slot, leader);
             tma_load_2d_pair(to, &a.x, column, m0, bar);
-            tma_load_2d_pair(to + a_bytes, &a.weight, column, n0 + rank * a.b_rows, bar);
+            tma_load_2d_pair(to + a_bytes, &a.weight, column, n0 + half * a.b_rows, bar);
           } else {
             tma_load_2d(to, &a.x, column, m0, full + 8 * slot);
             tma_load_2d(to + a_bytes, &a.weight, column, n0, full + 8 * slot);
           }
         }
       }
-      if (!ok && (!kPair || rank == 0))  // copies in flight land before the CTAs end
+      if (!ok && half == 0)  // copies in flight land before the CTAs end
         for (int i = first; i < issued; i += kDensePairs) {
           if (i < issued - a.slots) continue;
           const long long t0 = clock64();
@@ -301,10 +305,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     }
   } else if (warp >= kWarpMma0) {
     // each into an accumulator of its own
-    if (lane == 0 && (!kPair || rank == 0)) {
-      const auto report = [](uint32_t bar) {
+    if (lane == 0 && half == 0) {
+      const auto report = [&](uint32_t bar) {
         if constexpr (kPair)
-          tc_commit_pair_mc(bar, 3);
+          tc_commit_pair_mc(bar, static_cast<uint16_t>(3u << leader));
         else
           tc_commit(bar);
       };
@@ -344,8 +348,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   } else {
     // lane + 32 (warp % 4) = token of the tile, half of the experts; in the end
     // the sums take the ring's place
-    const int half = (a.tile_n / 2 + 15) / 16 * 16;
-    const int c0 = warp < 4 ? 0 : half, cols = warp < 4 ? half : a.tile_n - half;
+    const int left = (a.tile_n / 2 + 15) / 16 * 16;
+    const int c0 = warp < 4 ? 0 : left, cols = warp < 4 ? left : a.tile_n - left;
     const uint32_t at = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + c0;
     float sum[kMaxTileN / 2] = {};
     bool ok = true;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if constexpr (kPair)
-            mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * j, 0));
+            mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * j, leader));
           else
             mbar_arrive(drained + 8 * j);
         }
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   }
   // a split: every CTA finishes a share of the tokens, whose sums the others
   // send it, one bulk copy each
-  const int rows = kPair ? kTileM : kTileM / a.split, pitch = sum_pitch(a.tile_n);
+  const int rows = kTileM / a.split, pitch = sum_pitch(a.tile_n);
   const uint32_t share = static_cast<uint32_t>(rows * pitch * 4);
   const uint32_t inbox = ring + static_cast<uint32_t>(tile_sums_bytes(a.tile_n));
   bool whole = true;
@@ -411,11 +415,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     if (threadIdx.x == 0) mbar_arrive_expect_tx(received, share * (a.split - 1));
     cluster_sync_all();  // everybody's ring is done with, and expects
     if (static_cast<int>(threadIdx.x) < a.split && static_cast<int>(threadIdx.x) != rank) {
-      const uint32_t to = threadIdx.x;
+      const uint32_t to = threadIdx.x, cta = kPair ? 2 * to + half : to;
       asm volatile(
           "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes "
-          "[%0], [%1], %2, [%3];" ::"r"(map_to_cta(inbox + rank * share, to)),
-          "r"(ring + to * share), "r"(share), "r"(map_to_cta(received, to))
+          "[%0], [%1], %2, [%3];" ::"r"(map_to_cta(inbox + rank * share, cta)),
+          "r"(ring + to * share), "r"(share), "r"(map_to_cta(received, cta))
           : "memory");
     }
     whole = dense_wait(received, 0, failed);
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const float* others = reinterpret_cast<const float*>(smem + (inbox - ring));
   const int n_end = min(a.tile_n, a.num_experts - n0);
   for (int r = warp; r < rows; r += kDenseThreads / 32) {
-    const int m = kPair ? r : rank * rows + r;
+    const int m = rank * rows + r;
     if (m0 + m >= a.tokens) break;
     float* out = a.logits + static_cast<long long>(m0 + m) * a.num_experts + n0;
     if (a.split == 1) {
@@ -442,6 +446,81 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   if (a.split > 1) cluster_sync_all();  // the sums stay until all are sent
 }
 
+namespace {
+
+// How many clusters of `ctas` run at once with one CTA an SM: clusters stay
+// inside a GPC, so eights leave some SMs out.
+int clusters_at_once(int ctas, int sms) {
+  static std::atomic<int> known[kMaxSplit + 1];
+  if (ctas == 1) return sms;
+  if (const int n = known[ctas]) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas * sms));
+  cfg.blockDim = dim3(kDenseThreads);
+  cfg.dynamicSmemBytes = kRingBytes + 2048;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(w4a16_router_dense_kernel<false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kRingBytes + 2048) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, w4a16_router_dense_kernel<false>, &cfg) != cudaSuccess ||
+      n <= 0)
+    n = std::max(1, sms / (2 * ctas));
+  known[ctas] = n;
+  return n;
+}
+
+// The fastest shape by an estimate in cycles: waves of clusters, each a CTA's
+// steps at the rate at which an SM takes operands from L2 (50 bytes a cycle
+// were measured) or at which the threads get round their loops, plus the
+// tile's sums on their way out. Against every shape timed (65 to 8192 tokens of
+// six weights) the choice is within 2 per cent of the fastest in the mean, 11
+// at most; hidden 7168 x 384 experts, us: 777 tokens 18 (a pair of 128 experts, split by 4: 17; one
+// CTA, split by 4: 19), 4096 tokens 29 (pairs unsplit 36, one CTA 34), 8192
+// tokens 41 (one CTA 54).
+bool dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a) {
+  bool best_pair = false;
+  double best = 0;
+  for (int pair = 0; pair < 2; ++pair)
+    for (int width = 64; width <= kMaxTileN; width += 64) {
+      DenseArgs c = {};
+      const int step = pair ? 32 : 16;  // of an MMA's N
+      c.n_tiles = ceil_div(num_experts, width);
+      c.tile_n = ceil_div(ceil_div(num_experts, c.n_tiles), step) * step;
+      c.b_rows = pair ? c.tile_n / 2 : c.tile_n;
+      // 128 columns a step where four fit
+      c.sub = pair && dense_slots(c.b_rows, 2) >= 4 ? 2 : 1;
+      c.k_steps = ceil_div(hidden, c.sub * kKStep);
+      c.slots = dense_slots(c.b_rows, c.sub);
+      c.tmem_cols = 32;
+      while (c.tmem_cols < c.tile_n * kDensePairs) c.tmem_cols *= 2;
+      const double step_cycles =
+          std::max(c.sub * (kTileM + c.b_rows) * kKStep * 2 / 50.0, c.sub == 1 ? 510.0 : 880.0);
+      const double tiles =
+          static_cast<double>(ceil_div(tokens, pair ? 2 * kTileM : kTileM)) * c.n_tiles;
+      for (c.split = 1; c.split * (pair ? 2 : 1) <= kMaxSplit && c.split <= c.k_steps; c.split *= 2) {
+        if (c.split > 1 && 2 * tile_sums_bytes(c.tile_n) > kRingBytes) break;
+        const int ctas = c.split * (pair ? 2 : 1);
+        const double waves = std::ceil(tiles / clusters_at_once(ctas, sms));
+        const double cost = waves * (ceil_div(c.k_steps, c.split) * step_cycles + 3000 +
+                                     c.tile_n * 28 + (c.split > 1 ? 4500 : 0));
+        if (best == 0 || cost < best) {
+          best = cost;
+          best_pair = pair != 0;
+          *a = c;
+        }
+      }
+    }
+  return best_pair;
+}
+
+}  // namespace
+
 cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
                                  int tokens, int hidden, int num_experts, float* logits, int sms,
                                  cudaStream_t stream) {
@@ -456,41 +535,23 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
     return run(w4a16_router_few_kernel<kFewBlock / 8>);
   }
   DenseArgs a;
+  const bool pair = dense_shape(tokens, num_experts, hidden, sms, &a);
   a.logits = logits;
   a.tokens = tokens;
   a.num_experts = num_experts;
-  // tiles as wide as can be, of 256 tokens by two CTAs; narrower ones of 128
-  // where these would leave half the SMs idle, and then as many CTAs on the
-  // columns of a tile as there are SMs for, with at least four k steps each
-  const int m_tiles = ceil_div(tokens, kTileM);
-  a.n_tiles = ceil_div(num_experts, kMaxTileN);
-  const bool pair = static_cast<long long>(m_tiles) * a.n_tiles * 2 > sms;
-  if (!pair) a.n_tiles = ceil_div(num_experts, kSplitTileN);
-  const int step = pair ? 32 : 16;  // of an MMA's N
-  a.tile_n = ceil_div(ceil_div(num_experts, a.n_tiles), step) * step;
-  a.b_rows = pair ? a.tile_n / 2 : a.tile_n;
-  // 128 columns a step where four fit: the copy and MMA threads get round their
-  // loops fast enough then (8192 tokens x 384 experts: 42 us with 64 columns)
-  a.sub = pair && dense_slots(a.b_rows, 2) >= 4 ? 2 : 1;
-  a.k_steps = ceil_div(hidden, a.sub * kKStep);
-  a.slots = dense_slots(a.b_rows, a.sub);
-  a.tmem_cols = 32;
-  while (a.tmem_cols < a.tile_n * kDensePairs) a.tmem_cols *= 2;
-  const long long tiles = static_cast<long long>(pair ? ceil_div(m_tiles, 2) : m_tiles) * a.n_tiles;
-  a.split = 1;
-  while (!pair && a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.k_steps / (a.split * 2) >= 4)
-    a.split *= 2;
   if (!encode_rows_tmap(&a.x, x, tokens, hidden, x_stride, kTileM) ||
       !encode_rows_tmap(&a.weight, weight, num_experts, hidden, hidden, a.b_rows))
     return cudaErrorInvalidValue;
-  const int ctas = pair ? 2 : a.split;
-  if (tiles * ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int ctas = (pair ? 2 : 1) * a.split;
+  const long long grid =
+      static_cast<long long>(ceil_div(tokens, pair ? 2 * kTileM : kTileM)) * a.n_tiles * ctas;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const auto kernel = pair ? w4a16_router_dense_kernel<true> : w4a16_router_dense_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 2048);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, static_cast<int>(tiles * ctas), kDenseThreads,
-                          dense_smem(a), ctas, stream, a);
+  return launch_dependent(kernel, static_cast<int>(grid), kDenseThreads, dense_smem(a), ctas,
+                          stream, a);
 }
 
 }  // namespace w4a16
