@@ -18,7 +18,7 @@
 //
 // 384 experts of hidden 7168, in a graph: 1 token 3.2 us, 48 tokens 6.5 us, both
 // latency (launch, one round of loads, the cluster's exchange; the weight alone
-// is 0.8 us of the copy rate). 8192 tokens: 41 us, 1.1 PFLOP/s, 0.57 of a
+// is 0.8 us of the copy rate). 8192 tokens: 40 us, 1.1 PFLOP/s, 0.59 of a
 // library product's rate, on 128 of 152 SMs: 7 us are launch, first loads and
 // the logits' way out, the rest is bound by the operands' way into an SM
 // (28 KB of 64 columns at 50 bytes a cycle, against 384 cycles of MMAs).
@@ -214,7 +214,9 @@ __device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volati
 // one CTA. a.split CTAs or pairs of a cluster share a tile by its columns.
 // A wait that gives up (none does unless the hardware fails) ends the CTA's
 // work in order and leaves NaN in its logits.
-template <bool kPair>
+// kSub * kKStep columns are a step (of a constant count: a loop over a variable
+// one cost the MMA threads 0.6 us of 777 tokens' 7.7).
+template <bool kPair, int kSub>
 __global__ void __launch_bounds__(kDenseThreads, 1)
     w4a16_router_dense_kernel(const __grid_constant__ DenseArgs a) {
   extern __shared__ uint8_t raw[];
@@ -229,12 +231,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                  drained = done + 8 * kDensePairs, received = drained + 8 * kDensePairs;
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.b_rows) * kKStep * 2;
-  const uint32_t sub_bytes = a_bytes + b_bytes, slot_bytes = sub_bytes * a.sub;
+  const uint32_t sub_bytes = a_bytes + b_bytes, slot_bytes = sub_bytes * kSub;
   const int ctas = (kPair ? 2 : 1) * a.split;  // of a tile
   const int id = static_cast<int>(blockIdx.x) % ctas;  // in the cluster
   const int half = kPair ? id & 1 : 0, rank = kPair ? id >> 1 : id;  // of the tokens, columns
   const uint32_t leader = static_cast<uint32_t>(kPair ? id & ~1 : id);
-  const int chunk = kChunk / a.sub;
+  constexpr int kRun = kChunk / kSub;
   const int tile = static_cast<int>(blockIdx.x) / ctas;
   const int m0 = (kPair ? tile / a.n_tiles * 2 + half : tile / a.n_tiles) * kTileM;
   const int n0 = tile % a.n_tiles * a.tile_n;
@@ -281,9 +283,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         if (!ok) break;
         if (half == 0)
           mbar_arrive_expect_tx(full + 8 * slot, kPair ? 2 * slot_bytes : slot_bytes);
-        for (int j = 0; j < a.sub; ++j) {
+#pragma unroll
+        for (int j = 0; j < kSub; ++j) {
           const uint32_t to = ring + slot * slot_bytes + j * sub_bytes;
-          const int column = (k * a.sub + j) * kKStep;
+          const int column = (k * kSub + j) * kKStep;
           if constexpr (kPair) {
             const uint32_t bar = map_to_cta(full + 8 * slot, leader);
             tma_load_2d_pair(to, &a.x, column, m0, bar);
@@ -319,22 +322,23 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       int n = 0;  // steps of this thread
       for (int i = first; k0 + i < k1; i += kDensePairs, ++n) {
         const int slot = i % a.slots;
-        if (n > 0 && n % chunk == 0) {
+        if (n > 0 && n % kRun == 0) {
           report(done + 8 * first);
-          ok = dense_wait<kPair>(drained + 8 * first, (n / chunk - 1) & 1, failed);
+          ok = dense_wait<kPair>(drained + 8 * first, (n / kRun - 1) & 1, failed);
           if (!ok) break;
           tc_fence_after();
         }
         ok = dense_wait(full + 8 * slot, i / a.slots & 1, failed);
         if (!ok) break;
         tc_fence_after();
-        for (int u = 0; u < a.sub; ++u) {
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
           const uint32_t from = ring + slot * slot_bytes + u * sub_bytes;
           const uint64_t ad = smem_desc_sw128_kmajor(from);
           const uint64_t bd = smem_desc_sw128_kmajor(from + a_bytes);
 #pragma unroll
           for (int j = 0; j < kKStep / 16; ++j) {  // 32 bytes further along k
-            const uint32_t add = n % chunk != 0 || u > 0 || j > 0;
+            const uint32_t add = n % kRun != 0 || u > 0 || j > 0;
             if constexpr (kPair)
               mma_bf16_ss_pair(d, ad + 2 * j, bd + 2 * j, idesc, add);
             else
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       bool any = false;
       for (int j = 0; j < kDensePairs && ok; ++j) {
         // chunk c of MMA thread j, which has the steps j, j + kDensePairs, ...
-        if (j + c * chunk * kDensePairs >= k1 - k0) continue;
+        if (j + c * kRun * kDensePairs >= k1 - k0) continue;
         any = true;
         ok = __all_sync(0xffffffffu, dense_wait(done + 8 * j, c & 1, failed));
         if (!ok) break;
@@ -465,10 +469,10 @@ int clusters_at_once(int ctas, int sms) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(w4a16_router_dense_kernel<false>,
+  if (cudaFuncSetAttribute(w4a16_router_dense_kernel<false, 1>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kRingBytes + 2048) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, w4a16_router_dense_kernel<false>, &cfg) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, w4a16_router_dense_kernel<false, 1>, &cfg) != cudaSuccess ||
       n <= 0)
     n = std::max(1, sms / (2 * ctas));
   known[ctas] = n;
@@ -479,10 +483,10 @@ int clusters_at_once(int ctas, int sms) {
 // steps at the rate at which an SM takes operands from L2 (50 bytes a cycle
 // were measured) or at which the threads get round their loops, plus the
 // tile's sums on their way out. Against every shape timed (65 to 8192 tokens of
-// six weights) the choice is within 2 per cent of the fastest in the mean, 11
-// at most; hidden 7168 x 384 experts, us: 777 tokens 18 (a pair of 128 experts, split by 4: 17; one
-// CTA, split by 4: 19), 4096 tokens 29 (pairs unsplit 36, one CTA 34), 8192
-// tokens 41 (one CTA 54).
+// six weights) the choice is within 2 per cent of the fastest in the mean, 14
+// at most; hidden 7168 x 384 experts, us: 777 tokens 17 (a pair of 128 experts,
+// split by 4: 16; one CTA, split by 4: 18), 4096 tokens 28 (pairs unsplit 35,
+// one CTA 33), 8192 tokens 40 (one CTA 54).
 bool dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a) {
   bool best_pair = false;
   double best = 0;
@@ -508,7 +512,7 @@ bool dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a)
         const int ctas = c.split * (pair ? 2 : 1);
         const double waves = std::ceil(tiles / clusters_at_once(ctas, sms));
         const double cost = waves * (ceil_div(c.k_steps, c.split) * step_cycles + 3000 +
-                                     c.tile_n * 28 + (c.split > 1 ? 4500 : 0));
+                                     c.tile_n * 28 + (c.split == 1 ? 0 : pair ? 4500 : 3500));
         if (best == 0 || cost < best) {
           best = cost;
           best_pair = pair != 0;
@@ -546,7 +550,9 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
   const long long grid =
       static_cast<long long>(ceil_div(tokens, pair ? 2 * kTileM : kTileM)) * a.n_tiles * ctas;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const auto kernel = pair ? w4a16_router_dense_kernel<true> : w4a16_router_dense_kernel<false>;
+  const auto kernel = !pair ? w4a16_router_dense_kernel<false, 1>
+                      : a.sub == 1 ? w4a16_router_dense_kernel<true, 1>
+                                   : w4a16_router_dense_kernel<true, 2>;
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 2048);
   if (e != cudaSuccess) return e;
