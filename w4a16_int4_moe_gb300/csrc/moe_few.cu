@@ -1062,14 +1062,26 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
           // the CTA that arrives last adds the shares, in the CTAs' order
           finish = epilogue_arrive(&counters->item[0][cta0], cta1 - cta0, last_arrival, etid);
           if (finish) {
-#pragma unroll 2
-            for (int b = cta0; b <= cta1; ++b) {
-              const float* f = shares + (2 * b + (b == cta0 ? 1 : 0)) * share + at_g;
+            // (four at a time, so that a trip to L2 brings four)
+            for (int b0 = cta0; b0 <= cta1; b0 += 4) {
+              float part[4][kRowsPerPass][2];
 #pragma unroll
-              for (int r = 0; r < kRowsPerPass; ++r)
-                if (r < n) {
-                  gate[r] += __ldcg(f + r * kTileRows);
-                  up[r] += __ldcg(f + r * kTileRows + 16);
+              for (int j = 0; j < 4; ++j) {
+                const int b = b0 + j;
+                const float* f = shares + (2 * b + (b == cta0 ? 1 : 0)) * share + at_g;
+#pragma unroll
+                for (int r = 0; r < kRowsPerPass; ++r) {
+                  const bool in = b <= cta1 && r < n;
+                  part[j][r][0] = in ? __ldcg(f + r * kTileRows) : 0.f;
+                  part[j][r][1] = in ? __ldcg(f + r * kTileRows + 16) : 0.f;
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < kRowsPerPass; ++r) {
+                  gate[r] += part[j][r][0];
+                  up[r] += part[j][r][1];
                 }
             }
           }
