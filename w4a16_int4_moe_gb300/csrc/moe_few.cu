@@ -844,17 +844,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
             next_s -= S;
             ++next_q;
           }
-          int next_valid = 0;
+          // (behind the last stage the same columns come again, unused: a
+          // branch of its own would be met with its instructions not there)
+          int next_valid = valid;
+          const uint8_t* next = here;
           const float2 factor = next_factor;
           if (at < gu_end) {
             if (next_q != q) point(next_q);
             next_valid = groups0 - 8 * next_s;
+            next = cols + next_s * (2 * kStageK);
             next_factor = *reinterpret_cast<const float2*>(factors + 2 * next_s);
           }
           const uint32_t base = wait_stage();
           stage_mma<1>(valid, base + codes_at, base + scales_at, x,
-                       make_float4(factor.x, factor.x, factor.y, factor.y), here,
-                       cols + next_s * (2 * kStageK), next_valid, acc);
+                       make_float4(factor.x, factor.x, factor.y, factor.y), here, next,
+                       next_valid, acc);
           free_stage();
         }
         // [row of the pass][128] of this warpgroup, in the buffers by turns
@@ -927,7 +931,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
             at += kGroups;
             next_s += kGroups;
             more = next_s < S && at < stop;
-            int next_valid = 0;
+            int next_valid = valid;
+            const uint8_t* next = here;
             const float4 factor = next_factor;
             if (at < dn_end) {
               if (next_s >= S) {
@@ -938,11 +943,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
                 point(next_c);
               }
               next_valid = groups1 - 8 * next_s;
+              next = cols + next_s * (2 * kStageK);
               next_factor = *reinterpret_cast<const float4*>(factors + 4 * next_s);
             }
             const uint32_t base = wait_stage();
-            stage_mma<2>(valid, base + codes_at, base + scales_at, x, factor, here,
-                         cols + next_s * (2 * kStageK), next_valid, acc);
+            stage_mma<2>(valid, base + codes_at, base + scales_at, x, factor, here, next,
+                         next_valid, acc);
             free_stage();
           }
           if (t <= last) {
