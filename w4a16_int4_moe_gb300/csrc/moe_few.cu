@@ -230,7 +230,7 @@ __device__ __forceinline__ uint4 load16(const void* from) {
   return *reinterpret_cast<const uint4*>(from);
 }
 
-// kG groups of 32 k of one 64-k step: 64 weight rows of this warp (four 16-row
+// The two groups of 32 k of a 64-k step: 64 weight rows of this warp (four 16-row
 // MMA tiles) times eight columns, of which a thread keeps the even one or
 // both; acc += scale * sum of every group.
 // k order inside a group: thread t of a quad holds word t of each weight row
@@ -238,21 +238,21 @@ __device__ __forceinline__ uint4 load16(const void* from) {
 // takes k = 8t .. 8t + 3, the second the rest, so both operands use one order.
 // The scales of four rows and both groups come as one transposed ldmatrix
 // whose addresses repeat two 16-byte runs.
-template <int kCols, int kG>
+template <int kCols>
 __device__ __forceinline__ void step_mma(uint32_t codes, uint32_t scales, const uint4& b0,
                                          const uint4& b1, float (&acc)[kMt][2 * kCols]) {
   constexpr uint32_t kLow = 0x00780078u, kHigh = 0x07800780u;
   const uint32_t minus8[4] = {0x80408040u, 0x80408040u, 0x84008400u, 0x84008400u};
-  uint32_t w[kG][kMt / 2][4], sc[kMt / 2][4];
+  uint32_t w[2][kMt / 2][4], sc[kMt / 2][4];
 #pragma unroll
-  for (int g = 0; g < kG; ++g)
+  for (int g = 0; g < 2; ++g)
 #pragma unroll
     for (int h = 0; h < kMt / 2; ++h)
       ldmatrix_x4(codes + g * (kTileRows * 16) + h * 512, w[g][h]);
 #pragma unroll
   for (int h = 0; h < kMt / 2; ++h) ldmatrix_x4_trans(scales + h * 64, sc[h]);
 #pragma unroll
-  for (int g = 0; g < kG; ++g) {
+  for (int g = 0; g < 2; ++g) {
     const uint4 b = g == 0 ? b0 : b1;
     float i[4];
     mma16816(i, minus8, b.x, b.y, 0.f, 0.f, 0.f, 0.f);
@@ -288,19 +288,17 @@ __device__ __forceinline__ void half_mma(int valid, uint32_t codes, uint32_t sca
   const auto step = [&](auto st, int n, int next_n) {
     constexpr int kS = decltype(st)::value;
     float part[kMt][2 * kCols] = {};
-    if (n >= 2)
-      step_mma<kCols, 2>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
-                         x.b[2 * kS + 1], part);
-    else if (n == 1)
-      step_mma<kCols, 1>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
+    if (n > 0)  // (a second group that the row does not have has scale 0)
+      step_mma<kCols>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
                          x.b[2 * kS + 1], part);
     const float f = kS == 0 ? factor.x : factor.y;
 #pragma unroll
     for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
       for (int i = 0; i < 2 * kCols; ++i) acc[mt][i] = fmaf(f, part[mt][i], acc[mt][i]);
-    if (next_n > 0) x.b[2 * kS] = load16(next + kS * 128);
-    if (next_n > 1) x.b[2 * kS + 1] = load16(next + kS * 128 + 64);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    x.b[2 * kS] = next_n > 0 ? load16(next + kS * 128) : zero;
+    x.b[2 * kS + 1] = next_n > 1 ? load16(next + kS * 128 + 64) : zero;
   };
   if (valid >= 4 && next_valid >= 4) {  // nearly always: no branch inside
     step(std::integral_constant<int, 0>(), 2, 2);
