@@ -45,12 +45,13 @@
 // atomics, so the result depends only on the sizes and the routing.
 //
 // Measured, hidden 7168, top-8 of 384: 48 local experts of inter 2048, 32
-// tokens: 133 us for 719 MB, 5.4 TB/s (0.79 of the copy rate); 384 experts of
-// inter 256, 16 tokens: 80 us for 340 MB, 4.3 TB/s (0.63); 1 token 23.5 us, of
-// which the 25 MB are 3.7: routing, the fill of the ring, the activation's
-// exchange between the CTAs and the tail are a chain of latencies. What bounds
-// the large ones is the loop of the compute warps: waits for columns from L2
-// and for the next slot (tensor pipe 27 per cent, ALU 39, issue slots 44).
+// tokens: 134 us for 719 MB, 5.4 TB/s (0.79 of the copy rate); 384 experts of
+// inter 256, 16 tokens: 81 us for 340 MB, 4.2 TB/s (0.62); 1 token 23.3 us, of
+// which the 25 MB are 3.7. Inside the products the weights come at 6.2 TB/s
+// (gate_up) and 5.3 (down, where the two columns of a row and the sums by token
+// cost the compute warps more: tensor pipe 27 per cent of the whole call, ALU
+// 40, issue slots 44); the rest is a chain of latencies: rows and routing 4.5
+// us, lists 1.6, first copies 2.3, the activation's exchange 3 to 6.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
