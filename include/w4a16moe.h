@@ -531,8 +531,13 @@ size_t w4a16_moe_few_tokens_workspace_size(int tokens, int topk, int hidden, int
  * and out 16-byte aligned, the other arrays by their elements (else
  * W4A16_ERR_INVALID_ARG); ws_bytes >=
  * w4a16_moe_few_tokens_workspace_size(tokens, topk, hidden, inter) (else
- * W4A16_ERR_WORKSPACE). No host synchronisation: graph-capturable. A
- * device-side wait that gives up is reported by w4a16_read_device_status.
+ * W4A16_ERR_WORKSPACE). No host synchronisation: graph-capturable. Its
+ * CTAs, one per SM, exchange rows and activations, so all of them must become
+ * resident while it runs: it may share the device with kernels that end by
+ * themselves, but not with a second such call (or w4a16_moe_layer) on a stream
+ * of another priority, which could take the SMs that it still waits for. A
+ * device-side wait that gives up is reported by w4a16_read_device_status
+ * (W4A16_ERR_TIMEOUT); the next call is right again.
  */
 w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed_down,
                                   int num_experts, int hidden, int inter, const void* x,
