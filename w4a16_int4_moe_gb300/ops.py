@@ -398,14 +398,12 @@ def w4a16_silu_and_mul(x: torch.Tensor, out: Optional[torch.Tensor] = None, stre
 # pass plain integers: no ctypes object is built per pointer, and the current
 # stream is read without making a Stream object.
 
-def _raw_stream(device, stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return _current_stream(device.index)
+_BF16, _E4M3, _F32, _I32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (of CUDA builds)
 
 
-def _current_stream(index):
-    return torch._C._cuda_getCurrentRawStream(0 if index is None else index)
+def _raw_stream(t: torch.Tensor, stream):
+    return _current_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _refuse(fn: str, why: str):
@@ -431,9 +429,12 @@ def _blob(fn: str, what: str, t: torch.Tensor, size: int):
 def _rows(fn: str, what: str, t: torch.Tensor):
     """t is BF16 [rows, columns] on a GPU with adjacent columns; returns
     (address, rows, columns, row stride)."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 2 or not t.is_cuda:
+    if t.dtype is not _BF16 or not t.is_cuda or t.dim() != 2:
         _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}")
-    (rows, columns), (pitch, step) = t.shape, t.stride()
+    rows, columns = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), rows, columns, columns
+    pitch, step = t.stride()
     if step != 1 and columns > 1:
         _refuse(fn, f"{what}: strides {t.stride()}")
     return t.data_ptr(), rows, columns, pitch if rows > 1 else max(pitch, columns)
@@ -444,24 +445,25 @@ def w4a16_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
                        fp8_group: int = W4A16_FP8_NONE, bf16_out: bool = True, out=None,
                        stream=None):
     """h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight.
-    Returns (bf16(y), bf16(h), e4m3(y / scale), scale), each None when not
+    Returns (bf16(y), bf16(h), e4m3(y * (1 / scale)), scale), each None when not
     asked for: bf16_out, residual, fp8_group (W4A16_FP8_GROUP: a scale per 128
     columns, W4A16_FP8_ROW: one per row). out: the four tensors to write, None
     for an absent one (it then decides which of y and its 8-bit form is
-    written, and the third entry may be the residual itself). x and residual
+    written, and the second entry may be the residual itself). x and residual
     BF16 [T, H], rows may be strided."""
     fn = "w4a16_add_rms_norm"
     x_at, rows, hidden, x_stride = _rows(fn, "x", x)
-    w_at = _need(fn, "weight", weight, torch.bfloat16, (hidden,))
+    w_at = _need(fn, "weight", weight, _BF16, (hidden,))
     r_at, r_stride = None, 0
     if residual is not None:
         r_at, r_rows, r_cols, r_stride = _rows(fn, "residual", residual)
         if r_rows != rows or r_cols != hidden:
             _refuse(fn, f"residual {tuple(residual.shape)} for x {tuple(x.shape)}")
-    if fp8_group not in (W4A16_FP8_NONE, W4A16_FP8_ROW, W4A16_FP8_GROUP):
-        raise W4A16Error(fn, W4A16_ERR_UNSUPPORTED, f"fp8_group {fp8_group}")
-    shape = (rows, hidden)
-    groups = (rows, 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP))
+    shape, groups = (rows, hidden), None
+    if fp8_group != W4A16_FP8_NONE:
+        if fp8_group not in (W4A16_FP8_ROW, W4A16_FP8_GROUP):
+            raise W4A16Error(fn, W4A16_ERR_UNSUPPORTED, f"fp8_group {fp8_group}")
+        groups = (rows, 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP))
     if out is None:
         out = (torch.empty(shape, dtype=torch.bfloat16, device=x.device) if bf16_out else None,
                torch.empty(shape, dtype=torch.bfloat16, device=x.device)
@@ -472,11 +474,11 @@ def w4a16_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     y, res_out, y8, scales = out
     _check(fn, load_library().w4a16_add_rms_norm(
         x_at, x_stride, r_at, r_stride, w_at, eps, rows, hidden,
-        None if y is None else _need(fn, "out", y, torch.bfloat16, shape),
-        None if res_out is None else _need(fn, "residual_out", res_out, torch.bfloat16, shape),
-        None if y8 is None else _need(fn, "out_fp8", y8, torch.float8_e4m3fn, shape),
-        None if scales is None else _need(fn, "scales", scales, torch.float32, groups),
-        fp8_group, _raw_stream(x.device, stream)))
+        None if y is None else _need(fn, "out", y, _BF16, shape),
+        None if res_out is None else _need(fn, "residual_out", res_out, _BF16, shape),
+        None if y8 is None else _need(fn, "out_fp8", y8, _E4M3, shape),
+        None if scales is None else _need(fn, "scales", scales, _F32, groups),
+        fp8_group, _raw_stream(x, stream)))
     return out
 
 
@@ -486,12 +488,12 @@ def w4a16_router_logits(x: torch.Tensor, weight: torch.Tensor,
     fn = "w4a16_router_logits"
     x_at, tokens, hidden, x_stride = _rows(fn, "x", x)
     experts = weight.shape[0]
-    w_at = _need(fn, "weight", weight, torch.bfloat16, (experts, hidden))
+    w_at = _need(fn, "weight", weight, _BF16, (experts, hidden))
     if out is None:
         out = torch.empty((tokens, experts), dtype=torch.float32, device=x.device)
     _check(fn, load_library().w4a16_router_logits(
         x_at, x_stride, w_at, tokens, hidden, experts,
-        _need(fn, "out", out, torch.float32, (tokens, experts)), _raw_stream(x.device, stream)))
+        _need(fn, "out", out, _F32, (tokens, experts)), _raw_stream(x, stream)))
     return out
 
 
@@ -513,7 +515,7 @@ def w4a16_moe_few_tokens(packed_gate_up: torch.Tensor, packed_down: torch.Tensor
     fn = "w4a16_moe_few_tokens"
     tokens, topk = picks = topk_ids.shape
     fp8 = x_scales is not None
-    x_at = _need(fn, "x", x, torch.float8_e4m3fn if fp8 else torch.bfloat16, (tokens, hidden))
+    x_at = _need(fn, "x", x, _E4M3 if fp8 else _BF16, (tokens, hidden))
     s_at = None
     if fp8:
         s_at = _need(fn, "x_scales", x_scales, torch.float32,
@@ -537,10 +539,10 @@ def w4a16_moe_few_tokens(packed_gate_up: torch.Tensor, packed_down: torch.Tensor
         _blob(fn, "packed_down", packed_down, down_size), num_experts, hidden, inter, x_at,
         W4A16_DTYPE_FP8 if fp8 else W4A16_DTYPE_BF16, s_at, tokens, topk, lg_at, lg_type, experts,
         1 if renormalize else 0, expert_offset,
-        _need(fn, "topk_ids", topk_ids, torch.int32, picks),
-        _need(fn, "topk_weights", topk_weights, torch.float32, picks),
-        _need(fn, "out", out, torch.float32, (tokens, hidden)), flags,
-        _blob(fn, "workspace", workspace, 0), workspace.numel(), _raw_stream(x.device, stream)))
+        _need(fn, "topk_ids", topk_ids, _I32, picks),
+        _need(fn, "topk_weights", topk_weights, _F32, picks),
+        _need(fn, "out", out, _F32, (tokens, hidden)), flags,
+        _blob(fn, "workspace", workspace, 0), workspace.numel(), _raw_stream(x, stream)))
     return out
 
 
