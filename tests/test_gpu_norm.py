@@ -152,3 +152,14 @@ def test_on_a_side_stream_and_in_a_graph(cuda_dev):
     torch.cuda.synchronize()
     for a, b in zip(out, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("fp8_group", [0, 128, -1])
+@pytest.mark.parametrize("tokens,hidden,residual,pitch", [
+    # more rows than SMs, and than four times as many, at every division of a row
+    (400, 2088, True, 0), (700, 2600, True, 0), (200, 3336, False, 3400), (200, 5000, True, 0),
+    (200, 8000, True, 8008), (200, 10000, True, 0), (170, 12280, False, 0), (170, 16000, True, 0),
+    (100, 10008, True, 0),
+])
+def test_norm_of_many_rows(cuda_dev, tokens, hidden, residual, pitch, fp8_group):
+    test_norm(cuda_dev, tokens, hidden, residual, pitch, fp8_group)

@@ -829,9 +829,11 @@ w4a16_status w4a16_add_rms_norm(const uint16_t* x, long long x_stride, const uin
       !aligned16(residual_out) || (reinterpret_cast<uintptr_t>(out_fp8) & 7u) != 0 ||
       (reinterpret_cast<uintptr_t>(scales) & 3u) != 0)
     return W4A16_ERR_INVALID_ARG;
+  const int sms = current_sm_count();
+  if (sms <= 0) return W4A16_ERR_CUDA;
   NormArgs a = {x,    x_stride, residual, residual_stride, weight, eps,      rows,
                 hidden, out,    residual_out, out_fp8,     scales, fp8_group};
-  return cuda_status(launch_add_rms_norm(a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_add_rms_norm(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 w4a16_status w4a16_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,

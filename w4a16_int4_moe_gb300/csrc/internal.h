@@ -242,7 +242,7 @@ struct NormArgs {
   int fp8_group;  // W4A16_FP8_*
 };
 constexpr int kNormMaxHidden = 16384;
-cudaError_t launch_add_rms_norm(const NormArgs& args, cudaStream_t stream);
+cudaError_t launch_add_rms_norm(const NormArgs& args, int sms, cudaStream_t stream);
 
 // The router's product (router.cu).
 cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,

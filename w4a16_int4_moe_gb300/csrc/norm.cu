@@ -9,12 +9,12 @@
 //
 // Bound by memory for many rows, by latency for few: 8192 rows of 7168 with a
 // residual, BF16 and 8-bit outputs and group scales take 79 us, 6.7 TB/s of the
-// 530 MB, which is the copy rate; 576 such rows 9 us (4.1 TB/s), one BF16 row
-// 3.7 us. A row is read once into registers (eight columns a thread and chunk:
-// 16-byte loads), its sum of squares joined over the threads of the row, and
-// everything is written from registers. A block of 16 lanes holds the 128
-// columns of a group of the 8-bit
-// form, so a group's largest value needs four shuffles and no shared memory.
+// 530 MB, which is the copy rate; 576 such rows 9 us (4.1 TB/s), one 2.3, one
+// BF16 row 1.9 (in a graph). A row is read once into registers (eight columns a
+// thread and chunk: 16-byte loads), its sum of squares joined over the threads
+// of the row, and everything is written from registers. A block of 16 lanes
+// holds the 128 columns of a group of the 8-bit form, so a group's largest
+// value needs four shuffles and no shared memory.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -181,7 +181,14 @@ __global__ void __launch_bounds__(kThreads) w4a16_add_rms_norm_kernel(const Norm
   if (threadIdx.x == 0) a.scales[row] = scale;
 }
 
-cudaError_t launch_add_rms_norm(const NormArgs& args, cudaStream_t stream) {
+// Threads and chunks of a row. With at most a row an SM, more threads and fewer
+// chunks: a row of 7168 takes 2.2 us on 512 x 2 and 2.7 on 256 x 4 (with group
+// scales). With more rows as few threads' registers without columns as can be,
+// in CTAs of 128 or 256: 8192 rows of 2088 take 21 us on 128 x 3 and 27 on
+// 384 x 1 or 256 x 2, 8192 of 7168 79 us on 256 x 4 and 88 on 512 x 2; up to
+// four rows an SM the former's CTAs fit at once and 384 x 1 is faster (576 rows
+// of 2088: 2.4 and 2.7 us).
+cudaError_t launch_add_rms_norm(const NormArgs& args, int sms, cudaStream_t stream) {
   const int need = (args.hidden + 7) / 8;  // threads of one chunk
   const auto run = [&](void (*kernel)(NormArgs), int threads) {
     return launch_dependent(kernel, args.rows, threads, 0, 1, stream, args);
@@ -189,8 +196,15 @@ cudaError_t launch_add_rms_norm(const NormArgs& args, cudaStream_t stream) {
   if (need <= 32) return run(w4a16_add_rms_norm_kernel<32, 1>, 32);
   if (need <= 128) return run(w4a16_add_rms_norm_kernel<128, 1>, 128);
   if (need <= 256) return run(w4a16_add_rms_norm_kernel<256, 1>, 256);
+  if (need <= 384 && args.rows <= 4 * sms) return run(w4a16_add_rms_norm_kernel<384, 1>, 384);
+  if (need <= 384) return run(w4a16_add_rms_norm_kernel<128, 3>, 128);
   if (need <= 512) return run(w4a16_add_rms_norm_kernel<256, 2>, 256);
+  if (need <= 1024 && args.rows <= sms) return run(w4a16_add_rms_norm_kernel<512, 2>, 512);
+  if (need <= 768) return run(w4a16_add_rms_norm_kernel<256, 3>, 256);
   if (need <= 1024) return run(w4a16_add_rms_norm_kernel<256, 4>, 256);
+  if (args.rows <= sms) return run(w4a16_add_rms_norm_kernel<512, 4>, 512);
+  if (need <= 1280) return run(w4a16_add_rms_norm_kernel<256, 5>, 256);
+  if (need <= 1536) return run(w4a16_add_rms_norm_kernel<256, 6>, 256);
   return run(w4a16_add_rms_norm_kernel<512, 4>, 512);
 }
 
