@@ -95,3 +95,12 @@ def test_router_many_tokens(cuda_dev, tokens, hidden, experts, pitch):
     g.check("logits")
     _check(g.t, x, w)
     assert torch.equal(ops.w4a16_router_logits(x, w), g.t)
+
+
+@pytest.mark.parametrize("tokens,hidden,experts", [
+    # both sides of one wave of the few-token kernel
+    (400, 2088, 60), (640, 2088, 60), (1500, 128, 16), (1800, 128, 16), (500, 1024, 32),
+    (384, 7168, 64), (420, 7168, 64), (33, 520, 1024), (16, 520, 1024), (8, 520, 1024),
+])
+def test_router_between_the_kernels(cuda_dev, tokens, hidden, experts):
+    test_router_many_tokens(cuda_dev, tokens, hidden, experts, 0)

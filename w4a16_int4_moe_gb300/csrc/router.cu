@@ -3,12 +3,12 @@
 //
 // Two kernels, by the number of tokens:
 //
-//   * up to kFewTokens: the weight (5.5 MB for 384 experts of hidden 7168) is
-//     read once and every token with it. A cluster of eight CTAs shares
-//     sixteen experts, each CTA an eighth of the columns, so that all SMs read
-//     a part of the weight at once; m16n8k16 MMAs straight from global memory
-//     (no operand is used twice by an SM), partial sums joined through the
-//     cluster's shared memory;
+//   * few, as long as all of its CTAs run at once (64 tokens of 384 experts, 400
+//     of 60): a cluster of eight CTAs shares sixteen experts and 32 tokens, each
+//     CTA an eighth of the columns, so that all SMs read a part of the weight
+//     (5.5 MB for 384 experts of hidden 7168) at once; m16n8k16 MMAs straight
+//     from global memory (no operand is used twice by a CTA), partial sums
+//     joined through the cluster's shared memory;
 //   * more: a dense product on tcgen05, 128 tokens (256 of a CTA pair) x up to
 //     256 experts a tile, both operands by TMA, accumulators in TMEM. Where the
 //     tiles are fewer than the SMs, a cluster of up to eight CTAs splits the
@@ -39,9 +39,6 @@ namespace {
 
 // ----------------------------------------------------------- few tokens ---
 
-// (at 65 tokens x 384 experts x 7168 columns the two kernels take 10 us each,
-// at 64 tokens this one 6.5)
-constexpr int kFewTokens = 64;
 constexpr int kFewBlock = 32;  // tokens of a CTA at most (64: 9.9 us for 48 tokens, 32: 6.5)
 constexpr int kFewCluster = 8;
 constexpr int kFewWarps = 8;
@@ -452,16 +449,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 
 namespace {
 
-// How many clusters of `ctas` run at once with one CTA an SM: clusters stay
-// inside a GPC, so eights leave some SMs out.
-int clusters_at_once(int ctas, int sms) {
-  static std::atomic<int> known[kMaxSplit + 1];
-  if (ctas == 1) return sms;
-  if (const int n = known[ctas]) return n;
+// How many clusters of `ctas` run at once (they stay inside a GPC, so eights of
+// one CTA an SM leave some SMs out); 0 if that cannot be said.
+template <typename Kernel>
+int clusters_at_once(Kernel kernel, int ctas, int threads, size_t smem, std::atomic<int>& known) {
+  if (const int n = known) return n;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas * sms));
-  cfg.blockDim = dim3(kDenseThreads);
-  cfg.dynamicSmemBytes = kRingBytes + 2048;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = static_cast<unsigned>(ctas);
@@ -469,14 +465,32 @@ int clusters_at_once(int ctas, int sms) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(w4a16_router_dense_kernel<false, 1>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kRingBytes + 2048) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, w4a16_router_dense_kernel<false, 1>, &cfg) != cudaSuccess ||
-      n <= 0)
-    n = std::max(1, sms / (2 * ctas));
-  known[ctas] = n;
+  if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem)) != cudaSuccess)
+    return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  known = n;
   return n;
+}
+
+int dense_clusters_at_once(int ctas, int sms) {
+  static std::atomic<int> known[kMaxSplit + 1];
+  if (ctas == 1) return sms;
+  const int n = clusters_at_once(w4a16_router_dense_kernel<false, 1>, ctas, kDenseThreads,
+                                 kRingBytes + 2048, known[ctas]);
+  return n > 0 ? n : std::max(1, sms / (2 * ctas));
+}
+
+// One wave of the few-token kernel is faster than the dense one and two are
+// not: hidden 7168 x 384 experts, 64 tokens (48 clusters of 51 that run at once)
+// 6.4 us against 9.0, 65 tokens 10.6 against 9.0; 2088 x 60, 192 tokens 3.8
+// against 7.6, 600 tokens (76) 8.1 against 7.8; 7168 x 1024, 16 tokens (64 of
+// 74) 5.6 against 10.8, 64 tokens (128) 17.8 against 11.8.
+template <int kNt>
+bool few_fits(long long clusters) {
+  static std::atomic<int> known;
+  return clusters <= clusters_at_once(w4a16_router_few_kernel<kNt>, kFewCluster, kFewWarps * 32, 0,
+                                      known);
 }
 
 // The fastest shape by an estimate in cycles: waves of clusters, each a CTA's
@@ -510,7 +524,7 @@ bool dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a)
       for (c.split = 1; c.split * (pair ? 2 : 1) <= kMaxSplit && c.split <= c.k_steps; c.split *= 2) {
         if (c.split > 1 && 2 * tile_sums_bytes(c.tile_n) > kRingBytes) break;
         const int ctas = c.split * (pair ? 2 : 1);
-        const double waves = std::ceil(tiles / clusters_at_once(ctas, sms));
+        const double waves = std::ceil(tiles / dense_clusters_at_once(ctas, sms));
         const double cost = waves * (ceil_div(c.k_steps, c.split) * step_cycles + 3000 +
                                      c.tile_n * 28 + (c.split == 1 ? 0 : pair ? 4500 : 3500));
         if (best == 0 || cost < best) {
@@ -528,16 +542,16 @@ bool dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a)
 cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
                                  int tokens, int hidden, int num_experts, float* logits, int sms,
                                  cudaStream_t stream) {
-  if (tokens <= kFewTokens) {
-    const int grid = ceil_div(num_experts, kFewExperts) * ceil_div(tokens, kFewBlock) * kFewCluster;
-    const auto run = [&](auto kernel) {
-      return launch_dependent(kernel, grid, kFewWarps * 32, 0, kFewCluster, stream, x, x_stride,
-                              weight, tokens, hidden, num_experts, logits);
-    };
-    if (tokens <= 8) return run(w4a16_router_few_kernel<1>);
-    if (tokens <= 16) return run(w4a16_router_few_kernel<2>);
-    return run(w4a16_router_few_kernel<kFewBlock / 8>);
-  }
+  const long long clusters =
+      static_cast<long long>(ceil_div(num_experts, kFewExperts)) * ceil_div(tokens, kFewBlock);
+  const auto few = [&](auto kernel) {
+    return launch_dependent(kernel, static_cast<int>(clusters) * kFewCluster, kFewWarps * 32, 0,
+                            kFewCluster, stream, x, x_stride, weight, tokens, hidden, num_experts,
+                            logits);
+  };
+  if (tokens <= 8 && few_fits<1>(clusters)) return few(w4a16_router_few_kernel<1>);
+  if (tokens <= 16 && few_fits<2>(clusters)) return few(w4a16_router_few_kernel<2>);
+  if (few_fits<kFewBlock / 8>(clusters)) return few(w4a16_router_few_kernel<kFewBlock / 8>);
   DenseArgs a;
   const bool pair = dense_shape(tokens, num_experts, hidden, sms, &a);
   a.logits = logits;
