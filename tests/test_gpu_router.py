@@ -104,3 +104,12 @@ def test_router_many_tokens(cuda_dev, tokens, hidden, experts, pitch):
 ])
 def test_router_between_the_kernels(cuda_dev, tokens, hidden, experts):
     test_router_many_tokens(cuda_dev, tokens, hidden, experts, 0)
+
+
+@pytest.mark.parametrize("tokens,hidden,experts", [
+    # clusters of eight, four, two and one of the small kernel
+    (300, 2088, 60), (777, 2088, 60), (1200, 2088, 60), (1600, 136, 16), (2500, 136, 16),
+    (4000, 136, 16), (8100, 136, 16), (1900, 264, 64), (2000, 4096, 16),
+])
+def test_router_small_clusters(cuda_dev, tokens, hidden, experts):
+    test_router_many_tokens(cuda_dev, tokens, hidden, experts, hidden + 8)

@@ -4,8 +4,8 @@
 // Two kernels, by the number of tokens:
 //
 //   * few, as long as all of its CTAs run at once (64 tokens of 384 experts, 400
-//     of 60): a cluster of eight CTAs shares sixteen experts and 32 tokens, each
-//     CTA an eighth of the columns, so that all SMs read a part of the weight
+//     of 60): a cluster of up to eight CTAs shares sixteen experts and 32 tokens,
+//     each CTA a share of the columns, so that all SMs read a part of the weight
 //     (5.5 MB for 384 experts of hidden 7168) at once; m16n8k16 MMAs straight
 //     from global memory (no operand is used twice by a CTA), partial sums
 //     joined through the cluster's shared memory;
@@ -40,7 +40,6 @@ namespace {
 // ----------------------------------------------------------- few tokens ---
 
 constexpr int kFewBlock = 32;  // tokens of a CTA at most (64: 9.9 us for 48 tokens, 32: 6.5)
-constexpr int kFewCluster = 8;
 constexpr int kFewWarps = 8;
 constexpr int kFewExperts = 16;  // of a cluster (MMA M)
 
@@ -54,10 +53,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 
 }  // namespace
 
-// kNt tiles of eight tokens. Columns go in blocks of 32: thread t of a quad
+// kNt tiles of eight tokens, clusters of kCl CTAs. Columns go in blocks of 32: thread t of a quad
 // takes columns 8t .. 8t + 7 of a block, of both operands alike, so one 16-byte
 // load a row feeds two MMAs whatever order the MMA gives its k.
-template <int kNt>
+template <int kNt, int kCl>
 __global__ void __launch_bounds__(kFewWarps * 32)
     w4a16_router_few_kernel(const uint16_t* __restrict__ x, long long x_stride,
                             const uint16_t* __restrict__ weight, int tokens, int hidden,
@@ -67,7 +66,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int tile = static_cast<int>(blockIdx.x) / kFewCluster;
+  const int tile = static_cast<int>(blockIdx.x) / kCl;
   const int e_tiles = (num_experts + kFewExperts - 1) / kFewExperts;
   const int e0 = tile % e_tiles * kFewExperts;
   const int t0 = tile / e_tiles * (8 * kNt);
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   grid_dependency_wait();
   grid_dependents_go();
   const int blocks = (hidden + 31) / 32;
-  const int first = blocks * rank / kFewCluster, last = blocks * (rank + 1) / kFewCluster;
+  const int first = blocks * rank / kCl, last = blocks * (rank + 1) / kCl;
   const uint16_t* a0 = weight + static_cast<long long>(min(e0 + g, num_experts - 1)) * hidden;
   const uint16_t* a1 = weight + static_cast<long long>(min(e0 + g + 8, num_experts - 1)) * hidden;
   const uint16_t* b[kNt];
@@ -119,14 +118,14 @@ __global__ void __launch_bounds__(kFewWarps * 32)
     sums[i] = v;
   }
   cluster_sync_all();
-  // every CTA of the cluster writes an eighth of the outputs
+  // every CTA of the cluster writes its share of the outputs
   for (int i = rank * kFewWarps * 32 + static_cast<int>(threadIdx.x); i < kFewExperts * tokens;
-       i += kFewCluster * kFewWarps * 32) {
+       i += kCl * kFewWarps * 32) {
     const int tok = i / kFewExperts, e = e0 + i % kFewExperts;
     const uint32_t at = smem_u32(sums + i);
     float v = 0.f;
 #pragma unroll
-    for (int c = 0; c < kFewCluster; ++c)
+    for (int c = 0; c < kCl; ++c)
       v += ld_cluster_f32(map_to_cta(at, static_cast<uint32_t>(c)));
     if (e < num_experts) logits[static_cast<long long>(tok) * num_experts + e] = v;
   }
@@ -481,18 +480,6 @@ int dense_clusters_at_once(int ctas, int sms) {
   return n > 0 ? n : std::max(1, sms / (2 * ctas));
 }
 
-// One wave of the few-token kernel is faster than the dense one and two are
-// not: hidden 7168 x 384 experts, 64 tokens (48 clusters of 51 that run at once)
-// 6.4 us against 9.0, 65 tokens 10.6 against 9.0; 2088 x 60, 192 tokens 3.8
-// against 7.6, 600 tokens (76) 8.1 against 7.8; 7168 x 1024, 16 tokens (64 of
-// 74) 5.6 against 10.8, 64 tokens (128) 17.8 against 11.8.
-template <int kNt>
-bool few_fits(long long clusters) {
-  static std::atomic<int> known;
-  return clusters <= clusters_at_once(w4a16_router_few_kernel<kNt>, kFewCluster, kFewWarps * 32, 0,
-                                      known);
-}
-
 // The fastest shape by an estimate in cycles: waves of clusters, each a CTA's
 // steps at the rate at which an SM takes operands from L2 (50 bytes a cycle
 // were measured) or at which the threads get round their loops, plus the
@@ -501,8 +488,7 @@ bool few_fits(long long clusters) {
 // at most; hidden 7168 x 384 experts, us: 777 tokens 17 (a pair of 128 experts,
 // split by 4: 16; one CTA, split by 4: 18), 4096 tokens 28 (pairs unsplit 35,
 // one CTA 33), 8192 tokens 40 (one CTA 54).
-bool dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a) {
-  bool best_pair = false;
+double dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a, bool* best_pair) {
   double best = 0;
   for (int pair = 0; pair < 2; ++pair)
     for (int width = 64; width <= kMaxTileN; width += 64) {
@@ -529,12 +515,29 @@ bool dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a)
                                      c.tile_n * 28 + (c.split == 1 ? 0 : pair ? 4500 : 3500));
         if (best == 0 || cost < best) {
           best = cost;
-          best_pair = pair != 0;
+          *best_pair = pair != 0;
           *a = c;
         }
       }
     }
-  return best_pair;
+  return best;
+}
+
+// One wave of the few-token kernel is faster than the dense one and two are
+// not, so its clusters are the largest that all run at once, if the columns
+// that a CTA then has (2200 ns and 4.7 a column) take less than the dense kernel
+// needs and, in clusters that have been made smaller, are not more than some
+// 1100 (7168 x 16, 2000 tokens on fours: 14.5 us against 11.0). Hidden 7168 x 384 experts, 64 tokens (48 clusters of eight, 51
+// run at once) 6.4 us against 9.0, 65 tokens 10.6 against 9.0; 2088 x 60, 192
+// tokens 3.8 against 7.6, 777 tokens (fours) 6.2 against 7.8; 7168 x 1024, 16
+// tokens (64 of 74) 5.6 against 10.8; 256 x 64, 2000 tokens 3.4 against 6.1.
+template <int kNt, int kCl>
+bool few_fits(long long clusters, int hidden, double dense_cycles) {
+  static std::atomic<int> known;
+  return clusters <= clusters_at_once(w4a16_router_few_kernel<kNt, kCl>, kCl, kFewWarps * 32, 0,
+                                      known) &&
+         (kCl == 8 || hidden <= 1100 * kCl) &&
+         4200 + 9.0 * hidden / kCl < dense_cycles + 2900;
 }
 
 }  // namespace
@@ -542,18 +545,24 @@ bool dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a)
 cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
                                  int tokens, int hidden, int num_experts, float* logits, int sms,
                                  cudaStream_t stream) {
+  DenseArgs a;
+  bool pair = false;
+  const double dense = dense_shape(tokens, num_experts, hidden, sms, &a, &pair);
   const long long clusters =
       static_cast<long long>(ceil_div(num_experts, kFewExperts)) * ceil_div(tokens, kFewBlock);
-  const auto few = [&](auto kernel) {
-    return launch_dependent(kernel, static_cast<int>(clusters) * kFewCluster, kFewWarps * 32, 0,
-                            kFewCluster, stream, x, x_stride, weight, tokens, hidden, num_experts,
-                            logits);
+  const auto few = [&](auto kernel, int ctas) {
+    return launch_dependent(kernel, static_cast<int>(clusters) * ctas, kFewWarps * 32, 0, ctas,
+                            stream, x, x_stride, weight, tokens, hidden, num_experts, logits);
   };
-  if (tokens <= 8 && few_fits<1>(clusters)) return few(w4a16_router_few_kernel<1>);
-  if (tokens <= 16 && few_fits<2>(clusters)) return few(w4a16_router_few_kernel<2>);
-  if (few_fits<kFewBlock / 8>(clusters)) return few(w4a16_router_few_kernel<kFewBlock / 8>);
-  DenseArgs a;
-  const bool pair = dense_shape(tokens, num_experts, hidden, sms, &a);
+  constexpr int kNt = kFewBlock / 8;
+  if (tokens <= 8 && few_fits<1, 8>(clusters, hidden, dense))
+    return few(w4a16_router_few_kernel<1, 8>, 8);
+  if (tokens <= 16 && few_fits<2, 8>(clusters, hidden, dense))
+    return few(w4a16_router_few_kernel<2, 8>, 8);
+  if (few_fits<kNt, 8>(clusters, hidden, dense)) return few(w4a16_router_few_kernel<kNt, 8>, 8);
+  if (few_fits<kNt, 4>(clusters, hidden, dense)) return few(w4a16_router_few_kernel<kNt, 4>, 4);
+  if (few_fits<kNt, 2>(clusters, hidden, dense)) return few(w4a16_router_few_kernel<kNt, 2>, 2);
+  if (few_fits<kNt, 1>(clusters, hidden, dense)) return few(w4a16_router_few_kernel<kNt, 1>, 1);
   a.logits = logits;
   a.tokens = tokens;
   a.num_experts = num_experts;
