@@ -113,3 +113,8 @@ def test_router_between_the_kernels(cuda_dev, tokens, hidden, experts):
 ])
 def test_router_small_clusters(cuda_dev, tokens, hidden, experts):
     test_router_many_tokens(cuda_dev, tokens, hidden, experts, hidden + 8)
+
+
+def test_router_widest_tiles(cuda_dev):
+    # 256 experts a tile, steps of 64 columns
+    test_router_many_tokens(cuda_dev, 10000, 264, 256, 0)

@@ -168,8 +168,8 @@ struct DenseArgs {
 // Ring slots, a multiple of the threads that take turns: each slot then belongs
 // to one copy and one MMA thread. (In a ring of five a thread could come to a
 // slot two phases ahead of it, which a wait on the phase's parity cannot tell
-// from done.) 4 of 128 columns in a pair at N = 192, 6 of 64 at N = 256, 6 or 8
-// of 64 in a split.
+// from done.) 4 of 128 columns in a pair at N = 192, 6 of 64 at N = 256, 4 to 8
+// of 64 of one CTA.
 int dense_slots(int b_rows, int sub) {
   const int fit = std::min(kMaxRing, kRingBytes / ((kTileM + b_rows) * sub * kKStep * 2));
   return fit / kDensePairs * kDensePairs;
