@@ -118,7 +118,8 @@ __host__ __device__ inline size_t share_floats(int tokens) {
 }
 
 // An MMA operand: `rows` rows of k FP16 values, and of every `block` columns
-// the factor of the values (a row's factors padded to whole stages).
+// the factor of the values (room for a row's factors in whole stages; those of
+// blocks that the row does not have are never written, and not used).
 struct Operand {
   size_t factors, bytes;  // byte offset, total
   int blocks;             // of a row
@@ -288,15 +289,18 @@ __device__ __forceinline__ void half_mma(int valid, uint32_t codes, uint32_t sca
                                          float (&acc)[kMt][2 * kCols]) {
   const auto step = [&](auto st, int n, int next_n) {
     constexpr int kS = decltype(st)::value;
-    float part[kMt][2 * kCols] = {};
-    if (n > 0)  // (a second group that the row does not have has scale 0)
+    if (n > 0) {  // (a second group that the row does not have has scale 0)
+      float part[kMt][2 * kCols] = {};
       step_mma<kCols>(codes + kS * kStepBytes, scales + kS * kStepBytes, x.b[2 * kS],
                          x.b[2 * kS + 1], part);
-    const float f = kS == 0 ? factor.x : factor.y;
+      // (a step that the row does not have has no factor either: what was read
+      // for it is whatever the memory held, and 0 times that may be NaN)
+      const float f = kS == 0 ? factor.x : factor.y;
 #pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
+      for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-      for (int i = 0; i < 2 * kCols; ++i) acc[mt][i] = fmaf(f, part[mt][i], acc[mt][i]);
+        for (int i = 0; i < 2 * kCols; ++i) acc[mt][i] = fmaf(f, part[mt][i], acc[mt][i]);
+    }
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     x.b[2 * kS] = next_n > 0 ? load16(next + kS * 128) : zero;
     x.b[2 * kS + 1] = next_n > 1 ? load16(next + kS * 128 + 64) : zero;
