@@ -5,9 +5,18 @@
 #include <cuda_bf16.h>
 
 #include <cfloat>
+#include <cmath>
 #include <cstdint>
 
 namespace w4a16 {
+
+// An integer that orders logits as they are ordered: 0 (never chosen) for a NaN
+// and for -inf, which masks an expert; the lowest finite value is a logit like
+// any other (key 0x00800000), and -0 counts as +0.
+__device__ __forceinline__ uint32_t logit_key(float v) {
+  const uint32_t bits = __float_as_uint(v + 0.f);
+  return v >= -FLT_MAX ? ((bits >> 31) != 0 ? ~bits : bits | 0x80000000u) : 0u;
+}
 
 // Top-k of token t by one warp (all 32 lanes take part); kPer logits per
 // lane, so num_experts <= 32 * kPer.
@@ -19,9 +28,7 @@ __device__ __forceinline__ void route_token(const void* __restrict__ logits, int
                                             float* __restrict__ topk_weights) {
   const int lane = threadIdx.x & 31;
   // this lane's logits: experts lane, lane + 32, ... (the loads carry no
-  // branch, so that all of them are in flight at once); keys order them as
-  // integers (0: never chosen; -0 counts as +0; a NaN or a value at or below
-  // the lowest finite number is not chosen)
+  // branch, so that all of them are in flight at once)
   float v[kPer];
   uint32_t key[kPer];
   float mx = -FLT_MAX;
@@ -39,11 +46,9 @@ __device__ __forceinline__ void route_token(const void* __restrict__ logits, int
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const bool in = lane + 32 * i < num_experts;
-    if (!in) v[i] = -FLT_MAX;
+    if (lane + 32 * i >= num_experts) v[i] = -INFINITY;
     mx = fmaxf(mx, v[i]);
-    const uint32_t bits = __float_as_uint(v[i] + 0.f);
-    key[i] = v[i] > -FLT_MAX ? ((bits >> 31) != 0 ? ~bits : bits | 0x80000000u) : 0u;
+    key[i] = logit_key(v[i]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -140,10 +145,9 @@ __device__ __forceinline__ void route_token_cta(const void* __restrict__ logits,
   }
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
-    if (32 * (warp + j * kWarps) + lane >= num_experts) v[j] = -FLT_MAX;
+    if (32 * (warp + j * kWarps) + lane >= num_experts) v[j] = -INFINITY;
     mx = fmaxf(mx, v[j]);
-    const uint32_t bits = __float_as_uint(v[j] + 0.f);
-    key[j] = v[j] > -FLT_MAX ? ((bits >> 31) != 0 ? ~bits : bits | 0x80000000u) : 0u;
+    key[j] = logit_key(v[j]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
