@@ -189,14 +189,19 @@ class W4A16MoE:
         for this GPU's experts [expert_offset, expert_offset + num_experts),
         on the device (w4a16_topk_softmax)."""
         tokens = router_logits.shape[0]
-        if not hasattr(self, "_route_ids") or self._route_ids.shape[0] < tokens:
-            self._route_ids = torch.empty((self.max_tokens, self.topk), dtype=torch.int32,
-                                          device=self.device)
-            self._route_w = torch.empty((self.max_tokens, self.topk), dtype=torch.float32,
-                                        device=self.device)
-        out = (self._route_ids[:tokens], self._route_w[:tokens])
         return ops.w4a16_topk_softmax(router_logits, self.topk, renormalize, expert_offset,
-                                      self.num_experts, out=out, stream=stream)
+                                      self.num_experts, out=self._routing(tokens, stream),
+                                      stream=stream)
+
+    def _routing(self, tokens: int, stream):
+        """The layer's own (topk_ids, topk_weights), made by the first call."""
+        if not hasattr(self, "_route_ids"):
+            with ops.on_stream(stream):
+                self._route_ids = torch.empty((self.max_tokens, self.topk), dtype=torch.int32,
+                                              device=self.device)
+                self._route_w = torch.empty((self.max_tokens, self.topk), dtype=torch.float32,
+                                            device=self.device)
+        return self._route_ids[:tokens], self._route_w[:tokens]
 
     def route_align(self, router_logits: torch.Tensor, expert_offset: int = 0,
                     renormalize: bool = True, stream=None):
@@ -205,14 +210,10 @@ class W4A16MoE:
         tokens = router_logits.shape[0]
         if tokens > self.max_tokens:
             raise ValueError("more tokens than the layer was planned for")
-        if not hasattr(self, "_route_ids"):
-            self._route_ids = torch.empty((self.max_tokens, self.topk), dtype=torch.int32,
-                                          device=self.device)
-            self._route_w = torch.empty((self.max_tokens, self.topk), dtype=torch.float32,
-                                        device=self.device)
+        ids, w = self._routing(tokens, stream)
         if not hasattr(self, "_arrivals"):
-            self._arrivals = torch.zeros(1, dtype=torch.int32, device=self.device)
-        ids, w = self._route_ids[:tokens], self._route_w[:tokens]
+            with ops.on_stream(stream):
+                self._arrivals = torch.zeros(1, dtype=torch.int32, device=self.device)
         ops.w4a16_moe_route_align(
             router_logits, self.topk, self.block_m, self._arrivals, renormalize, expert_offset,
             self.num_experts, self.capacity,
@@ -237,7 +238,8 @@ class W4A16MoE:
         if tokens > self.max_tokens:
             raise ValueError("more tokens than the layer was planned for")
         if out is None:
-            out = torch.empty((tokens, self.hidden), dtype=torch.float32, device=x.device)
+            with ops.on_stream(stream):
+                out = torch.empty((tokens, self.hidden), dtype=torch.float32, device=x.device)
         self.align(topk_ids, stream)
         return self.experts(x, topk_weights, out=out, stream=stream)
 
@@ -269,14 +271,8 @@ class W4A16MoE:
         """few_tokens from router logits [T, E_global], the routing in the same
         launch. routing: (topk_ids int32, topk_weights fp32) [T, topk] tensors
         that receive it (the layer's own buffers when None)."""
-        tokens = x.shape[0]
         if routing is None:
-            if not hasattr(self, "_route_ids"):
-                self._route_ids = torch.empty((self.max_tokens, self.topk), dtype=torch.int32,
-                                              device=self.device)
-                self._route_w = torch.empty((self.max_tokens, self.topk), dtype=torch.float32,
-                                            device=self.device)
-            routing = (self._route_ids[:tokens], self._route_w[:tokens])
+            routing = self._routing(x.shape[0], stream)
         return self._few(x, routing[0], routing[1], x_scales, out, stream, logits=router_logits,
                          renormalize=renormalize, expert_offset=expert_offset)
 
@@ -285,7 +281,8 @@ class W4A16MoE:
         """gate_up(+act) and down over the routing tensors already aligned."""
         tokens = x.shape[0]
         if out is None:
-            out = torch.empty((tokens, self.hidden), dtype=torch.float32, device=x.device)
+            with ops.on_stream(stream):
+                out = torch.empty((tokens, self.hidden), dtype=torch.float32, device=x.device)
         if self.single_launch:
             return self.layer_single_launch(x, tokens, topk_weights, out, stream)
         if self.fused_act:

@@ -8,6 +8,7 @@ unloadable library raises ``RuntimeError`` (there is no CPU fallback).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -163,6 +164,14 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def on_stream(stream):
+    """The context in which a call makes its memory: what is allocated (or
+    filled, or copied) inside belongs to the stream that the call runs on, so
+    that the allocator hands it on only behind that stream's work. None: the
+    current stream, as without a context."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 # ------------------------------------------------------------- host only --
 
 def w4a16_version() -> int:
@@ -222,9 +231,10 @@ def w4a16_moe_align_block_size(topk_ids: torch.Tensor, num_experts: int, block_m
         capacity = w4a16_align_capacity(numel, num_experts, block_m)
     dev = topk_ids.device
     if out is None:
-        out = (torch.empty(capacity, dtype=torch.int32, device=dev),
-               torch.empty(capacity // block_m, dtype=torch.int32, device=dev),
-               torch.empty(1, dtype=torch.int32, device=dev))
+        with on_stream(stream):
+            out = (torch.empty(capacity, dtype=torch.int32, device=dev),
+                   torch.empty(capacity // block_m, dtype=torch.int32, device=dev),
+                   torch.empty(1, dtype=torch.int32, device=dev))
     sorted_ids, expert_ids, ntp = out
     _check("w4a16_moe_align_block_size", load_library().w4a16_moe_align_block_size(
         _ptr(topk_ids), tokens, topk, num_experts, block_m, capacity,
@@ -240,7 +250,8 @@ def w4a16_prepack(q: torch.Tensor, scales: torch.Tensor, group: int = 32,
     k = kh * 2
     size = w4a16_prepack_size(e, n, k, group, layout)
     if out is None:
-        out = torch.empty(size, dtype=torch.uint8, device=q.device)
+        with on_stream(stream):
+            out = torch.empty(size, dtype=torch.uint8, device=q.device)
     _check("w4a16_prepack", load_library().w4a16_prepack(
         _ptr(q), _ptr(scales), e, n, k, group, layout, _ptr(out), out.numel(), _stream(stream)))
     return out
@@ -248,8 +259,9 @@ def w4a16_prepack(q: torch.Tensor, scales: torch.Tensor, group: int = 32,
 
 def w4a16_unpack(packed: torch.Tensor, num_experts: int, n: int, k: int,
                  layout: int = W4A16_LAYOUT_KTILE64, stream=None):
-    q = torch.empty((num_experts, n, k // 2), dtype=torch.uint8, device=packed.device)
-    s = torch.empty((num_experts, n, k // 32), dtype=torch.int16, device=packed.device)
+    with on_stream(stream):
+        q = torch.empty((num_experts, n, k // 2), dtype=torch.uint8, device=packed.device)
+        s = torch.empty((num_experts, n, k // 32), dtype=torch.int16, device=packed.device)
     _check("w4a16_unpack", load_library().w4a16_unpack(
         _ptr(packed), num_experts, n, k, layout, _ptr(q), _ptr(s), _stream(stream)))
     return q, s
@@ -279,12 +291,13 @@ def w4a16_moe_indexed_gemm(mode: int, packed: torch.Tensor, num_experts: int, n:
     """GATE_UP: out BF16 [tokens*topk, n]; GATE_UP_SILU: out BF16
     [tokens*topk, n/2]; DOWN: out FP32 [tokens, n]."""
     if out is None:
-        if mode == W4A16_GATE_UP:
-            out = torch.empty((tokens * topk, n), dtype=torch.bfloat16, device=a.device)
-        elif mode == W4A16_GATE_UP_SILU:
-            out = torch.empty((tokens * topk, n // 2), dtype=torch.bfloat16, device=a.device)
-        else:
-            out = torch.empty((tokens, n), dtype=torch.float32, device=a.device)
+        with on_stream(stream):
+            if mode == W4A16_GATE_UP:
+                out = torch.empty((tokens * topk, n), dtype=torch.bfloat16, device=a.device)
+            elif mode == W4A16_GATE_UP_SILU:
+                out = torch.empty((tokens * topk, n // 2), dtype=torch.bfloat16, device=a.device)
+            else:
+                out = torch.empty((tokens, n), dtype=torch.float32, device=a.device)
     _check("w4a16_moe_indexed_gemm", load_library().w4a16_moe_indexed_gemm(
         mode, _ptr(packed), num_experts, n, k, _ptr(a), tokens, topk, _ptr(sorted_ids),
         _ptr(expert_ids), _ptr(num_tokens_padded), sorted_ids.numel(), _ptr(topk_weights),
@@ -300,7 +313,8 @@ def w4a16_moe_grouped_gemm(kind: int, packed: torch.Tensor, num_experts: int, n:
     """CONTIGUOUS: a [m, k] -> out [m, n]; MASKED: a [E, m, k] -> out [E, m, n] (BF16)."""
     if out is None:
         shape = (m, n) if kind == W4A16_GROUPED_CONTIGUOUS else (num_experts, m, n)
-        out = torch.empty(shape, dtype=torch.bfloat16, device=a.device)
+        with on_stream(stream):
+            out = torch.empty(shape, dtype=torch.bfloat16, device=a.device)
     _check("w4a16_moe_grouped_gemm", load_library().w4a16_moe_grouped_gemm(
         kind, _ptr(packed), num_experts, n, k, _ptr(a), m, _ptr(layout), expected_m, _ptr(out),
         flags, None if plan is None else ctypes.byref(plan), _ptr(workspace), workspace.numel(),
@@ -321,7 +335,8 @@ def w4a16_moe_layer(packed_gate_up: torch.Tensor, packed_down: torch.Tensor, num
     """The layer's gate_up (fused activation) and down in one launch:
     out FP32 [tokens, hidden]."""
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=torch.float32, device=x.device)
+        with on_stream(stream):
+            out = torch.empty((tokens, hidden), dtype=torch.float32, device=x.device)
     _check("w4a16_moe_layer", load_library().w4a16_moe_layer(
         _ptr(packed_gate_up), _ptr(packed_down), num_experts, hidden, inter, _ptr(x), tokens,
         topk, _ptr(sorted_ids), _ptr(expert_ids), _ptr(num_tokens_padded), sorted_ids.numel(),
@@ -342,12 +357,14 @@ def w4a16_topk_softmax(logits: torch.Tensor, topk: int, renormalize: bool = True
     if dtype is None:
         raise W4A16Error("w4a16_topk_softmax", W4A16_ERR_INVALID_ARG,
                          f"logits of dtype {logits.dtype}")
-    if out is None:
-        out = (torch.empty((tokens, topk), dtype=torch.int32, device=logits.device),
-               torch.empty((tokens, topk), dtype=torch.float32, device=logits.device))
+    with on_stream(stream):
+        logits = logits.contiguous()
+        if out is None:
+            out = (torch.empty((tokens, topk), dtype=torch.int32, device=logits.device),
+                   torch.empty((tokens, topk), dtype=torch.float32, device=logits.device))
     ids, w = out
     _check("w4a16_topk_softmax", load_library().w4a16_topk_softmax(
-        _ptr(logits.contiguous()), dtype, tokens, e, topk, int(bool(renormalize)), expert_offset,
+        _ptr(logits), dtype, tokens, e, topk, int(bool(renormalize)), expert_offset,
         num_local_experts, _ptr(ids), _ptr(w), _stream(stream)))
     return ids, w
 
@@ -369,14 +386,15 @@ def w4a16_moe_route_align(logits: torch.Tensor, topk: int, block_m: int,
     if capacity is None:
         capacity = w4a16_align_capacity(tokens * topk, num_local_experts, block_m)
     dev = logits.device
-    if out is None:
-        out = (torch.empty((tokens, topk), dtype=torch.int32, device=dev),
-               torch.empty((tokens, topk), dtype=torch.float32, device=dev),
-               torch.empty(capacity, dtype=torch.int32, device=dev),
-               torch.empty(capacity // block_m, dtype=torch.int32, device=dev),
-               torch.empty(1, dtype=torch.int32, device=dev))
+    with on_stream(stream):
+        logits = logits.contiguous()
+        if out is None:
+            out = (torch.empty((tokens, topk), dtype=torch.int32, device=dev),
+                   torch.empty((tokens, topk), dtype=torch.float32, device=dev),
+                   torch.empty(capacity, dtype=torch.int32, device=dev),
+                   torch.empty(capacity // block_m, dtype=torch.int32, device=dev),
+                   torch.empty(1, dtype=torch.int32, device=dev))
     ids, w, sorted_ids, expert_ids, ntp = out
-    logits = logits.contiguous()
     _check("w4a16_moe_route_align", load_library().w4a16_moe_route_align(
         _ptr(logits), dtype, tokens, e, topk, int(bool(renormalize)), expert_offset,
         num_local_experts, block_m, sorted_ids.numel(), _ptr(ids), _ptr(w), _ptr(sorted_ids),
@@ -388,7 +406,8 @@ def w4a16_silu_and_mul(x: torch.Tensor, out: Optional[torch.Tensor] = None, stre
     rows, two_i = x.shape
     inter = two_i // 2
     if out is None:
-        out = torch.empty((rows, inter), dtype=torch.bfloat16, device=x.device)
+        with on_stream(stream):
+            out = torch.empty((rows, inter), dtype=torch.bfloat16, device=x.device)
     _check("w4a16_silu_and_mul", load_library().w4a16_silu_and_mul(
         _ptr(x), rows, inter, _ptr(out), _stream(stream)))
     return out
@@ -465,12 +484,11 @@ def w4a16_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             raise W4A16Error(fn, W4A16_ERR_UNSUPPORTED, f"fp8_group {fp8_group}")
         groups = (rows, 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP))
     if out is None:
-        out = (torch.empty(shape, dtype=torch.bfloat16, device=x.device) if bf16_out else None,
-               torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-               if residual is not None else None,
-               torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
-               if fp8_group else None,
-               torch.empty(groups, dtype=torch.float32, device=x.device) if fp8_group else None)
+        kinds = ((shape, _BF16, bf16_out), (shape, _BF16, residual is not None),
+                 (shape, _E4M3, fp8_group), (groups, _F32, fp8_group))
+        with on_stream(stream):
+            out = tuple(torch.empty(size, dtype=dtype, device=x.device) if wanted else None
+                        for size, dtype, wanted in kinds)
     y, res_out, y8, scales = out
     _check(fn, load_library().w4a16_add_rms_norm(
         x_at, x_stride, r_at, r_stride, w_at, eps, rows, hidden,
@@ -490,7 +508,8 @@ def w4a16_router_logits(x: torch.Tensor, weight: torch.Tensor,
     experts = weight.shape[0]
     w_at = _need(fn, "weight", weight, _BF16, (experts, hidden))
     if out is None:
-        out = torch.empty((tokens, experts), dtype=torch.float32, device=x.device)
+        with on_stream(stream):
+            out = torch.empty((tokens, experts), dtype=torch.float32, device=x.device)
     _check(fn, load_library().w4a16_router_logits(
         x_at, x_stride, w_at, tokens, hidden, experts,
         _need(fn, "out", out, _F32, (tokens, experts)), _raw_stream(x, stream)))
@@ -530,7 +549,8 @@ def w4a16_moe_few_tokens(packed_gate_up: torch.Tensor, packed_down: torch.Tensor
         experts = logits.shape[1]
         lg_at = _need(fn, "logits", logits, dtype, (tokens, experts))
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=torch.float32, device=x.device)
+        with on_stream(stream):
+            out = torch.empty((tokens, hidden), dtype=torch.float32, device=x.device)
     # 128-row tiles of 64-column steps, 4608 bytes each
     gate_up_size = num_experts * -(-2 * inter // 128) * -(-hidden // 64) * 4608
     down_size = num_experts * -(-hidden // 128) * -(-inter // 64) * 4608
@@ -568,10 +588,11 @@ def w4a16_moe_indexed_gemm_noalloc(mode: int, packed: torch.Tensor, num_experts:
     as the workspace. Only ``out`` is allocated here when the caller passes
     none (a caller that cannot allocate passes its own)."""
     if out is None:
-        if mode == W4A16_GATE_UP:
-            out = torch.empty((tokens * topk, n), dtype=torch.bfloat16, device=a.device)
-        else:
-            out = torch.empty((tokens, n), dtype=torch.float32, device=a.device)
+        with on_stream(stream):
+            if mode == W4A16_GATE_UP:
+                out = torch.empty((tokens * topk, n), dtype=torch.bfloat16, device=a.device)
+            else:
+                out = torch.empty((tokens, n), dtype=torch.float32, device=a.device)
     _check("w4a16_moe_indexed_gemm_noalloc", load_library().w4a16_moe_indexed_gemm_noalloc(
         mode, _ptr(packed), num_experts, n, k, _ptr(a), tokens, topk, _ptr(sorted_ids),
         _ptr(expert_ids), _ptr(num_tokens_padded), sorted_ids.numel(), _ptr(topk_weights),
