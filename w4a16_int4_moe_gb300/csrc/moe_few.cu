@@ -396,6 +396,21 @@ __device__ __forceinline__ bool epilogue_arrive(int* counter, int last, int* fla
   return *flag != 0;
 }
 
+// One warp of a CTA that has used the counters for the last time. The last CTA
+// to say so leaves all of them zero for the next call, whatever it did itself:
+// after a wait that gave up the CTAs may have read different routings.
+__device__ __forceinline__ void leave_counters(FewCounters* counters, int lane) {
+  int last = 0;
+  if (lane == 0) last = atomicAdd(&counters->exits, 1) == static_cast<int>(gridDim.x) - 1;
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
+  for (int i = lane; i < 2 * kMaxCtas; i += 32) counters->item[0][i] = 0;
+  if (lane == 0) {
+    counters->act_done = 0;
+    counters->rows_done = 0;
+    counters->exits = 0;
+  }
+}
+
 __device__ __forceinline__ void slot_next(int& slot, uint32_t& phase, int step, int slots) {
   slot += step;
   if (slot >= slots) {
@@ -678,12 +693,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
            i < static_cast<long long>(a.tokens) * a.hidden;
            i += static_cast<long long>(gridDim.x) * kFewThreads)
         a.out[i] = 0.f;
-    if (tid == 0) {
+    if (warp == 0) {
       gpu_fence();
-      if (atomicAdd(&counters->exits, 1) == static_cast<int>(gridDim.x) - 1) {
-        counters->rows_done = 0;
-        counters->exits = 0;
-      }
+      leave_counters(counters, lane);
     }
     return;
   }
@@ -977,20 +989,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) w4a16_moe_few_kernel(const Few
     const int etid = tid - 32 * kWarpEpilogue0;
     bool live = true;
     uint32_t items = 0;  // sums taken, the two buffers by turns
-    // This CTA has used the counters for the last time (the first warp calls
-    // it); the last one to say so leaves them zero for the next call.
     const auto leave = [&]() {
-      if (etid >= 32) return;
-      int last = 0;
-      if (etid == 0)
-        last = atomicAdd(&counters->exits, 1) == static_cast<int>(gridDim.x) - 1;
-      if (!__shfl_sync(0xffffffffu, last, 0)) return;
-      for (int i = etid; i < 2 * kMaxCtas; i += 32) counters->item[0][i] = 0;
-      if (etid == 0) {
-        counters->act_done = 0;
-        counters->rows_done = 0;
-        counters->exits = 0;
-      }
+      if (etid < 32) leave_counters(counters, etid);
     };
     if (gu_count > 0) {
       const int S = gu.stages;
