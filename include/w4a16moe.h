@@ -481,8 +481,9 @@ w4a16_status w4a16_add_rms_norm(const uint16_t* x, long long x_stride, const uin
  * hidden a multiple of 8, num_experts at most 1024 (else
  * W4A16_ERR_UNSUPPORTED), x_stride a multiple of 8 and at least hidden, x and
  * weight 16-byte and logits 4-byte aligned (else W4A16_ERR_INVALID_ARG). The
- * order of the additions depends on the sizes only. No workspace, no host
- * synchronisation: graph-capturable.
+ * order of the additions depends on the sizes and on how many thread-block
+ * clusters the device runs at once: repeated calls on a device give the same
+ * bits. No workspace, no host synchronisation: graph-capturable.
  */
 w4a16_status w4a16_router_logits(const uint16_t* x, long long x_stride, const uint16_t* weight,
                                  int tokens, int hidden, int num_experts, float* logits,

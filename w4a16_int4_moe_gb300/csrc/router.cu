@@ -14,7 +14,8 @@
 //     tiles are fewer than the SMs, a cluster of up to eight CTAs splits the
 //     columns of one.
 //
-// The order of the additions follows from the sizes alone.
+// The order of the additions follows from the sizes and from how many clusters
+// the device runs at once.
 //
 // 384 experts of hidden 7168, in a graph: 1 token 3.2 us, 48 tokens 6.5 us, both
 // latency (launch, one round of loads, the cluster's exchange; the weight alone
@@ -448,11 +449,18 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 
 namespace {
 
-// How many clusters of `ctas` run at once (they stay inside a GPC, so eights of
-// one CTA an SM leave some SMs out); 0 if that cannot be said.
+// How many clusters of a kernel run at once, by device (0: not asked yet).
+constexpr int kMaxDevices = 64;
+using ClustersAtOnce = std::atomic<int>[kMaxDevices];
+
+// How many clusters of `ctas` run at once on the current device (they stay
+// inside a GPC, so eights of one CTA an SM leave some SMs out). 0 and an error
+// if that cannot be said: a guess would let the same sizes take another order
+// of additions in one call than in the next.
 template <typename Kernel>
-int clusters_at_once(Kernel kernel, int ctas, int threads, size_t smem, std::atomic<int>& known) {
-  if (const int n = known) return n;
+int clusters_at_once(Kernel kernel, int ctas, int threads, size_t smem, ClustersAtOnce& known,
+                     int device, cudaError_t* error) {
+  if (const int n = known[device]) return n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -464,20 +472,24 @@ int clusters_at_once(Kernel kernel, int ctas, int threads, size_t smem, std::ato
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem)) != cudaSuccess)
+  cudaError_t e = cudaSuccess;
+  if (smem > 0)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  if (e != cudaSuccess) {
+    *error = e;
     return 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
-  known = n;
+  }
+  known[device] = n;
   return n;
 }
 
-int dense_clusters_at_once(int ctas, int sms) {
-  static std::atomic<int> known[kMaxSplit + 1];
+int dense_clusters_at_once(int ctas, int sms, int device, cudaError_t* error) {
+  static ClustersAtOnce known[kMaxSplit + 1];
   if (ctas == 1) return sms;
-  const int n = clusters_at_once(w4a16_router_dense_kernel<false, 1>, ctas, kDenseThreads,
-                                 kRingBytes + 2048, known[ctas]);
-  return n > 0 ? n : std::max(1, sms / (2 * ctas));
+  return std::max(1, clusters_at_once(w4a16_router_dense_kernel<false, 1>, ctas, kDenseThreads,
+                                      kRingBytes + 2048, known[ctas], device, error));
 }
 
 // The fastest shape by an estimate in cycles: waves of clusters, each a CTA's
@@ -488,7 +500,8 @@ int dense_clusters_at_once(int ctas, int sms) {
 // at most; hidden 7168 x 384 experts, us: 777 tokens 17 (a pair of 128 experts,
 // split by 4: 16; one CTA, split by 4: 18), 4096 tokens 28 (pairs unsplit 35,
 // one CTA 33), 8192 tokens 40 (one CTA 54).
-double dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* a, bool* best_pair) {
+double dense_shape(int tokens, int num_experts, int hidden, int sms, int device, DenseArgs* a,
+                   bool* best_pair, cudaError_t* error) {
   double best = 0;
   for (int pair = 0; pair < 2; ++pair)
     for (int width = 64; width <= kMaxTileN; width += 64) {
@@ -510,7 +523,7 @@ double dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* 
       for (c.split = 1; c.split * (pair ? 2 : 1) <= kMaxSplit && c.split <= c.k_steps; c.split *= 2) {
         if (c.split > 1 && 2 * tile_sums_bytes(c.tile_n) > kRingBytes) break;
         const int ctas = c.split * (pair ? 2 : 1);
-        const double waves = std::ceil(tiles / dense_clusters_at_once(ctas, sms));
+        const double waves = std::ceil(tiles / dense_clusters_at_once(ctas, sms, device, error));
         const double cost = waves * (ceil_div(c.k_steps, c.split) * step_cycles + 3000 +
                                      c.tile_n * 28 + (c.split == 1 ? 0 : pair ? 4500 : 3500));
         if (best == 0 || cost < best) {
@@ -532,10 +545,11 @@ double dense_shape(int tokens, int num_experts, int hidden, int sms, DenseArgs* 
 // tokens 3.8 against 7.6, 777 tokens (fours) 6.2 against 7.8; 7168 x 1024, 16
 // tokens (64 of 74) 5.6 against 10.8; 256 x 64, 2000 tokens 3.4 against 6.1.
 template <int kNt, int kCl>
-bool few_fits(long long clusters, int hidden, double dense_cycles) {
-  static std::atomic<int> known;
+bool few_fits(long long clusters, int hidden, double dense_cycles, int device,
+              cudaError_t* error) {
+  static ClustersAtOnce known;
   return clusters <= clusters_at_once(w4a16_router_few_kernel<kNt, kCl>, kCl, kFewWarps * 32, 0,
-                                      known) &&
+                                      known, device, error) &&
          (kCl == 8 || hidden <= 1100 * kCl) &&
          4200 + 9.0 * hidden / kCl < dense_cycles + 2900;
 }
@@ -547,22 +561,32 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
                                  cudaStream_t stream) {
   DenseArgs a;
   bool pair = false;
-  const double dense = dense_shape(tokens, num_experts, hidden, sms, &a, &pair);
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device >= kMaxDevices) return cudaErrorInvalidDevice;
+  const double dense = dense_shape(tokens, num_experts, hidden, sms, device, &a, &pair, &e);
   const long long clusters =
       static_cast<long long>(ceil_div(num_experts, kFewExperts)) * ceil_div(tokens, kFewBlock);
   const auto few = [&](auto kernel, int ctas) {
+    if (e != cudaSuccess) return e;
     return launch_dependent(kernel, static_cast<int>(clusters) * ctas, kFewWarps * 32, 0, ctas,
                             stream, x, x_stride, weight, tokens, hidden, num_experts, logits);
   };
   constexpr int kNt = kFewBlock / 8;
-  if (tokens <= 8 && few_fits<1, 8>(clusters, hidden, dense))
+  if (tokens <= 8 && few_fits<1, 8>(clusters, hidden, dense, device, &e))
     return few(w4a16_router_few_kernel<1, 8>, 8);
-  if (tokens <= 16 && few_fits<2, 8>(clusters, hidden, dense))
+  if (tokens <= 16 && few_fits<2, 8>(clusters, hidden, dense, device, &e))
     return few(w4a16_router_few_kernel<2, 8>, 8);
-  if (few_fits<kNt, 8>(clusters, hidden, dense)) return few(w4a16_router_few_kernel<kNt, 8>, 8);
-  if (few_fits<kNt, 4>(clusters, hidden, dense)) return few(w4a16_router_few_kernel<kNt, 4>, 4);
-  if (few_fits<kNt, 2>(clusters, hidden, dense)) return few(w4a16_router_few_kernel<kNt, 2>, 2);
-  if (few_fits<kNt, 1>(clusters, hidden, dense)) return few(w4a16_router_few_kernel<kNt, 1>, 1);
+  if (few_fits<kNt, 8>(clusters, hidden, dense, device, &e))
+    return few(w4a16_router_few_kernel<kNt, 8>, 8);
+  if (few_fits<kNt, 4>(clusters, hidden, dense, device, &e))
+    return few(w4a16_router_few_kernel<kNt, 4>, 4);
+  if (few_fits<kNt, 2>(clusters, hidden, dense, device, &e))
+    return few(w4a16_router_few_kernel<kNt, 2>, 2);
+  if (few_fits<kNt, 1>(clusters, hidden, dense, device, &e))
+    return few(w4a16_router_few_kernel<kNt, 1>, 1);
+  if (e != cudaSuccess) return e;
   a.logits = logits;
   a.tokens = tokens;
   a.num_experts = num_experts;
@@ -576,8 +600,8 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
   const auto kernel = !pair ? w4a16_router_dense_kernel<false, 1>
                       : a.sub == 1 ? w4a16_router_dense_kernel<true, 1>
                                    : w4a16_router_dense_kernel<true, 2>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 2048);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kRingBytes + 2048);
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, static_cast<int>(grid), kDenseThreads, dense_smem(a), ctas,
                           stream, a);
