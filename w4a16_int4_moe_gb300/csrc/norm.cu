@@ -5,7 +5,8 @@
 //   BF16 residual, the BF16 y and the e4m3 y / scale are each rounded once.
 //   scale = max(amax |y|, 1e-10) / 448 of a 128-column group or of the row
 //   (448 is the largest e4m3 value; the floor keeps the scale a normal number,
-//   so that an all-zero group divides to zero).
+//   so that an all-zero group divides to zero; a group or row with an infinity
+//   or a NaN has a NaN scale and NaN codes).
 //
 // Bound by memory for many rows, by latency for few: 8192 rows of 7168 with a
 // residual, BF16 and 8-bit outputs and group scales take 79 us, 6.7 TB/s of the
@@ -54,6 +55,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The scale of a group or row with this amax: NaN also beside an infinity
+// (infinity * 0), whose finite neighbours would become zeros that decode to NaN.
+__device__ __forceinline__ float group_scale(float amax) {
+  return __fdiv_rn(fmaf(amax, 0.f, amax), kE4m3Max);
 }
 
 // eight values times the scale's reciprocal, rounded to e4m3 (the product is
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) w4a16_add_rms_norm_kernel(const Norm
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float scale = __fdiv_rn(top, kE4m3Max);
+    const float scale = group_scale(top);
     if (k < a.hidden) {
       *reinterpret_cast<uint2*>(a.out_fp8 + at + k) = codes8(h[c], scale);
       if ((threadIdx.x & 15) == 0)
@@ -172,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) w4a16_add_rms_norm_kernel(const Norm
   }
   if (a.fp8_group != W4A16_FP8_ROW) return;
   amax = row_join<kThreads>(amax, part[1], [](float p, float q) { return max_nan(p, q); });
-  const float scale = __fdiv_rn(amax, kE4m3Max);
+  const float scale = group_scale(amax);
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
     const int k = 8 * (c * kThreads + static_cast<int>(threadIdx.x));
