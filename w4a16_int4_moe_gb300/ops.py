@@ -478,7 +478,7 @@ def w4a16_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         r_at, r_rows, r_cols, r_stride = _rows(fn, "residual", residual)
         if r_rows != rows or r_cols != hidden:
             _refuse(fn, f"residual {tuple(residual.shape)} for x {tuple(x.shape)}")
-    shape, groups = (rows, hidden), None
+    shape, groups = (rows, hidden), (rows, 0)
     if fp8_group != W4A16_FP8_NONE:
         if fp8_group not in (W4A16_FP8_ROW, W4A16_FP8_GROUP):
             raise W4A16Error(fn, W4A16_ERR_UNSUPPORTED, f"fp8_group {fp8_group}")
