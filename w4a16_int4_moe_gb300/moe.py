@@ -188,13 +188,15 @@ class W4A16MoE:
         """Router logits [T, E_global] (fp32 or BF16) -> (topk_ids, topk_weights)
         for this GPU's experts [expert_offset, expert_offset + num_experts),
         on the device (w4a16_topk_softmax)."""
-        tokens = router_logits.shape[0]
         return ops.w4a16_topk_softmax(router_logits, self.topk, renormalize, expert_offset,
-                                      self.num_experts, out=self._routing(tokens, stream),
+                                      self.num_experts,
+                                      out=self._routing(router_logits.shape[0], stream),
                                       stream=stream)
 
     def _routing(self, tokens: int, stream):
         """The layer's own (topk_ids, topk_weights), made by the first call."""
+        if tokens > self.max_tokens:
+            raise ValueError("more tokens than the layer was planned for")
         if not hasattr(self, "_route_ids"):
             with ops.on_stream(stream):
                 self._route_ids = torch.empty((self.max_tokens, self.topk), dtype=torch.int32,
@@ -207,10 +209,7 @@ class W4A16MoE:
                     renormalize: bool = True, stream=None):
         """route() and align() in one launch (w4a16_moe_route_align): returns
         (topk_ids, topk_weights) and fills the layer's routing tensors."""
-        tokens = router_logits.shape[0]
-        if tokens > self.max_tokens:
-            raise ValueError("more tokens than the layer was planned for")
-        ids, w = self._routing(tokens, stream)
+        ids, w = self._routing(router_logits.shape[0], stream)
         if not hasattr(self, "_arrivals"):
             with ops.on_stream(stream):
                 self._arrivals = torch.zeros(1, dtype=torch.int32, device=self.device)
