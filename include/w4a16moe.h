@@ -506,7 +506,7 @@ size_t w4a16_moe_few_tokens_workspace_size(int tokens, int topk, int hidden, int
  * e = topk_ids[t, s], over the picks of this GPU's experts. Unlike the indexed
  * GEMMs it rounds nothing to BF16 in between: sums are FP32, the weights are
  * (q - 8) times the scale applied in FP32, and the operands of the products
- * are FP16 numbers times a power of two per block: x exactly down to 2^-28 of
+ * are FP16 numbers times a power of two per block: x exactly down to 2^-27 of
  * its 128-column block's largest value, the activation in two parts, 22 bits
  * from its 64-column block's largest. It adds in an order that depends only on
  * the sizes and the routing: repeated calls give the same bits. An expert's

@@ -34,7 +34,7 @@
 //     pairs q - 8 for BF16 MMAs 0.55. e4m3 MMAs, for which the code bytes would
 //     do as they are, cost more: mma.sync converts their operands;
 //   * the rows are put into FP16 first, times a power of two per block of 128
-//     columns (a BF16 value fits exactly down to 2^-28 of its block's largest;
+//     columns (a BF16 value fits exactly down to 2^-27 of its block's largest;
 //     rows in e4m3 fit as they are); the FP32 activation goes into two FP16
 //     parts per block of 64, 22 bits, each part a column of the MMA;
 //   * two warps finish the items from shared memory while the others go on.
