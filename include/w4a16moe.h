@@ -509,7 +509,7 @@ size_t w4a16_moe_few_tokens_workspace_size(int tokens, int topk, int hidden, int
  * are FP16 numbers times a power of two per block: x exactly down to 2^-27 of
  * its 128-column block's largest value, the activation in two parts, 22 bits
  * from its 64-column block's largest. It adds in an order that depends only on
- * the sizes and the routing: repeated calls give the same bits. An expert's
+ * the sizes, the routing and the device's SMs: repeated calls give the same bits. An expert's
  * weights are read once per four of its rows.
  *   packed_gate_up  [num_experts, 2*inter, hidden], W4A16_LAYOUT_KTILE64_GLU16;
  *   packed_down     [num_experts, hidden, inter], W4A16_LAYOUT_KTILE64;

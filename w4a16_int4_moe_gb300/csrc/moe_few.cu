@@ -42,7 +42,8 @@
 // An item (gate_up: one tile of one expert; down: one tile over all experts)
 // may be cut between CTAs: each writes its FP32 share to the workspace and
 // the CTA that arrives last adds the shares in order. Nothing is added with
-// atomics, so the result depends only on the sizes and the routing.
+// atomics, so the result depends only on the sizes, the routing and the number
+// of CTAs.
 //
 // Measured, hidden 7168, top-8 of 384: 48 local experts of inter 2048, 32
 // tokens: 134 us for 719 MB, 5.4 TB/s (0.79 of the copy rate); 384 experts of

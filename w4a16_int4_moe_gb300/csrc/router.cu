@@ -18,8 +18,8 @@
 // the device runs at once.
 //
 // 384 experts of hidden 7168, in a graph: 1 token 3.2 us, 48 tokens 6.5 us, both
-// latency (launch, one round of loads, the cluster's exchange; the weight alone
-// is 0.8 us of the copy rate). 8192 tokens: 40 us, 1.1 PFLOP/s, 0.59 of a
+// latency (launch, one round of loads, two for 48 tokens, the cluster's exchange;
+// the weight alone is 0.8 us of the copy rate). 8192 tokens: 40 us, 1.1 PFLOP/s, 0.59 of a
 // library product's rate, on 128 of 152 SMs: 7 us are launch, first loads and
 // the logits' way out, the rest is bound by the operands' way into an SM
 // (28 KB of 64 columns at 50 bytes a cycle, against 384 cycles of MMAs).

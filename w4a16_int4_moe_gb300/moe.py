@@ -299,9 +299,11 @@ class MoEBlock:
 
     Up to W4A16_FEW_TOKENS_MAX tokens (with GLU16 gate_up weights) take three
     launches: norm, router, experts; more tokens take the layer's GEMM path
-    (W4A16MoE.forward_from_logits). fp8_rows=True hands the few-token experts
-    the norm's 8-bit rows (the form that tokens have after an exchange in 8
-    bits); the router always reads the BF16 rows."""
+    (W4A16MoE.forward_from_logits). (The limit is the few-token call's own: with
+    many rows an expert the GEMM path may be faster before it.) fp8_rows=True
+    hands the few-token experts the norm's 8-bit rows (the form that tokens have
+    after an exchange in 8 bits) and has no effect on the GEMM path; the router
+    always reads the BF16 rows."""
 
     def __init__(self, norm_weight: torch.Tensor, router_weight: torch.Tensor, experts: W4A16MoE,
                  eps: float = 1e-6, expert_offset: int = 0, renormalize: bool = True,
