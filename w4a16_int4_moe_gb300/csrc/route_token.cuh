@@ -27,29 +27,26 @@ __device__ __forceinline__ void route_token(const void* __restrict__ logits, int
                                             int32_t* __restrict__ topk_ids,
                                             float* __restrict__ topk_weights) {
   const int lane = threadIdx.x & 31;
-  // this lane's logits: experts lane, lane + 32, ... (the loads carry no
-  // branch, so that all of them are in flight at once)
+  // this lane's logits: experts lane, lane + 32, ... (predicated loads from one
+  // address: all of them are in flight at once, and addresses of their own would
+  // take more registers than the logits)
   float v[kPer];
-  uint32_t key[kPer];
   float mx = -FLT_MAX;
-  const long long row = static_cast<long long>(t) * num_experts;
+  const long long first = static_cast<long long>(t) * num_experts + lane;
+  const int mine = num_experts - lane;
   if (bf16_logits) {
-    const uint16_t* from = static_cast<const uint16_t*>(logits) + row;
+    const uint16_t* from = static_cast<const uint16_t*>(logits) + first;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      v[i] = __uint_as_float(
-          static_cast<uint32_t>(__ldg(from + min(lane + 32 * i, num_experts - 1))) << 16);
+      v[i] = 32 * i < mine ? __uint_as_float(static_cast<uint32_t>(__ldg(from + 32 * i)) << 16)
+                           : -INFINITY;
   } else {
-    const float* from = static_cast<const float*>(logits) + row;
+    const float* from = static_cast<const float*>(logits) + first;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = __ldg(from + min(lane + 32 * i, num_experts - 1));
+    for (int i = 0; i < kPer; ++i) v[i] = 32 * i < mine ? __ldg(from + 32 * i) : -INFINITY;
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (lane + 32 * i >= num_experts) v[i] = -INFINITY;
-    mx = fmaxf(mx, v[i]);
-    key[i] = logit_key(v[i]);
-  }
+  for (int i = 0; i < kPer; ++i) mx = fmaxf(mx, v[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float sum = 0.f;
@@ -59,6 +56,9 @@ __device__ __forceinline__ void route_token(const void* __restrict__ logits, int
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
 
+  uint32_t key[kPer];  // (from here on in place of the logits)
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = logit_key(v[i]);
   // k rounds of arg-max (largest logit, then lowest id) over the lanes' own
   // best ones, two warp reductions a round. A lane keeps its two largest; it
   // looks through its others only when it has lost both. Lane s keeps round s.
