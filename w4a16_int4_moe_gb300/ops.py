@@ -164,12 +164,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def on_stream(stream):
     """The context in which a call makes its memory: what is allocated (or
     filled, or copied) inside belongs to the stream that the call runs on, so
     that the allocator hands it on only behind that stream's work. None: the
     current stream, as without a context."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 # ------------------------------------------------------------- host only --
@@ -357,9 +360,11 @@ def w4a16_topk_softmax(logits: torch.Tensor, topk: int, renormalize: bool = True
     if dtype is None:
         raise W4A16Error("w4a16_topk_softmax", W4A16_ERR_INVALID_ARG,
                          f"logits of dtype {logits.dtype}")
-    with on_stream(stream):
-        logits = logits.contiguous()
-        if out is None:
+    if not logits.is_contiguous():
+        with on_stream(stream):
+            logits = logits.contiguous()
+    if out is None:
+        with on_stream(stream):
             out = (torch.empty((tokens, topk), dtype=torch.int32, device=logits.device),
                    torch.empty((tokens, topk), dtype=torch.float32, device=logits.device))
     ids, w = out
@@ -386,9 +391,11 @@ def w4a16_moe_route_align(logits: torch.Tensor, topk: int, block_m: int,
     if capacity is None:
         capacity = w4a16_align_capacity(tokens * topk, num_local_experts, block_m)
     dev = logits.device
-    with on_stream(stream):
-        logits = logits.contiguous()
-        if out is None:
+    if not logits.is_contiguous():
+        with on_stream(stream):
+            logits = logits.contiguous()
+    if out is None:
+        with on_stream(stream):
             out = (torch.empty((tokens, topk), dtype=torch.int32, device=dev),
                    torch.empty((tokens, topk), dtype=torch.float32, device=dev),
                    torch.empty(capacity, dtype=torch.int32, device=dev),
