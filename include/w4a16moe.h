@@ -549,6 +549,90 @@ w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed
                                   size_t ws_bytes, void* stream);
 
 /*
+ * A product with one INT4 weight for a few tokens: a dense projection, or a
+ * shared expert, in the routed experts' own format.
+ *   out[t, r] = addend[t, r] + sum over c of x[t, c] * (q[r, c] - 8) * scale
+ *   (W4A16_LAYOUT_KTILE64, out [tokens, n]), or, gated
+ *   (W4A16_LAYOUT_KTILE64_GLU16: weight rows [gate; up], out [tokens, n/2]),
+ *   out[t, i] = silu(x[t] . Wgate_i^T) * (x[t] . Wup_i^T).
+ * The codes and x enter the products exactly, the scale is applied to a
+ * group's FP32 sum, sums are FP32, and the result is rounded once.
+ *   packed  w4a16_prepack's blob of one expert, [1, n, k] in `layout`;
+ *   x       BF16 [tokens, k], row stride x_stride elements;
+ *   addend  FP32 [tokens, n] or NULL (it may be out itself; gated: NULL);
+ *   out     out_dtype (W4A16_DTYPE_F32 or W4A16_DTYPE_BF16), rows contiguous.
+ * tokens at most W4A16_FEW_TOKENS_MAX, k a multiple of 32, n at least 1 (GLU16: a
+ * multiple of 128), both at most 2^20 (else W4A16_ERR_UNSUPPORTED); x_stride a
+ * multiple of 8 and at least k, pointers 16-byte aligned (else
+ * W4A16_ERR_INVALID_ARG). The order of the additions depends on the sizes and
+ * on the device: repeated calls give the same bits. More tokens: the GEMM
+ * calls, with one expert. No workspace, no host synchronisation: graph-capturable.
+ */
+w4a16_status w4a16_linear_few_tokens(const void* packed, int layout, int n, int k,
+                                     const uint16_t* x, long long x_stride, int tokens,
+                                     const float* addend, void* out, int out_dtype, void* stream);
+
+/*
+ * The products of an expert whose weights are BF16 (a shared expert, the dense
+ * layers of a model), for any number of tokens:
+ *   out[t, r] = addend[t, r] + x[t] . weight[r]^T              (gated == 0)
+ *   out[t, i] = silu(x[t] . weight[i]^T) * (x[t] . weight[n/2 + i]^T)  (gated != 0)
+ * FP32 sums, one rounding of the result.
+ *   weight  BF16 [n, k]; gated: n/2 gate rows, then n/2 up rows;
+ *   x       BF16 [tokens, k], row stride x_stride elements;
+ *   addend  FP32 [tokens, n] or NULL (it may be out itself; gated: NULL);
+ *   out     out_dtype (W4A16_DTYPE_F32 or W4A16_DTYPE_BF16) [tokens, n], gated
+ *           [tokens, n/2].
+ * k a multiple of 8, n at least 1 (gated: even), both at most 2^20, tokens at
+ * most 2^24 (else W4A16_ERR_UNSUPPORTED); x_stride a multiple of 8, at least k and below 2^31,
+ * pointers 16-byte aligned (else W4A16_ERR_INVALID_ARG). The order of the
+ * additions depends on the sizes and on the device: repeated calls give the same
+ * bits. No workspace, no host synchronisation: graph-capturable.
+ */
+w4a16_status w4a16_dense(const uint16_t* weight, int n, int k, int gated, const uint16_t* x,
+                         long long x_stride, int tokens, const float* addend, void* out,
+                         int out_dtype, void* stream);
+
+/*
+ * What stands between a block (the experts) and the next one: the norm of the
+ * block's output, its gate and scales, the residual, the next block's norm.
+ *   p = x * rsqrt(mean(x^2) + eps) * (post_weight + weight_offset)
+ *                                            (p = x when post_weight is NULL)
+ *   h = residual_scale * residual + branch_scale * gate * p
+ *                        (without residual or gate: without that term, factor)
+ *   h_out = bf16(h)
+ *   y = h * rsqrt(mean(h^2) + eps) * (pre_weight + weight_offset)
+ *                                                  (from the unrounded h)
+ *   out = bf16(y); out_fp8 and scales of y as in w4a16_add_rms_norm.
+ * FP32 throughout.
+ *   x        x_dtype (W4A16_DTYPE_F32: what the experts leave, or
+ *            W4A16_DTYPE_BF16) [rows, hidden], row stride x_stride elements;
+ *   post_weight, pre_weight  BF16 [hidden]; post_weight may be NULL, and
+ *            pre_weight exactly when out and out_fp8 are (no norm behind the
+ *            residual, fp8_group W4A16_FP8_NONE);
+ *   gate     BF16 [rows, hidden], row stride gate_stride, or one row for all
+ *            (gate_stride 0), or NULL;
+ *   residual BF16 [rows, hidden], row stride residual_stride, or NULL;
+ *   out, h_out  BF16 [rows, hidden]; h_out may be NULL when out or out_fp8 is
+ *            given, and it may be residual itself when residual_stride ==
+ *            hidden; no other output may overlap an input;
+ *   out_fp8, scales, fp8_group  as in w4a16_add_rms_norm.
+ * A row that holds a NaN or an infinity does not touch other rows. hidden a
+ * multiple of 8 up to 16384 (else W4A16_ERR_UNSUPPORTED), strides multiples of
+ * 8 and at least hidden (gate_stride also 0), pointers 16-byte (out_fp8 8-byte,
+ * scales 4-byte) aligned, eps finite and not negative, the offset and the scales
+ * finite (else W4A16_ERR_INVALID_ARG). No workspace, no host synchronisation:
+ * graph-capturable.
+ */
+w4a16_status w4a16_block_norm(const void* x, int x_dtype, long long x_stride,
+                              const uint16_t* post_weight, const uint16_t* gate,
+                              long long gate_stride, const uint16_t* residual,
+                              long long residual_stride, const uint16_t* pre_weight,
+                              float weight_offset, float branch_scale, float residual_scale,
+                              float eps, int rows, int hidden, uint16_t* out, uint16_t* h_out,
+                              uint8_t* out_fp8, float* scales, int fp8_group, void* stream);
+
+/*
  * No-allocation variant of w4a16_moe_indexed_gemm. The pages have no
  * counterpart of this call; it exists for callers that cannot allocate
  * device memory when they call the operator: a host whose caching allocator

@@ -926,6 +926,104 @@ w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed
   return cuda_status(launch_moe_few(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
+// What both products ask of their arguments behind the sizes.
+static w4a16_status check_product(const ProductArgs& a, int out_dtype) {
+  if (a.weight == nullptr || !aligned16(a.weight)) return W4A16_ERR_INVALID_ARG;
+  if (out_dtype != W4A16_DTYPE_F32 && out_dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+  if (a.gated && a.addend != nullptr) return W4A16_ERR_INVALID_ARG;
+  if (a.x_stride < a.k || a.x_stride % 8 != 0 || a.x_stride > 0x7fffffffLL)
+    return W4A16_ERR_INVALID_ARG;
+  if (a.tokens == 0) return W4A16_OK;
+  if (a.x == nullptr || a.out == nullptr) return W4A16_ERR_INVALID_ARG;
+  if (!aligned16(a.x) || !aligned16(a.out) || !aligned16(a.addend)) return W4A16_ERR_INVALID_ARG;
+  if (a.addend == a.out && out_dtype != W4A16_DTYPE_F32) return W4A16_ERR_INVALID_ARG;
+  return W4A16_OK;
+}
+
+w4a16_status w4a16_linear_few_tokens(const void* packed, int layout, int n, int k,
+                                     const uint16_t* x, long long x_stride, int tokens,
+                                     const float* addend, void* out, int out_dtype, void* stream) {
+  if (n <= 0 || k <= 0 || tokens < 0) return W4A16_ERR_INVALID_ARG;
+  if (layout != W4A16_LAYOUT_KTILE64 && layout != W4A16_LAYOUT_KTILE64_GLU16)
+    return W4A16_ERR_INVALID_ARG;
+  const bool gated = layout == W4A16_LAYOUT_KTILE64_GLU16;
+  if (k % kGroup != 0 || tokens > W4A16_FEW_TOKENS_MAX || n > kProductMaxSize ||
+      k > kProductMaxSize || (gated && n % kTileRows != 0))
+    return W4A16_ERR_UNSUPPORTED;
+  const ProductArgs a = {packed, n,      k,   gated, x, x_stride, tokens,
+                         addend, out, out_dtype == W4A16_DTYPE_F32};
+  const w4a16_status st = check_product(a, out_dtype);
+  if (st != W4A16_OK || tokens == 0) return st;
+  const int sms = current_sm_count();
+  if (sms <= 0) return W4A16_ERR_CUDA;
+  return cuda_status(launch_linear_few(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_dense(const uint16_t* weight, int n, int k, int gated, const uint16_t* x,
+                         long long x_stride, int tokens, const float* addend, void* out,
+                         int out_dtype, void* stream) {
+  if (n <= 0 || k <= 0 || tokens < 0) return W4A16_ERR_INVALID_ARG;
+  if (k % 8 != 0 || n > kProductMaxSize || k > kProductMaxSize || tokens > kDenseMaxTokens ||
+      (gated != 0 && n % 2 != 0))
+    return W4A16_ERR_UNSUPPORTED;
+  const ProductArgs a = {weight, n,      k,   gated != 0, x, x_stride, tokens,
+                         addend, out, out_dtype == W4A16_DTYPE_F32};
+  const w4a16_status st = check_product(a, out_dtype);
+  if (st != W4A16_OK || tokens == 0) return st;
+  const int sms = current_sm_count();
+  if (sms <= 0) return W4A16_ERR_CUDA;
+  return cuda_status(launch_dense(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_block_norm(const void* x, int x_dtype, long long x_stride,
+                              const uint16_t* post_weight, const uint16_t* gate,
+                              long long gate_stride, const uint16_t* residual,
+                              long long residual_stride, const uint16_t* pre_weight,
+                              float weight_offset, float branch_scale, float residual_scale,
+                              float eps, int rows, int hidden, uint16_t* out, uint16_t* h_out,
+                              uint8_t* out_fp8, float* scales, int fp8_group, void* stream) {
+  if (rows < 0 || hidden <= 0 || !(eps >= 0.f) || std::isinf(eps)) return W4A16_ERR_INVALID_ARG;
+  if (!std::isfinite(weight_offset) || !std::isfinite(branch_scale) ||
+      !std::isfinite(residual_scale))
+    return W4A16_ERR_INVALID_ARG;
+  if (x_dtype != W4A16_DTYPE_F32 && x_dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+  if (hidden % 8 != 0 || hidden > kNormMaxHidden) return W4A16_ERR_UNSUPPORTED;
+  if (fp8_group != W4A16_FP8_NONE && fp8_group != W4A16_FP8_ROW && fp8_group != W4A16_FP8_GROUP)
+    return W4A16_ERR_UNSUPPORTED;
+  if (rows == 0) return W4A16_OK;
+  const bool fp8 = fp8_group != W4A16_FP8_NONE;
+  if (x == nullptr || fp8 != (out_fp8 != nullptr) || fp8 != (scales != nullptr))
+    return W4A16_ERR_INVALID_ARG;
+  const bool normed = out != nullptr || fp8;
+  if (normed != (pre_weight != nullptr) || (!normed && h_out == nullptr))
+    return W4A16_ERR_INVALID_ARG;
+  if (x_stride < hidden || x_stride % 8 != 0) return W4A16_ERR_INVALID_ARG;
+  if (residual != nullptr && (residual_stride < hidden || residual_stride % 8 != 0))
+    return W4A16_ERR_INVALID_ARG;
+  if (gate != nullptr && gate_stride != 0 && (gate_stride < hidden || gate_stride % 8 != 0))
+    return W4A16_ERR_INVALID_ARG;
+  if (residual != nullptr && residual == h_out && residual_stride != hidden)
+    return W4A16_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(post_weight) || !aligned16(gate) || !aligned16(residual) ||
+      !aligned16(pre_weight) || !aligned16(out) || !aligned16(h_out) ||
+      (reinterpret_cast<uintptr_t>(out_fp8) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(scales) & 3u) != 0)
+    return W4A16_ERR_INVALID_ARG;
+  const int sms = current_sm_count();
+  if (sms <= 0) return W4A16_ERR_CUDA;
+  const BlockNormArgs a = {x,           x_dtype == W4A16_DTYPE_F32,
+                           x_stride,    post_weight,
+                           gate,        gate_stride,
+                           residual,    residual_stride,
+                           pre_weight,  weight_offset,
+                           branch_scale, residual_scale,
+                           eps,         rows,
+                           hidden,      out,
+                           h_out,       out_fp8,
+                           scales,      fp8_group};
+  return cuda_status(launch_block_norm(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
 w4a16_status w4a16_read_device_status(void* workspace, int* detail, void* stream) {
   if (workspace == nullptr) return W4A16_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

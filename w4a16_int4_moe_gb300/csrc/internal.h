@@ -273,6 +273,45 @@ size_t few_workspace_bytes(int tokens, int topk, int hidden, int inter);
 bool few_supported(int tokens, int topk, int num_experts, int hidden, int inter);
 cudaError_t launch_moe_few(const FewArgs& args, int sms, cudaStream_t stream);
 
+// Products with one weight: plain (out[t, r]) or gated (out[t, i] from the weight
+// rows i and n/2 + i).
+struct ProductArgs {
+  const void* weight;
+  int n, k, gated;
+  const uint16_t* x;
+  long long x_stride;
+  int tokens;
+  const float* addend;
+  void* out;
+  int f32_out;
+};
+constexpr int kProductMaxSize = 1 << 20;    // n and k
+constexpr int kDenseMaxTokens = 1 << 24;
+// A packed INT4 weight (GLU16 layout when gated) and up to 32 tokens, or a BF16 one.
+cudaError_t launch_linear_few(const ProductArgs& args, int sms, cudaStream_t stream);
+cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream);
+
+// The norms after and before a block (block_norm.cu).
+struct BlockNormArgs {
+  const void* x;
+  int x_f32;
+  long long x_stride;
+  const uint16_t* post_weight;
+  const uint16_t* gate;
+  long long gate_stride;
+  const uint16_t* residual;
+  long long residual_stride;
+  const uint16_t* pre_weight;
+  float weight_offset, branch_scale, residual_scale, eps;
+  int rows, hidden;
+  uint16_t* out;
+  uint16_t* h_out;
+  uint8_t* out_fp8;
+  float* scales;
+  int fp8_group;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& args, int sms, cudaStream_t stream);
+
 cudaError_t launch_silu_and_mul(const uint16_t* in, int rows, int inter, uint16_t* out,
                                 cudaStream_t stream);
 

@@ -53,7 +53,7 @@ EXPORTED = (
     "w4a16_topk_softmax", "w4a16_deterministic_bytes", "w4a16_layer_workspace_size",
     "w4a16_moe_layer", "w4a16_moe_route_align", "w4a16_grouped_plan", "w4a16_plan_info",
     "w4a16_add_rms_norm", "w4a16_router_logits", "w4a16_moe_few_tokens_workspace_size",
-    "w4a16_moe_few_tokens",
+    "w4a16_moe_few_tokens", "w4a16_linear_few_tokens", "w4a16_dense", "w4a16_block_norm",
 )
 
 
@@ -136,6 +136,10 @@ def load_library(path: Optional[str] = None):
         "w4a16_moe_few_tokens_workspace_size": (_Z, [_I, _I, _I, _I]),
         "w4a16_moe_few_tokens": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _I, _I, _P, _I, _I, _I, _I,
                                       _P, _P, _P, _I, _P, _Z, _P]),
+        "w4a16_linear_few_tokens": (_I, [_P, _I, _I, _I, _P, _L, _I, _P, _P, _I, _P]),
+        "w4a16_dense": (_I, [_P, _I, _I, _I, _P, _L, _I, _P, _P, _I, _P]),
+        "w4a16_block_norm": (_I, [_P, _I, _L, _P, _P, _L, _P, _L, _P, _F, _F, _F, _F, _I, _I, _P,
+                                  _P, _P, _P, _I, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -452,10 +456,10 @@ def _blob(fn: str, what: str, t: torch.Tensor, size: int):
     return t.data_ptr()
 
 
-def _rows(fn: str, what: str, t: torch.Tensor):
-    """t is BF16 [rows, columns] on a GPU with adjacent columns; returns
-    (address, rows, columns, row stride)."""
-    if t.dtype is not _BF16 or not t.is_cuda or t.dim() != 2:
+def _rows(fn: str, what: str, t: torch.Tensor, dtype=_BF16):
+    """t is BF16 (or of this type) [rows, columns] on a GPU with adjacent columns;
+    returns (address, rows, columns, row stride)."""
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2:
         _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}")
     rows, columns = t.shape
     if t.is_contiguous():
@@ -570,6 +574,146 @@ def w4a16_moe_few_tokens(packed_gate_up: torch.Tensor, packed_down: torch.Tensor
         _need(fn, "topk_weights", topk_weights, _F32, picks),
         _need(fn, "out", out, _F32, (tokens, hidden)), flags,
         _blob(fn, "workspace", workspace, 0), workspace.numel(), _raw_stream(x, stream)))
+    return out
+
+
+# The calls below take all tensors on one device, which need not be the current
+# one: the library launches on the current device, so it is made current.
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # (of CUDA builds)
+
+
+def _one_device(fn: str, x: torch.Tensor, *others):
+    """The context in which x's device is the current one; the other tensors
+    (None: absent) are on it too, else W4A16_ERR_INVALID_ARG."""
+    device = x.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            _refuse(fn, f"tensors on {x.device} and on {t.device}")
+    if device < 0 or device == _current_device():
+        return _HERE
+    return torch.cuda.device(device)
+
+
+def _product(fn: str, call, x, n: int, k: int, gated: bool, addend, out, out_dtype, stream, weight,
+             *sizes):
+    """The part that both products share: x's rows, addend, output and the call."""
+    x_at, tokens, columns, x_stride = _rows(fn, "x", x)
+    if columns != k:
+        _refuse(fn, f"x {tuple(x.shape)} for a weight of {k} columns")
+    shape = (tokens, n // 2 if gated else n)
+    with _one_device(fn, x, weight, addend, out):
+        if out is None:
+            with on_stream(stream):
+                out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        dtype = out.dtype
+        if dtype is not _F32 and dtype is not _BF16:
+            _refuse(fn, f"out: {dtype}")
+        _check(fn, call(
+            weight.data_ptr(), *sizes, x_at, x_stride, tokens,
+            None if addend is None else _need(fn, "addend", addend, _F32, shape),
+            _need(fn, "out", out, dtype, shape),
+            W4A16_DTYPE_F32 if dtype is _F32 else W4A16_DTYPE_BF16, _raw_stream(x, stream)))
+    return out
+
+
+def w4a16_linear_few_tokens(x: torch.Tensor, packed: torch.Tensor, n: int,
+                            layout: int = W4A16_LAYOUT_KTILE64,
+                            addend: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x . W^T (+ addend FP32 [T, n]) for up to W4A16_FEW_TOKENS_MAX tokens and one
+    packed INT4 weight [n, k] (w4a16_prepack of one expert), or, with
+    W4A16_LAYOUT_KTILE64_GLU16, silu(x . Wgate^T) * (x . Wup^T), [T, n/2].
+    x BF16 [T, k], rows may be strided. out (or out_dtype): FP32 or BF16; out may
+    be addend."""
+    fn = "w4a16_linear_few_tokens"
+    if x.dim() != 2:
+        _refuse(fn, f"x {tuple(x.shape)}")
+    k = x.shape[1]
+    # 128-row tiles of 64-column steps, 4608 bytes each
+    _blob(fn, "packed", packed, -(-n // 128) * -(-k // 64) * 4608)
+    return _product(fn, load_library().w4a16_linear_few_tokens, x, n, k,
+                    layout == W4A16_LAYOUT_KTILE64_GLU16, addend, out, out_dtype, stream, packed,
+                    layout, n, k)
+
+
+def w4a16_dense(x: torch.Tensor, weight: torch.Tensor, gated: bool = False,
+                addend: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x . W^T (+ addend FP32 [T, n]) for a BF16 weight [n, k], or, gated (the
+    weight's rows are n/2 of the gate, then n/2 of up),
+    silu(x . Wgate^T) * (x . Wup^T), [T, n/2]. x BF16 [T, k], rows may be
+    strided. out (or out_dtype): FP32 or BF16; out may be addend."""
+    fn = "w4a16_dense"
+    if weight.dim() != 2:
+        _refuse(fn, f"weight {tuple(weight.shape)}")
+    n, k = weight.shape
+    _need(fn, "weight", weight, _BF16, (n, k))
+    return _product(fn, load_library().w4a16_dense, x, n, k, gated, addend, out, out_dtype, stream,
+                    weight, n, k, 1 if gated else 0)
+
+
+def w4a16_block_norm(x: torch.Tensor, pre_weight: Optional[torch.Tensor], eps: float = 1e-6,
+                     post_weight: Optional[torch.Tensor] = None,
+                     gate: Optional[torch.Tensor] = None,
+                     residual: Optional[torch.Tensor] = None, branch_scale: float = 1.0,
+                     residual_scale: float = 1.0, weight_offset: float = 0.0,
+                     fp8_group: int = W4A16_FP8_NONE, bf16_out: bool = True, out=None,
+                     stream=None):
+    """p = x * rsqrt(mean(x^2) + eps) * (post_weight + weight_offset) (x itself
+    without post_weight), h = residual_scale * residual + branch_scale * gate * p,
+    y = h * rsqrt(mean(h^2) + eps) * (pre_weight + weight_offset).
+    Returns (bf16(y), bf16(h), e4m3(y * (1 / scale)), scale), the first, third and
+    fourth None when not asked for (bf16_out, fp8_group as in
+    w4a16_add_rms_norm; pre_weight None: h alone). out: the four tensors to
+    write, None for an absent one (it then decides what is written; the second
+    may be the residual itself). x FP32 or BF16 [T, H], residual BF16 [T, H], gate
+    BF16 [T, H] or [H]; rows may be strided."""
+    fn = "w4a16_block_norm"
+    f32 = x.dtype is _F32
+    x_at, rows, hidden, x_stride = _rows(fn, "x", x, _F32 if f32 else _BF16)
+    shape, groups = (rows, hidden), (rows, 0)
+
+    def weight(what, t):
+        return None if t is None else _need(fn, what, t, _BF16, (hidden,))
+
+    def same_rows(what, t):
+        at, *size, stride = _rows(fn, what, t)
+        if (*size,) != shape:
+            _refuse(fn, f"{what} {tuple(t.shape)} for x {tuple(x.shape)}")
+        return at, stride
+
+    post_at, pre_at = weight("post_weight", post_weight), weight("pre_weight", pre_weight)
+    r_at = g_at = None
+    r_stride = g_stride = 0
+    if residual is not None:
+        r_at, r_stride = same_rows("residual", residual)
+    if gate is not None:
+        if gate.dim() == 1:
+            g_at = weight("gate", gate)
+        else:
+            g_at, g_stride = same_rows("gate", gate)
+    if fp8_group != W4A16_FP8_NONE:
+        if fp8_group not in (W4A16_FP8_ROW, W4A16_FP8_GROUP):
+            raise W4A16Error(fn, W4A16_ERR_UNSUPPORTED, f"fp8_group {fp8_group}")
+        groups = (rows, 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP))
+    with _one_device(fn, x, post_weight, pre_weight, residual, gate, *(out or ())):
+        if out is None:
+            normed = pre_weight is not None
+            kinds = ((shape, _BF16, bf16_out and normed), (shape, _BF16, True),
+                     (shape, _E4M3, fp8_group), (groups, _F32, fp8_group))
+            with on_stream(stream):
+                out = tuple(torch.empty(size, dtype=dtype, device=x.device) if wanted else None
+                            for size, dtype, wanted in kinds)
+        y, h, y8, scales = out
+        _check(fn, load_library().w4a16_block_norm(
+            x_at, W4A16_DTYPE_F32 if f32 else W4A16_DTYPE_BF16, x_stride, post_at, g_at, g_stride,
+            r_at, r_stride, pre_at, weight_offset, branch_scale, residual_scale, eps, rows, hidden,
+            None if y is None else _need(fn, "out", y, _BF16, shape),
+            None if h is None else _need(fn, "h_out", h, _BF16, shape),
+            None if y8 is None else _need(fn, "out_fp8", y8, _E4M3, shape),
+            None if scales is None else _need(fn, "scales", scales, _F32, groups),
+            fp8_group, _raw_stream(x, stream)))
     return out
 
 
