@@ -1,0 +1,386 @@
+// product_few.cu -- products with one weight, packed INT4 or BF16, for up to 32
+// tokens, plain or gated:
+//
+//   out[t, r] = addend[t, r] + x[t] . w[r]^T
+//   out[t, i] = silu(x[t] . wgate[i]^T) * (x[t] . wup[i]^T)
+//
+// The weight is the traffic, and the time is that of reading it once, plus a
+// launch, a first load and the sums' way out. Every warp copies its own steps of
+// 64 columns into slots of its own (no barrier between warps before the sums),
+// several steps ahead, and multiplies with m16n8k16 MMAs whose M side are the
+// weight rows. A packed code enters as the BF16 number 16 + q, exact, one shift
+// and one three-input logic operation for two; the 24 too much comes off through
+// two more MMAs a group of 32; the scale is applied to the group's FP32 sum. So
+// no weight is rounded.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace w4a16 {
+
+namespace {
+
+// d = a . b + c, BF16 operands
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+        "f"(c[2]), "f"(c[3]));
+}
+
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+// The first `bytes` (16, or 0: nothing is read) of them, zeros behind
+__device__ __forceinline__ void copy16_of(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&w)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 load_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Rows of 128 bytes, 16-byte chunks c of odd rows in the other half, so that the
+// eight lanes of two rows that load at a time meet all banks.
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+  return static_cast<uint32_t>(row * 128 + ((c ^ (row & 1) << 2) << 4));
+}
+
+struct FewProduct {
+  ProductArgs a;
+  int split;       // CTAs of a cluster, which share the columns
+  int steps;       // of 64 columns
+  int slot_bytes;  // of a warp's step
+};
+
+// Bytes of a step of 64 columns of a warp's rows and of the tokens.
+constexpr int step_bytes(bool int4, int rows) { return rows * (int4 ? 36 : 128); }
+
+}  // namespace
+
+// A cluster has 16 * kMt weight rows, a CTA of it a share of the columns, of
+// which its warps take steps of 64 by turns. A warp copies its steps (the
+// weights, and the tokens' columns) into slots of its own, kDepth ahead. The sums
+// of the warps meet in shared memory, those of the CTAs through the cluster's.
+template <bool kInt4, bool kGated, int kMt, int kNt, int kWarps, int kDepth>
+__global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const FewProduct p) {
+  constexpr int kThreads = kWarps * 32;
+  constexpr int kRows = 16 * kMt;
+  constexpr int kTokens = 8 * kNt;
+  constexpr int kPitch = kRows + 4;  // of a token's sums
+  static_assert(kMt % 2 == 0, "gate and up rows by sixteens, codes by 32 rows");
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* part = reinterpret_cast<float*>(smem);  // [kWarps][kTokens][kPitch], in the slots' place
+  const ProductArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int block = static_cast<int>(blockIdx.x) / p.split;
+  const int columns = kGated ? a.n / 2 : a.n;
+  const int first = p.steps * rank / p.split + warp, last = p.steps * (rank + 1) / p.split;
+  const uint32_t slots = smem_u32(smem) + static_cast<uint32_t>(warp * kDepth * p.slot_bytes);
+  constexpr uint32_t kWeightBytes = step_bytes(kInt4, kRows);
+  // This lane's sources in the step that it fetches next. (k is a multiple of 8,
+  // and a packed step is whole: only chunks of x, and of BF16 weights, can lie
+  // behind the row's end.)
+  constexpr int kWeightCopies = kInt4 ? kRows / 16 : kRows / 4;
+  const uint8_t* w_from[kInt4 ? 2 : kWeightCopies];
+  if constexpr (kInt4) {
+    const int r0 = block * kRows;
+    const uint8_t* from = static_cast<const uint8_t*>(a.weight) +
+                          (static_cast<long long>(r0 / kTileRows) * p.steps + first) * kStepBytes;
+    w_from[0] = from + (r0 % kTileRows + lane) * 16;  // codes of row `lane`
+    w_from[1] = from + kStepQBytes + lane / (kRows / 8) * (kTileRows * 2) + r0 % kTileRows * 2 +
+                lane % (kRows / 8) * 16;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kWeightCopies; ++j) {
+      const int r = 4 * j + (lane >> 3);
+      int q = min(block * kRows + r, columns - 1);  // weight row
+      if constexpr (kGated)
+        q = min(block * (kRows / 2) + r / 32 * 16 + r % 16, columns - 1) + r / 16 % 2 * columns;
+      w_from[j] = static_cast<const uint8_t*>(a.weight) +
+                  (static_cast<long long>(q) * a.k + first * kKStep + (lane & 7) * 8) * 2;
+    }
+  }
+  const uint16_t* x_from = a.x + min(lane >> 3, a.tokens - 1) * a.x_stride + first * kKStep + (lane & 7) * 8;
+  int c_from = first * kKStep + (lane & 7) * 8;
+  grid_dependency_wait();
+  grid_dependents_go();
+
+  const uint32_t x_to = kWeightBytes + chunk_at(lane >> 3, lane & 7), w_to = lane * 16;
+  const long long x_four = 4 * a.x_stride;
+  const int x_last = a.tokens - 1 - (lane >> 3);
+  const auto fetch = [&](uint32_t slot) {
+    const int bytes = c_from < a.k ? 16 : 0;
+    if constexpr (kInt4) {
+#pragma unroll
+      for (int j = 0; j < kWeightCopies; ++j)  // codes [half][row][16]
+        copy16(slot + w_to + j * 512,
+               w_from[0] + j / (kRows / 32) * (kTileRows * 16) + j % (kRows / 32) * 512);
+      if (lane < kRows / 4)  // scales [half][row]
+        copy16(slot + w_to + 2 * kRows * 16, w_from[1]);
+      w_from[0] += kWarps * kStepBytes;
+      w_from[1] += kWarps * kStepBytes;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kWeightCopies; ++j) {
+        copy16_of(slot + x_to - kWeightBytes + j * 512, w_from[j], bytes);
+        w_from[j] += kWarps * kKStep * 2;
+      }
+    }
+    const uint16_t* from = x_from;
+#pragma unroll
+    for (int j = 0; j < 2 * kNt; ++j, from += x_four)
+      if (4 * j <= x_last) copy16_of(slot + x_to + j * 512, from, bytes);
+    x_from += kWarps * kKStep;
+    c_from += kWarps * kKStep;
+  };
+
+  float acc[kMt][kNt][4] = {};
+  uint32_t x_row[kNt][2];
+#pragma unroll
+  for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      x_row[nt][h] = kWeightBytes + chunk_at(min(8 * nt + g, a.tokens - 1), 4 * h + t);
+  const auto multiply = [&](uint32_t slot) {
+    uint32_t sc[kMt / 2][4];
+    if constexpr (kInt4) {
+      // lane = (matrix, row): matrix m gives rows 16 (m & 1) .. + 15 of half
+      // m >> 1; its eight addresses alternate between rows + 0 and rows + 8
+      const uint32_t scales = slot + 2 * kRows * 16 + (lane >> 4) * (kRows * 2) +
+                              ((lane >> 3 & 1) * 16 + (lane & 1) * 8) * 2;
+#pragma unroll
+      for (int j = 0; j < kMt / 2; ++j) ldmatrix_x4_trans(scales + j * 64, sc[j]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 x[kNt];
+#pragma unroll
+      for (int nt = 0; nt < kNt; ++nt) x[nt] = load_shared16(slot + x_row[nt][h]);
+      if constexpr (kInt4) {
+        // a code in bits 3 to 6 of the BF16 number 16 is 16 + q: 24 too much,
+        // which two MMAs take off all rows' sums at once
+        constexpr uint32_t kCodes = 0x00780078u, k16 = 0x41804180u, kMinus24 = 0xC1C0C1C0u;
+        const uint32_t minus[4] = {kMinus24, kMinus24, kMinus24, kMinus24};
+        const float none[4] = {};
+        float base[kNt][4];
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) {
+          mma16816(base[nt], minus, x[nt].x, x[nt].y, none);
+          mma16816(base[nt], minus, x[nt].z, x[nt].w, base[nt]);
+        }
+#pragma unroll
+        for (int j = 0; j < kMt / 2; ++j) {
+          uint32_t w[4];
+          ldmatrix_x4(slot + (h * kRows + j * 32 + lane) * 16, w);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int mt = 2 * j + i;
+            const uint32_t w0 = w[2 * i], w1 = w[2 * i + 1];
+            const uint32_t a0[4] = {(w0 << 3 & kCodes) | k16, (w1 << 3 & kCodes) | k16,
+                                    (w0 >> 1 & kCodes) | k16, (w1 >> 1 & kCodes) | k16};
+            const uint32_t a1[4] = {(w0 >> 5 & kCodes) | k16, (w1 >> 5 & kCodes) | k16,
+                                    (w0 >> 9 & kCodes) | k16, (w1 >> 9 & kCodes) | k16};
+            const uint32_t pair = sc[j][2 * h + i];
+            const float s0 = __uint_as_float(pair << 16), s1 = __uint_as_float(pair & 0xFFFF0000u);
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+              float c[4];
+              mma16816(c, a0, x[nt].x, x[nt].y, base[nt]);
+              mma16816(c, a1, x[nt].z, x[nt].w, c);
+              acc[mt][nt][0] = fmaf(s0, c[0], acc[mt][nt][0]);
+              acc[mt][nt][1] = fmaf(s0, c[1], acc[mt][nt][1]);
+              acc[mt][nt][2] = fmaf(s1, c[2], acc[mt][nt][2]);
+              acc[mt][nt][3] = fmaf(s1, c[3], acc[mt][nt][3]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt) {
+          const uint32_t at = slot + mt * 2048 + chunk_at(g, 4 * h + t);
+          const uint4 w0 = load_shared16(at), w1 = load_shared16(at + 8 * 128);
+          const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) {
+            mma16816(acc[mt][nt], a0, x[nt].x, x[nt].y, acc[mt][nt]);
+            mma16816(acc[mt][nt], a1, x[nt].z, x[nt].w, acc[mt][nt]);
+          }
+        }
+      }
+    }
+  };
+
+  // a group of copies a slot, also an empty one
+#pragma unroll 1
+  for (int d = 0; d < kDepth; ++d) {
+    if (first + d * kWarps < last) fetch(slots + d * p.slot_bytes);
+    copies_commit();
+  }
+  uint32_t slot = slots;
+#pragma unroll 1
+  for (int step = first; step < last; step += kWarps) {
+    copies_wait<kDepth - 1>();
+    __syncwarp();
+    multiply(slot);
+    __syncwarp();
+    if (step + kDepth * kWarps < last) fetch(slot);
+    copies_commit();
+    slot += p.slot_bytes;
+    if (slot == slots + kDepth * p.slot_bytes) slot = slots;
+  }
+  copies_wait<0>();
+  __syncthreads();
+
+  // [warp][token][row]
+#pragma unroll
+  for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        part[(warp * kTokens + 8 * nt + 2 * t + (i & 1)) * kPitch + mt * 16 + g + (i >> 1) * 8] =
+            acc[mt][nt][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.tokens * kRows; i += kThreads) {
+    const int at = i / kRows * kPitch + i % kRows;
+    float v = part[at];
+#pragma unroll
+    for (int s = 1; s < kWarps; ++s) v += part[s * kTokens * kPitch + at];
+    part[at] = v;
+  }
+  if (p.split > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  // every CTA of the cluster writes its share of the outputs
+  constexpr int kOut = kGated ? kRows / 2 : kRows;  // columns of the cluster
+  const int c0 = block * kOut;
+  for (int i = rank * kThreads + static_cast<int>(threadIdx.x); i < kOut * a.tokens;
+       i += p.split * kThreads) {
+    const int tok = i / kOut, c = i % kOut;
+    if (c0 + c >= columns) continue;
+    const auto sum = [&](int row) {
+      const float* at = part + tok * kPitch + row;
+      if (p.split == 1) return *at;
+      float v = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < p.split) v += ld_cluster_f32(map_to_cta(smem_u32(at), static_cast<uint32_t>(r)));
+      return v;
+    };
+    float v;
+    if constexpr (kGated) {
+      const int row = c / 16 * 32 + c % 16;
+      const float gate = sum(row);
+      v = gate / (1.f + expf(-gate)) * sum(row + 16);
+    } else {
+      v = sum(c);
+    }
+    const long long at = static_cast<long long>(tok) * columns + c0 + c;
+    if (a.addend != nullptr) v += a.addend[at];
+    if (a.f32_out)
+      static_cast<float*>(a.out)[at] = v;
+    else
+      static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+  }
+  if (p.split > 1) cluster_sync_all();  // the sums stay until all have read them
+}
+
+namespace {
+
+template <bool kInt4, bool kGated, int kMt, int kNt, int kWarps, int kDepth>
+cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
+  constexpr int kRows = 16 * kMt;
+  const auto kernel = w4a16_product_few_kernel<kInt4, kGated, kMt, kNt, kWarps, kDepth>;
+  FewProduct p;
+  p.a = args;
+  p.steps = ceil_div(args.k, kKStep);
+  p.slot_bytes = step_bytes(kInt4, kRows) + args.tokens * 128;
+  const int sums = kWarps * 8 * kNt * (kRows + 4) * 4;
+  const int smem = std::max(kWarps * kDepth * p.slot_bytes, sums);
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  if (e != cudaSuccess) return e;
+  const int blocks = ceil_div(args.n, kRows);
+  // a cluster of two, four or eight where all CTAs still find an SM and every
+  // warp a step. (Eights that want an SM each do not all find a place at once: 512
+  // rows of 7168 in BF16 7.6 us, in fours 4.5.)
+  const int most = smem > 100 << 10 ? 4 : 8;
+  p.split = 1;
+  while (p.split < most && 2 * blocks * p.split <= sms && p.steps >= 2 * p.split * kWarps)
+    p.split *= 2;
+  return launch_dependent(kernel, blocks * p.split, kWarps * 32, static_cast<size_t>(smem),
+                          p.split, stream, p);
+}
+
+}  // namespace
+
+// Rows of a CTA and steps in flight, us in a graph (weights not in L2): 32 rows
+// as long as the SMs have one CTA each, deeper then; with more rows than that
+// shallower slots, so that two CTAs fit an SM, or twice the rows.
+template <bool kInt4, bool kGated>
+cudaError_t few(const ProductArgs& args, int sms, cudaStream_t stream) {
+  const bool one = args.n <= 32 * sms;  // 32-row CTAs: at most one an SM
+  if constexpr (kInt4) {
+    if (args.tokens <= 8) {
+      if (args.n <= 64 * sms) return run<kInt4, kGated, 2, 1, 8, 5>(args, sms, stream);
+      return run<kInt4, kGated, 4, 1, 8, 4>(args, sms, stream);
+    }
+    if (args.tokens <= 16) return run<kInt4, kGated, 2, 2, 8, 4>(args, sms, stream);
+    return run<kInt4, kGated, 4, 4, 8, 3>(args, sms, stream);
+  } else {
+    if (args.tokens <= 8)
+      return one ? run<kInt4, kGated, 2, 1, 8, 5>(args, sms, stream)
+                 : run<kInt4, kGated, 2, 1, 8, 3>(args, sms, stream);
+    if (args.tokens <= 16)
+      return one ? run<kInt4, kGated, 2, 2, 8, 3>(args, sms, stream)
+                 : run<kInt4, kGated, 2, 2, 8, 2>(args, sms, stream);
+    return one ? run<kInt4, kGated, 2, 4, 8, 3>(args, sms, stream)
+               : run<kInt4, kGated, 4, 4, 8, 2>(args, sms, stream);
+  }
+}
+
+cudaError_t launch_linear_few(const ProductArgs& args, int sms, cudaStream_t stream) {
+  return args.gated ? few<true, true>(args, sms, stream) : few<true, false>(args, sms, stream);
+}
+
+cudaError_t launch_dense_few(const ProductArgs& args, int sms, cudaStream_t stream) {
+  return args.gated ? few<false, true>(args, sms, stream) : few<false, false>(args, sms, stream);
+}
+
+}  // namespace w4a16

@@ -104,10 +104,8 @@ cudaError_t launch_product(const ProductArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_linear_few(const ProductArgs& args, int, cudaStream_t stream) {
-  return launch_product<true>(args, stream);
-}
-cudaError_t launch_dense(const ProductArgs& args, int, cudaStream_t stream) {
+cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) {
+  if (args.tokens <= kDenseFewTokens) return launch_dense_few(args, sms, stream);
   return launch_product<false>(args, stream);
 }
 
