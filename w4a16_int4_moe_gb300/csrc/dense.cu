@@ -1,0 +1,614 @@
+// dense.cu -- products with one BF16 weight for many tokens, plain or gated:
+//
+//   out[t, r] = addend[t, r] + x[t] . w[r]^T
+//   out[t, i] = silu(x[t] . wgate[i]^T) * (x[t] . wup[i]^T)
+//
+// tcgen05 with 256 tokens x up to 256 weight rows a tile, by pairs of CTAs that go
+// from tile to tile; or, where there are fewer tiles than SMs, 128 tokens a tile
+// with the columns split over a cluster. A gated tile has as many gate as up
+// rows, so a token's gate and up lie in one TMEM lane.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace w4a16 {
+
+namespace {
+
+constexpr int kTileM = 128;      // tokens of a CTA
+constexpr int kSumWarps = 8;     // two a TMEM quarter, half of the columns each
+constexpr int kWarpCopy = kSumWarps, kWarpMma = kSumWarps + 1;
+constexpr int kDenseThreads = 32 * (kSumWarps + 2);
+constexpr int kMaxSlots = 8;
+constexpr int kChunk = 32;       // output columns of an epilogue warp at a time
+constexpr int kTileBytes = 32 * kChunk * 4;  // of its 32 tokens
+constexpr int kTilesBytes = kSumWarps * 2 * kTileBytes;
+constexpr int kRingBytes = 160 << 10;
+constexpr int kSmemBytes = 1024 + kRingBytes + kTilesBytes;
+constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
+
+// The tokens that a CTA multiplies when it has those from m0 on: 128 whole ones,
+// the last 128 where fewer (or none) are left. It writes only its own. (Rows that
+// the copy would fill with zeros behind the last token make the MMAs slower: a
+// tile of 255 tokens took 48 us, one of 256 41, one of 256 zero tokens 48.)
+__device__ __forceinline__ int first_token(int m0, int tokens) {
+  return max(min(m0, tokens - kTileM), 0);
+}
+
+struct DenseArgs {
+  CUtensorMap x, weight;
+  ProductArgs a;
+  int columns;       // of the output
+  int half;          // weight rows of a box: half of a tile's
+  int out_cols;      // output columns of a tile
+  int m_tiles, n_tiles, k_steps;
+  int slots;
+  int split;         // CTAs of a cluster that share a tile's columns of x (split kernel)
+};
+
+__device__ __forceinline__ bool give_up(volatile int* failed, long long t0) {
+  if (*failed) return true;
+  if (clock64() - t0 <= kGiveUpCycles) return false;
+  *failed = 1;
+  return true;
+}
+// kRemote: threads of other CTAs of the cluster arrive as well.
+template <bool kRemote>
+__device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+  const auto done = [&] {
+    return kRemote ? mbar_try_wait_cluster_now(bar, parity) : mbar_try_wait(bar, parity);
+  };
+  if (done()) return true;
+  const long long t0 = clock64();
+  while (!done())
+    if (give_up(failed, t0)) return false;
+  return true;
+}
+
+// A position in a ring of slots.
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
+  uint32_t w[16];
+  tmem_ld_32x32b_x16(at, w);
+  tmem_ld_wait_for(w);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+}
+
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+  uint32_t lo[16], hi[16];
+  tmem_ld_32x32b_x16(at, lo);
+  tmem_ld_32x32b_x16(at + 16, hi);
+  tmem_ld_wait_for(lo);
+  tmem_ld_wait_for(hi);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = __uint_as_float(lo[i]);
+    v[16 + i] = __uint_as_float(hi[i]);
+  }
+}
+
+// Offset of four columns of a row in a warp's tile of 32 x 32 floats, placed so
+// that both a column of rows and a row meet all banks.
+__device__ __forceinline__ int tile_at(int row, int quad) {
+  return row * kChunk + ((quad ^ (row & 7)) << 2);
+}
+
+__device__ __forceinline__ float silu_times(float gate, float up) {
+  return __fdividef(gate, 1.f + __expf(-gate)) * up;
+}
+
+// Four adjacent output values of a token, the columns from c on.
+__device__ __forceinline__ float4 load_addend(const DenseArgs& p, int token, int c) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.a.addend == nullptr || token >= p.a.tokens || c >= p.columns) return v;
+  const float* at = p.a.addend + static_cast<long long>(token) * p.columns + c;
+  if (p.columns % 4 == 0) return *reinterpret_cast<const float4*>(at);
+  float f[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c + i < p.columns) f[i] = at[i];
+  return make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store_out(const DenseArgs& p, int token, int c, float4 v) {
+  if (token >= p.a.tokens || c >= p.columns) return;
+  const long long at = static_cast<long long>(token) * p.columns + c;
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  if (p.a.f32_out) {
+    float* out = static_cast<float*>(p.a.out) + at;
+    if (p.columns % 4 == 0) {
+      *reinterpret_cast<float4*>(out) = v;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < p.columns) out[i] = f[i];
+  } else {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + at;
+    if (p.columns % 4 == 0) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+      *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                  *reinterpret_cast<const uint32_t*>(&hi));
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < p.columns) out[i] = __float2bfloat16_rn(f[i]);
+  }
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+}  // namespace
+
+// Pairs of CTAs: each copies its own 128 tokens and half of the tile's weight
+// rows (gated: one the gate rows, the other the up rows), the first CTA's MMA
+// thread issues for both, and every CTA keeps the sums of its tokens. Two
+// accumulators, so that a tile's sums leave while the next one is multiplied.
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    w4a16_dense_pair_kernel(const __grid_constant__ DenseArgs p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t bars[2 * kMaxSlots + 4];
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed_word;
+  volatile int* failed = &failed_word;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots,
+                 summed = full + 16 * kMaxSlots, drained = summed + 16;
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
+  const uint32_t slot_bytes = a_bytes + b_bytes;
+  const uint32_t rank = cluster_ctarank(), leader = 0;
+  const int cluster = static_cast<int>(blockIdx.x) / 2, clusters = static_cast<int>(gridDim.x) / 2;
+  const int tiles = p.m_tiles * p.n_tiles;
+  if (warp == kWarpMma) {
+    if (lane == 0) {
+      for (int i = 0; i < p.slots; ++i) {
+        mbar_init(full + 8 * i, 1);
+        mbar_init(empty + 8 * i, 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(summed + 8 * i, 1);
+        mbar_init(drained + 8 * i, 2 * kSumWarps);
+      }
+      *failed = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(&tmem_at), 512);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync_all();  // the other's barriers and TMEM are there
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_dependents_go();
+  const uint32_t tmem = tmem_at;
+  // tile i in groups of eight tiles of tokens, whose rows stay in L2 while the
+  // weight goes by
+  const auto place = [&](int i, int* m, int* n) {
+    constexpr int kGroup8 = 8;
+    const int per = kGroup8 * p.n_tiles, group = i / per, rest = i - group * per;
+    const int height = min(kGroup8, p.m_tiles - group * kGroup8);
+    *n = rest / height;
+    *m = group * kGroup8 + rest - *n * height;
+  };
+
+  if (warp == kWarpCopy) {
+    if (elect_one()) {
+      Ring r;
+      bool ok = true;
+      int issued = 0;
+      for (int tile = cluster; tile < tiles && ok; tile += clusters) {
+        int m, n;
+        place(tile, &m, &n);
+        const int m0 = first_token((2 * m + static_cast<int>(rank)) * kTileM, p.a.tokens);
+        const int w0 = p.a.gated ? n * p.half + static_cast<int>(rank) * p.columns
+                                 : (2 * n + static_cast<int>(rank)) * p.half;
+        for (int k = 0; k < p.k_steps; ++k) {
+          ok = dense_wait<true>(empty + 8 * r.slot, r.phase ^ 1u, failed);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * r.slot, 2 * slot_bytes);
+          const uint32_t bar = map_to_cta(full + 8 * r.slot, leader);
+          const uint32_t to = ring + r.slot * slot_bytes;
+          tma_load_2d_pair(to, &p.x, k * kKStep, m0, bar);
+          tma_load_2d_pair(to + a_bytes, &p.weight, k * kKStep, w0, bar);
+          ++issued;
+          r.next(p.slots);
+        }
+      }
+      if (!ok && rank == 0)  // copies in flight land before the CTAs end
+        for (int i = std::max(0, issued - p.slots); i < issued; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait_cluster_now(full + 8 * (i % p.slots), i / p.slots & 1) &&
+                 clock64() - t0 < kGiveUpCycles) {
+          }
+        }
+    }
+  } else if (warp == kWarpMma) {
+    if (rank == 0 && elect_one()) {
+      Ring r, acc;
+      const uint32_t idesc = idesc_bf16(2 * kTileM, static_cast<uint32_t>(2 * p.half));
+      bool ok = true;
+      for (int tile = cluster; tile < tiles && ok; tile += clusters) {
+        ok = dense_wait<true>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + 256 * acc.slot;
+        for (int k = 0; k < p.k_steps; ++k) {
+          ok = dense_wait<true>(full + 8 * r.slot, r.phase, failed);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t from = ring + r.slot * slot_bytes;
+          const uint64_t ad = smem_desc_sw128_kmajor(from);
+          const uint64_t bd = smem_desc_sw128_kmajor(from + a_bytes);
+#pragma unroll
+          for (int j = 0; j < kKStep / 16; ++j)  // 32 bytes further along k
+            mma_bf16_ss_pair(d, ad + 2 * j, bd + 2 * j, idesc, k > 0 || j > 0);
+          tc_commit_pair_mc(empty + 8 * r.slot, 3u);
+          r.next(p.slots);
+        }
+        if (ok) tc_commit_pair_mc(summed + 8 * acc.slot, 3u);
+        acc.next(2);
+      }
+    }
+  } else {
+    // lane + 32 (warp % 4) = token of the CTA, half of the columns
+    // in two tiles of 32 x 32 by turns, into which the addend is copied two
+    // chunks ahead (a load that is waited for takes its turn behind the operands'
+    // copies: 4000 cycles)
+    float* tiles_at = reinterpret_cast<float*>(smem + kRingBytes) + warp * (2 * 32 * kChunk);
+    const int quarter = warp % 4, side = warp / 4;
+    const int chunks = (p.out_cols + kChunk - 1) / kChunk;
+    const int first = side == 0 ? 0 : (chunks + 1) / 2, last = side == 0 ? (chunks + 1) / 2 : chunks;
+    const int row = lane >> 3, quad = lane & 7;  // of a store: four rows at a time
+    const bool ahead = p.a.addend != nullptr && p.columns % 4 == 0;
+    Ring acc;
+    for (int tile = cluster; tile < tiles; tile += clusters) {
+      int m, n;
+      place(tile, &m, &n);
+      const int m0 = (2 * m + static_cast<int>(rank)) * kTileM;  // its own tokens from here on
+      const int t0 = first_token(m0, p.a.tokens) + quarter * 32 + row;
+      const int c0 = n * p.out_cols + quad * 4;
+      const auto fetch = [&](int c) {
+        if (ahead && c < last) {
+          const uint32_t to = smem_u32(tiles_at + (c - first & 1) * (32 * kChunk));
+          const int column = c0 + c * kChunk;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int token = t0 + 4 * i;
+            const bool in = token >= m0 && token < p.a.tokens && column < p.columns;
+            copy16_of(to + tile_at(4 * i + row, quad) * 4,
+                      p.a.addend + (in ? static_cast<long long>(token) * p.columns + column : 0),
+                      in ? 16 : 0);
+          }
+        }
+        copies_commit();
+      };
+      fetch(first);
+      fetch(first + 1);
+      const bool ok = __all_sync(0xffffffffu, dense_wait<true>(summed + 8 * acc.slot, acc.phase, failed));
+      tc_fence_after();
+      const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 * acc.slot;
+#pragma unroll 1
+      for (int c = first; c < last; ++c) {
+        float* here = tiles_at + (c - first & 1) * (32 * kChunk);
+        float v[32];
+        tmem_load32(at + c * kChunk, v);
+        if (p.a.gated) {
+          float up[32];
+          tmem_load32(at + p.half + c * kChunk, up);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = silu_times(v[i], up[i]);
+        }
+        if (c == last - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * acc.slot, leader));
+        }
+        copies_wait<1>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float4* at4 = reinterpret_cast<float4*>(here + tile_at(lane, i));
+          float4 sum = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          if (ahead) sum = add4(sum, *at4);
+          const float nan = __uint_as_float(0x7FC00000u);
+          *at4 = ok ? sum : make_float4(nan, nan, nan, nan);
+        }
+        __syncwarp();
+        const bool in = c * kChunk + quad * 4 < p.out_cols;  // (else the next tile's)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float4 sum = *reinterpret_cast<const float4*>(here + tile_at(4 * i + row, quad));
+          const int token = t0 + 4 * i, column = c0 + c * kChunk;
+          if (token < m0 || !in) continue;
+          if (!ahead) sum = add4(sum, load_addend(p, token, column));
+          store_out(p, token, column, sum);
+        }
+        __syncwarp();
+        fetch(c + 2);
+      }
+      if (first == last) {  // no columns for this side
+        tc_fence_before();
+        if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * acc.slot, leader));
+      }
+      acc.next(2);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  cluster_sync_all();  // nothing reaches across any more
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Where tiles are few: 128 tokens x 2 * half weight rows by a cluster whose CTAs
+// split the columns of x. Their sums meet through the cluster's shared memory.
+__global__ void __launch_bounds__(kDenseThreads, 1)
+    w4a16_dense_split_kernel(const __grid_constant__ DenseArgs p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t bars[2 * kMaxSlots + 1];
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed_word;
+  volatile int* failed = &failed_word;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots, summed = full + 16 * kMaxSlots;
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
+  const uint32_t slot_bytes = a_bytes + 2 * b_bytes;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / p.split;
+  const int m = tile % p.m_tiles, n = tile / p.m_tiles;
+  const int m0 = first_token(m * kTileM, p.a.tokens), skip = m * kTileM - m0;
+  const int k0 = p.k_steps * rank / p.split, k1 = p.k_steps * (rank + 1) / p.split;
+  const uint32_t tmem_cols = p.half <= 16 ? 32 : p.half <= 32 ? 64 : p.half <= 64 ? 128 : 256;
+  if (warp == kWarpMma) {
+    if (lane == 0) {
+      for (int i = 0; i < p.slots; ++i) {
+        mbar_init(full + 8 * i, 1);
+        mbar_init(empty + 8 * i, 1);
+      }
+      mbar_init(summed, 1);
+      *failed = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(&tmem_at), tmem_cols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  grid_dependency_wait();
+  grid_dependents_go();
+  const uint32_t tmem = tmem_at;
+  bool ok = true;
+  if (warp == kWarpCopy) {
+    if (elect_one()) {
+      Ring r;
+      int k = k0;
+      const int w0 = p.a.gated ? n * p.half : 2 * n * p.half;
+      const int w1 = w0 + (p.a.gated ? p.columns : p.half);
+      for (; k < k1; ++k) {
+        ok = dense_wait<false>(empty + 8 * r.slot, r.phase ^ 1u, failed);
+        if (!ok) break;
+        const uint32_t to = ring + r.slot * slot_bytes, bar = full + 8 * r.slot;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        tma_load_2d(to + a_bytes, &p.weight, k * kKStep, w0, bar);
+        tma_load_2d(to + a_bytes + b_bytes, &p.weight, k * kKStep, w1, bar);
+        tma_load_2d(to, &p.x, k * kKStep, m0, bar);
+        r.next(p.slots);
+      }
+      if (!ok)  // copies in flight land before the CTA ends
+        for (int i = std::max(0, k - k0 - p.slots); i < k - k0; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(full + 8 * (i % p.slots), i / p.slots & 1) &&
+                 clock64() - t0 < kGiveUpCycles) {
+          }
+        }
+    }
+  } else if (warp == kWarpMma) {
+    if (elect_one()) {
+      Ring r;
+      const uint32_t idesc = idesc_bf16(kTileM, static_cast<uint32_t>(2 * p.half));
+      for (int k = k0; k < k1; ++k) {
+        ok = dense_wait<false>(full + 8 * r.slot, r.phase, failed);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t from = ring + r.slot * slot_bytes;
+        const uint64_t ad = smem_desc_sw128_kmajor(from);
+        const uint64_t bd = smem_desc_sw128_kmajor(from + a_bytes);
+#pragma unroll
+        for (int j = 0; j < kKStep / 16; ++j)
+          mma_bf16_ss(tmem, ad + 2 * j, bd + 2 * j, idesc, k > k0 || j > 0);
+        tc_commit(empty + 8 * r.slot);
+        r.next(p.slots);
+      }
+      if (ok) tc_commit(summed);
+    }
+  } else if (warp < kSumWarps) {
+    ok = __all_sync(0xffffffffu, dense_wait<false>(summed, 0, failed));
+    tc_fence_after();
+    // (nothing reads the ring any more: all of its copies were multiplied)
+    const int quarter = warp % 4, side = warp / 4, pitch = 2 * p.half + 4;
+    float* row = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * pitch;
+    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const bool live = m0 + quarter * 32 < p.a.tokens;  // (whole warps)
+    for (int c = side * 16; live && c < 2 * p.half; c += 32) {
+      float v[16];
+      tmem_load16(at + c, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(row + c + 4 * i) =
+            ok ? make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3])
+               : make_float4(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u),
+                             __uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+  if (p.split > 1) cluster_sync_all();
+  // every CTA of the cluster finishes a share of the tile, four columns a thread
+  const int pitch = 2 * p.half + 4, quads = p.out_cols / 4;
+  const int rows = min(kTileM, p.a.tokens - m * kTileM);
+  const float* sums = reinterpret_cast<const float*>(smem);
+  const int begin = rank * kDenseThreads + static_cast<int>(threadIdx.x), stride = p.split * kDenseThreads;
+  const int r_step = stride / quads, q_step = stride - r_step * quads;
+  int r = begin / quads + skip, q = begin % quads;
+  for (; r < rows + skip; r += r_step, q += q_step) {
+    if (q >= quads) {
+      q -= quads;
+      if (++r >= rows + skip) break;
+    }
+    const int c = 4 * q;
+    const auto sum = [&](int column) {
+      const float* at = sums + r * pitch + column;
+      if (p.split == 1) return *reinterpret_cast<const float4*>(at);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s < p.split)
+          v = add4(v, ld_cluster_f32x4(map_to_cta(smem_u32(at), static_cast<uint32_t>(s))));
+      return v;
+    };
+    float4 v = sum(c);
+    if (p.a.gated) {
+      const float4 up = sum(p.half + c);
+      v = make_float4(silu_times(v.x, up.x), silu_times(v.y, up.y), silu_times(v.z, up.z),
+                      silu_times(v.w, up.w));
+    }
+    const int token = m0 + r, column = n * p.out_cols + c;
+    store_out(p, token, column, add4(v, load_addend(p, token, column)));
+  }
+  if (p.split > 1) cluster_sync_all();  // the sums stay until all have read them
+}
+
+namespace {
+
+constexpr int kMaxSplit = 8;
+
+int split_clusters_at_once(int ctas, int sms, int device, cudaError_t* error) {
+  static ClustersAtOnce known[kMaxSplit + 1];
+  if (ctas == 1) return sms;
+  return std::max(1, clusters_at_once(w4a16_dense_split_kernel, ctas, kDenseThreads, kSmemBytes,
+                                      known[ctas], device, error));
+}
+int pairs_at_once(int device, cudaError_t* error) {
+  static ClustersAtOnce known;
+  return std::max(1, clusters_at_once(w4a16_dense_pair_kernel, 2, kDenseThreads, kSmemBytes, known,
+                                      device, error));
+}
+
+// The faster kernel and its tile by an estimate in us: rounds of tiles times the
+// steps of 64 columns of each, which the operands' way into an SM bounds (50 bytes
+// a cycle: 16 KB of tokens and 128 bytes a weight row), plus what a launch, the
+// ring's first fill and the last tile's sums take. Measured (gated, hidden 7168 x
+// 4096, 64 / 576 / 2048 tokens): split by 4 14.6 / 63 / 179, pairs of 192 44 / 38 /
+// 92, pairs of 256 48 / 41 / 74 us.
+bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cudaError_t* error) {
+  const int columns = a.gated ? a.n / 2 : a.n;
+  const int steps = ceil_div(a.k, kKStep);
+  double least = 0;
+  bool pair = false;
+  const auto consider = [&](const DenseArgs& c, bool is_pair, double cost) {
+    if (least > 0 && cost >= least) return;
+    least = cost;
+    pair = is_pair;
+    *best = c;
+  };
+  for (int tile_n = 64; tile_n <= 256; tile_n += 64) {
+    DenseArgs c = {};
+    c.columns = columns;
+    c.half = tile_n / 2;
+    c.out_cols = a.gated ? c.half : tile_n;
+    c.n_tiles = ceil_div(columns, c.out_cols);
+    c.k_steps = steps;
+    const double gate = a.gated ? tile_n * 0.01 : 0;
+
+    c.m_tiles = ceil_div(a.tokens, 2 * kTileM);
+    c.split = 1;
+    c.slots = std::min(kMaxSlots, kRingBytes / ((kTileM + c.half) * kKStep * 2));
+    const double rounds = std::ceil(static_cast<double>(c.m_tiles) * c.n_tiles /
+                                    pairs_at_once(device, error));
+    consider(c, true, rounds * std::max(steps * (0.095 + tile_n * 0.00085), 2.0 + tile_n * 0.008) +
+                          5 + tile_n * 0.01 + gate);
+
+    c.m_tiles = ceil_div(a.tokens, kTileM);
+    c.slots = std::min(kMaxSlots, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
+    const double rows = std::min(a.tokens, kTileM);
+    for (c.split = 1; c.split <= kMaxSplit && c.split <= steps; c.split *= 2) {
+      const double waves = std::ceil(static_cast<double>(c.m_tiles) * c.n_tiles /
+                                     split_clusters_at_once(c.split, sms, device, error));
+      const double sums = rows / kTileM * (1 + tile_n * 0.012 + gate) / (c.split > 1 ? 1.5 : 1);
+      consider(c, false, waves * (ceil_div(steps, c.split) * (0.07 + tile_n * 0.00125) + 4.5 +
+                                  (c.split > 1 ? 1.5 : 0) + sums));
+    }
+  }
+  return pair;
+}
+
+}  // namespace
+
+cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) {
+  if (args.tokens <= kDenseFewTokens) return launch_dense_few(args, sms, stream);
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device >= kMaxDevices) return cudaErrorInvalidDevice;
+  DenseArgs p;
+  const bool pair = dense_shape(args, sms, device, &p, &e);
+  if (e != cudaSuccess) return e;
+  p.a = args;
+  if (!encode_rows_tmap(&p.x, args.x, args.tokens, args.k, args.x_stride, kTileM) ||
+      !encode_rows_tmap(&p.weight, args.weight, args.n, args.k, args.k, p.half))
+    return cudaErrorInvalidValue;
+  const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
+  e = cudaFuncSetAttribute(pair ? w4a16_dense_pair_kernel : w4a16_dense_split_kernel,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  if (pair) {
+    const int clusters = static_cast<int>(std::min<long long>(tiles, pairs_at_once(device, &e)));
+    return launch_dependent(w4a16_dense_pair_kernel, 2 * clusters, kDenseThreads, kSmemBytes, 2,
+                            stream, p);
+  }
+  if (tiles * p.split > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int smem = 1024 + std::max(p.slots * (kTileM + 2 * p.half) * kKStep * 2,
+                                   kTileM * (2 * p.half + 4) * 4);
+  return launch_dependent(w4a16_dense_split_kernel, static_cast<int>(tiles) * p.split, kDenseThreads,
+                          static_cast<size_t>(smem), p.split, stream, p);
+}
+
+}  // namespace w4a16

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -224,6 +225,42 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, s
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// How many clusters of a kernel run at once, by device (0: not asked yet).
+constexpr int kMaxDevices = 64;
+using ClustersAtOnce = std::atomic<int>[kMaxDevices];
+
+// How many clusters of `ctas` run at once on the current device (they stay
+// inside a GPC, so eights of one CTA an SM leave some SMs out). 0 and an error
+// if that cannot be said: a guess would let the same sizes take another order
+// of additions in one call than in the next.
+template <typename Kernel>
+int clusters_at_once(Kernel kernel, int ctas, int threads, size_t smem, ClustersAtOnce& known,
+                     int device, cudaError_t* error) {
+  if (const int n = known[device]) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  cudaError_t e = cudaSuccess;
+  if (smem > 0)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  if (e != cudaSuccess) {
+    *error = e;
+    return 0;
+  }
+  known[device] = n;
+  return n;
 }
 
 // The residual's addition and the RMS norm (norm.cu).

@@ -79,6 +79,27 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   return p;
 }
 
+// ------------------------------------------- copies of a thread's own ---
+
+// 16 bytes, global -> shared, waited for by groups.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+// The first `bytes` (16, or 0: nothing is read) of them, zeros behind.
+__device__ __forceinline__ void copy16_of(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+               : "memory");
+}
+// What was copied since the last one is a group.
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the last kLeft groups of this thread are there.
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // ------------------------------------------------ tensor copies (TMA) ---
 
 // One box of a 2-D tensor map at (col, row).
@@ -176,6 +197,14 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
 // Every thread of both CTAs of the cluster (all threads must take part).
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile(
@@ -194,6 +223,17 @@ __device__ __forceinline__ void grid_dependency_wait() {
 // of this grid has come here.
 __device__ __forceinline__ void grid_dependents_go() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// True in one lane of the (whole, converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t mine;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(mine));
+  return mine != 0;
 }
 
 // ------------------------------------------------------------- tcgen05 ---
