@@ -1,6 +1,8 @@
 """Host-side refusals of the products with one weight and of the block's norms.
 No GPU needed: no call here reaches a kernel."""
 
+import contextlib
+
 import pytest
 import torch
 
@@ -99,22 +101,81 @@ def test_tensors_of_the_wrong_kind_are_refused(lib):
 
 
 class Placed:
-    """Stands for a tensor on a device."""
+    """Stands for a matrix on a device."""
+    dtype = torch.bfloat16
 
-    def __init__(self, device):
-        self.index, self.device = device, f"cuda:{device}"
+    def __init__(self, device, shape=(4, 256)):
+        self.index, self.device, self.shape = device, f"cuda:{device}", torch.Size(shape)
 
     def get_device(self):
         return self.index
 
+    def dim(self):
+        return len(self.shape)
 
-def test_one_device_for_all_tensors(monkeypatch):
-    monkeypatch.setattr(ops, "_current_device", lambda: 1)
-    made = []
-    monkeypatch.setattr(torch.cuda, "device", lambda d: made.append(d) or "made current")
-    assert ops._one_device("f", Placed(1), Placed(1), None) is ops._HERE and not made
-    assert ops._one_device("f", Placed(2), None, Placed(2)) == "made current"
-    assert made == [2]
-    with pytest.raises(ops.W4A16Error) as e:
-        ops._one_device("f", Placed(1), Placed(0))
-    assert e.value.status == INV
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return (self.shape[-1], 1)
+
+    def data_ptr(self):
+        return P
+
+
+class Entered(Exception):
+    pass
+
+
+def test_the_tensors_device_is_made_current(lib, monkeypatch):
+    current = [0]
+    monkeypatch.setattr(ops, "_current_device", lambda: current[0])
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d
+        try:
+            yield
+        finally:
+            current[0] = before
+    monkeypatch.setattr(torch.cuda, "device", device)
+
+    def stream(d):
+        assert current[0] == d == 1
+        raise Entered
+    monkeypatch.setattr(ops, "_current_stream", stream)
+    x, w, v = Placed(1), Placed(1, (8, 256)), Placed(1, (256,))
+    with pytest.raises(Entered):
+        ops.w4a16_dense(x, w, out=Placed(1, (4, 8)))
+    with pytest.raises(Entered):
+        ops.w4a16_block_norm(x, v, out=(Placed(1), Placed(1), None, None))
+    assert current == [0]
+    # on two devices: refused
+    for call in (lambda: ops.w4a16_dense(x, Placed(0, (8, 256)), out=Placed(1, (4, 8))),
+                 lambda: ops.w4a16_dense(x, w, out=Placed(0, (4, 8))),
+                 lambda: ops.w4a16_block_norm(x, Placed(0, (256,)), out=(x, x, None, None)),
+                 lambda: ops.w4a16_block_norm(x, v, residual=Placed(2), out=(x, x, None, None))):
+        with pytest.raises(ops.W4A16Error) as e:
+            call()
+        assert e.value.status == INV
+
+
+def test_shared_experts_that_do_not_fit_are_refused(lib):
+    from w4a16_int4_moe_gb300 import moe
+    bf = torch.bfloat16
+    gu, dn = torch.zeros(128, 96, dtype=bf), torch.zeros(96, 64, dtype=bf)
+    assert moe.SharedExpert(gu, dn).hidden == 96
+    for bad in ((gu, dn.t()), (gu[:64], dn), (gu[:, :64], dn), (gu[0], dn)):
+        with pytest.raises(ValueError):
+            moe.SharedExpert(*bad)
+    blob = torch.zeros(16, dtype=torch.uint8)
+    glu = moe.PackedExperts(blob, 1, 128, 96, GLU)
+    packed = moe.PackedExperts(blob, 1, 96, 64)
+    expert = moe.PackedSharedExpert(glu, packed, 8)
+    with pytest.raises(ValueError):
+        expert.forward(torch.zeros(9, 96, dtype=bf))
+    for bad in ((moe.PackedExperts(blob, 1, 128, 96), packed), (glu, moe.PackedExperts(blob, 1, 96, 96)),
+                (moe.PackedExperts(blob, 2, 128, 96, GLU), packed),
+                (glu, moe.PackedExperts(blob, 2, 96, 64))):
+        with pytest.raises(ValueError):
+            moe.PackedSharedExpert(*bad, 8)

@@ -293,6 +293,95 @@ class W4A16MoE:
         return out
 
 
+class SharedExpert:
+    """An expert that every token passes, weights in BF16: gate_up [2I, H] (gate
+    rows, then up rows) and down [H, I]. Two launches for any number of tokens
+    (w4a16_dense); the activation between them is BF16."""
+
+    def __init__(self, gate_up: torch.Tensor, down: torch.Tensor):
+        if (gate_up.dim() != 2 or down.dim() != 2 or gate_up.shape[0] != 2 * down.shape[1]
+                or gate_up.shape[1] != down.shape[0]):
+            raise ValueError("gate_up is [2I, H], down [H, I]")
+        self.gate_up, self.down = gate_up, down
+        self.hidden, self.inter = down.shape
+
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, add: bool = False,
+                stream=None) -> torch.Tensor:
+        """x BF16 [T, H] -> fp32 [T, H]; add: onto what out holds."""
+        act = ops.w4a16_dense(x, self.gate_up, gated=True, stream=stream)
+        return ops.w4a16_dense(act, self.down, addend=out if add else None,
+                               out_dtype=torch.float32, out=out, stream=stream)
+
+
+class PackedSharedExpert:
+    """SharedExpert with INT4 weights in the routed experts' own format: gate_up
+    packed with W4A16_LAYOUT_KTILE64_GLU16, both of one expert. Up to
+    W4A16_FEW_TOKENS_MAX tokens take two launches (w4a16_linear_few_tokens), more
+    the GEMM path, planned for max_tokens, with every token routed to the one
+    expert."""
+
+    def __init__(self, gate_up: PackedExperts, down: PackedExperts, max_tokens: int):
+        if gate_up.num_experts != 1 or gate_up.layout != ops.W4A16_LAYOUT_KTILE64_GLU16:
+            raise ValueError("a shared expert is one expert with GLU16 gate_up weights")
+        if down.num_experts != 1 or gate_up.n != 2 * down.k or gate_up.k != down.n:
+            raise ValueError("gate_up is [1, 2I, H], down [1, H, I]")
+        self.gate_up, self.down = gate_up, down
+        self.hidden, self.inter = down.n, down.k
+        self.max_tokens = max_tokens
+        self.layer = None
+        if max_tokens > ops.W4A16_FEW_TOKENS_MAX:
+            self.layer = W4A16MoE(gate_up, down, 1, max_tokens, single_launch=False)
+            dev = self.layer.device
+            self.ids = torch.zeros((max_tokens, 1), dtype=torch.int32, device=dev)
+            self.weights = torch.ones((max_tokens, 1), dtype=torch.float32, device=dev)
+
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, add: bool = False,
+                stream=None) -> torch.Tensor:
+        """x BF16 [T, H] -> fp32 [T, H]; add: onto what out holds."""
+        tokens = x.shape[0]
+        if tokens > self.max_tokens:
+            raise ValueError("more tokens than the expert was planned for")
+        if tokens <= ops.W4A16_FEW_TOKENS_MAX:
+            act = ops.w4a16_linear_few_tokens(x, self.gate_up.packed, self.gate_up.n,
+                                              self.gate_up.layout, stream=stream)
+            return ops.w4a16_linear_few_tokens(act, self.down.packed, self.down.n,
+                                               addend=out if add else None,
+                                               out_dtype=torch.float32, out=out, stream=stream)
+        layer = self.layer
+        layer.align(self.ids[:tokens], stream)
+        layer.gate_up_act(x, tokens, stream)
+        return ops.w4a16_moe_indexed_gemm(
+            ops.W4A16_DOWN, self.down.packed, 1, self.down.n, self.down.k, layer.act_buf[:tokens],
+            tokens, 1, layer.sorted_ids_dn, layer.expert_ids_dn, layer.ntp_dn, layer.plan_dn,
+            layer.workspace, topk_weights=self.weights[:tokens], out=out,
+            flags=ops.W4A16_FLAG_ACCUMULATE if add else 0, stream=stream)
+
+
+@dataclass
+class BlockNorm:
+    """The norms around the border between a block and the next one
+    (w4a16_block_norm): the norm of the block's output (post_weight, None: none),
+    its gate (BF16 [H] or [T, H]) and scales, the residual, and the norm in front
+    of the next block (pre_weight). weight_offset is added to both weights."""
+    pre_weight: torch.Tensor
+    post_weight: Optional[torch.Tensor] = None
+    gate: Optional[torch.Tensor] = None
+    branch_scale: float = 1.0
+    residual_scale: float = 1.0
+    weight_offset: float = 0.0
+    eps: float = 1e-6
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                fp8_group: int = ops.W4A16_FP8_NONE, stream=None):
+        """x fp32 or BF16 [T, H], residual BF16 [T, H] -> (the next block's rows
+        BF16, the new residual BF16, e4m3 rows and their scales or None)."""
+        return ops.w4a16_block_norm(
+            x, self.pre_weight, self.eps, post_weight=self.post_weight, gate=self.gate,
+            residual=residual, branch_scale=self.branch_scale,
+            residual_scale=self.residual_scale, weight_offset=self.weight_offset,
+            fp8_group=fp8_group, stream=stream)
+
+
 class MoEBlock:
     """The MoE half of a decoder layer on one GPU: the residual's addition and
     the RMS norm, the router's product, and the layer's experts.
@@ -303,16 +392,22 @@ class MoEBlock:
     many rows an expert the GEMM path may be faster before it.) fp8_rows=True
     hands the few-token experts the norm's 8-bit rows (the form that tokens have
     after an exchange in 8 bits) and has no effect on the GEMM path; the router
-    always reads the BF16 rows."""
+    always reads the BF16 rows. shared (SharedExpert or PackedSharedExpert): the
+    expert that every token passes, added to the routed experts' sum (where the
+    routed experts are spread over GPUs, give it to one of them). after: the norms
+    that forward_layer runs behind the block."""
 
     def __init__(self, norm_weight: torch.Tensor, router_weight: torch.Tensor, experts: W4A16MoE,
                  eps: float = 1e-6, expert_offset: int = 0, renormalize: bool = True,
-                 fp8_rows: bool = False):
+                 fp8_rows: bool = False, shared=None, after: Optional[BlockNorm] = None):
+        if shared is not None and shared.hidden != experts.hidden:
+            raise ValueError("the shared expert does not match the layer's hidden size")
         if norm_weight.shape != (experts.hidden,) or router_weight.shape[1] != experts.hidden:
             raise ValueError("norm and router weights do not match the layer's hidden size")
         self.norm_weight, self.router_weight, self.layer = norm_weight, router_weight, experts
         self.eps, self.expert_offset, self.renormalize = eps, expert_offset, renormalize
         self.fp8_rows = fp8_rows
+        self.shared, self.after = shared, after
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None, stream=None):
@@ -332,4 +427,16 @@ class MoEBlock:
         else:
             result = self.layer.forward_from_logits(y, logits, self.expert_offset,
                                                     self.renormalize, out=out, stream=stream)
+        if self.shared is not None:
+            self.shared.forward(y, out=result, add=True, stream=stream)
         return result, x if residual is None else new_residual
+
+    def forward_layer(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                      fp8_group: int = ops.W4A16_FP8_NONE, stream=None):
+        """forward() and the norms behind it (`after`), on a GPU that holds all of
+        the layer's experts: (the next block's rows BF16 [T, H], the new residual
+        BF16, e4m3 rows and their scales or None)."""
+        if self.after is None:
+            raise ValueError("forward_layer needs the norms behind the block")
+        y, residual = self.forward(x, residual, stream=stream)
+        return self.after.forward(y, residual, fp8_group, stream)

@@ -456,10 +456,10 @@ def _blob(fn: str, what: str, t: torch.Tensor, size: int):
     return t.data_ptr()
 
 
-def _rows(fn: str, what: str, t: torch.Tensor, dtype=_BF16):
-    """t is BF16 (or of this type) [rows, columns] on a GPU with adjacent columns;
-    returns (address, rows, columns, row stride)."""
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2:
+def _rows(fn: str, what: str, t: torch.Tensor):
+    """t is BF16 [rows, columns] on a GPU with adjacent columns; returns
+    (address, rows, columns, row stride)."""
+    if t.dtype is not _BF16 or not t.is_cuda or t.dim() != 2:
         _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}")
     rows, columns = t.shape
     if t.is_contiguous():
@@ -583,37 +583,55 @@ def w4a16_moe_few_tokens(packed_gate_up: torch.Tensor, packed_down: torch.Tensor
 _current_device = getattr(torch._C, "_cuda_getDevice", None)  # (of CUDA builds)
 
 
-def _one_device(fn: str, x: torch.Tensor, *others):
-    """The context in which x's device is the current one; the other tensors
-    (None: absent) are on it too, else W4A16_ERR_INVALID_ARG."""
-    device = x.get_device()
-    for t in others:
-        if t is not None and t.get_device() != device:
-            _refuse(fn, f"tensors on {x.device} and on {t.device}")
-    if device < 0 or device == _current_device():
-        return _HERE
-    return torch.cuda.device(device)
+def _place(fn: str, what: str, t: torch.Tensor, dtype, shape, device: int):
+    """The address of t, a contiguous tensor of this type and shape on this
+    device (else W4A16_ERR_INVALID_ARG)."""
+    if (t.dtype is not dtype or t.get_device() != device or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, "
+                    f"not contiguous {dtype} {tuple(shape)} on GPU {device}")
+    return t.data_ptr()
 
 
-def _product(fn: str, call, x, n: int, k: int, gated: bool, addend, out, out_dtype, stream, weight,
-             *sizes):
-    """The part that both products share: x's rows, addend, output and the call."""
-    x_at, tokens, columns, x_stride = _rows(fn, "x", x)
-    if columns != k:
-        _refuse(fn, f"x {tuple(x.shape)} for a weight of {k} columns")
-    shape = (tokens, n // 2 if gated else n)
-    with _one_device(fn, x, weight, addend, out):
-        if out is None:
-            with on_stream(stream):
-                out = torch.empty(shape, dtype=out_dtype, device=x.device)
-        dtype = out.dtype
-        if dtype is not _F32 and dtype is not _BF16:
-            _refuse(fn, f"out: {dtype}")
-        _check(fn, call(
-            weight.data_ptr(), *sizes, x_at, x_stride, tokens,
-            None if addend is None else _need(fn, "addend", addend, _F32, shape),
-            _need(fn, "out", out, dtype, shape),
-            W4A16_DTYPE_F32 if dtype is _F32 else W4A16_DTYPE_BF16, _raw_stream(x, stream)))
+def _place_rows(fn: str, what: str, t: torch.Tensor, dtype, shape, device: int):
+    """(address, row stride) of t, rows of this type and shape with adjacent
+    columns on this device (else W4A16_ERR_INVALID_ARG)."""
+    if t.dtype is dtype and t.get_device() == device and t.shape == shape:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        pitch, step = t.stride()
+        if step == 1 or shape[1] == 1:
+            return t.data_ptr(), pitch if shape[0] > 1 else max(pitch, shape[1])
+    _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}, not rows "
+                f"{dtype} {tuple(shape)} on GPU {device}")
+
+
+def _device_of(fn: str, what: str, t: torch.Tensor) -> int:
+    """The GPU that t, a matrix, is on."""
+    device = t.get_device()
+    if device < 0 or t.dim() != 2:
+        _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}")
+    return device
+
+
+def _product(fn: str, call, x, device: int, n: int, k: int, gated: bool, addend, out, out_dtype,
+             stream, weight_at, last):
+    """What both products share: x's rows, addend, output and the call. last: the
+    weight's arguments behind its address."""
+    shape = (x.shape[0], n // 2 if gated else n)
+    x_at, x_stride = _place_rows(fn, "x", x, _BF16, (shape[0], k), device)
+    if out is None:
+        with on_stream(stream):
+            out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    dtype = out.dtype
+    if dtype is not _F32 and dtype is not _BF16:
+        _refuse(fn, f"out: {dtype}")
+    _check(fn, call(
+        weight_at, *last, x_at, x_stride, shape[0],
+        None if addend is None else _place(fn, "addend", addend, _F32, shape, device),
+        _place(fn, "out", out, dtype, shape, device),
+        W4A16_DTYPE_F32 if dtype is _F32 else W4A16_DTYPE_BF16,
+        _current_stream(device) if stream is None else stream.cuda_stream))
     return out
 
 
@@ -627,14 +645,18 @@ def w4a16_linear_few_tokens(x: torch.Tensor, packed: torch.Tensor, n: int,
     x BF16 [T, k], rows may be strided. out (or out_dtype): FP32 or BF16; out may
     be addend."""
     fn = "w4a16_linear_few_tokens"
-    if x.dim() != 2:
-        _refuse(fn, f"x {tuple(x.shape)}")
+    device = _device_of(fn, "x", x)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return w4a16_linear_few_tokens(x, packed, n, layout, addend, out_dtype, out, stream)
     k = x.shape[1]
     # 128-row tiles of 64-column steps, 4608 bytes each
-    _blob(fn, "packed", packed, -(-n // 128) * -(-k // 64) * 4608)
-    return _product(fn, load_library().w4a16_linear_few_tokens, x, n, k,
-                    layout == W4A16_LAYOUT_KTILE64_GLU16, addend, out, out_dtype, stream, packed,
-                    layout, n, k)
+    at = _blob(fn, "packed", packed, -(-n // 128) * -(-k // 64) * 4608)
+    if packed.get_device() != device:
+        _refuse(fn, f"x on {x.device}, packed on {packed.device}")
+    return _product(fn, load_library().w4a16_linear_few_tokens, x, device, n, k,
+                    layout == W4A16_LAYOUT_KTILE64_GLU16, addend, out, out_dtype, stream, at,
+                    (layout, n, k))
 
 
 def w4a16_dense(x: torch.Tensor, weight: torch.Tensor, gated: bool = False,
@@ -645,12 +667,16 @@ def w4a16_dense(x: torch.Tensor, weight: torch.Tensor, gated: bool = False,
     silu(x . Wgate^T) * (x . Wup^T), [T, n/2]. x BF16 [T, k], rows may be
     strided. out (or out_dtype): FP32 or BF16; out may be addend."""
     fn = "w4a16_dense"
+    device = _device_of(fn, "x", x)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return w4a16_dense(x, weight, gated, addend, out_dtype, out, stream)
     if weight.dim() != 2:
         _refuse(fn, f"weight {tuple(weight.shape)}")
-    n, k = weight.shape
-    _need(fn, "weight", weight, _BF16, (n, k))
-    return _product(fn, load_library().w4a16_dense, x, n, k, gated, addend, out, out_dtype, stream,
-                    weight, n, k, 1 if gated else 0)
+    n, k = size = weight.shape
+    return _product(fn, load_library().w4a16_dense, x, device, n, k, gated, addend, out, out_dtype,
+                    stream, _place(fn, "weight", weight, _BF16, size, device),
+                    (n, k, 1 if gated else 0))
 
 
 def w4a16_block_norm(x: torch.Tensor, pre_weight: Optional[torch.Tensor], eps: float = 1e-6,
@@ -670,50 +696,49 @@ def w4a16_block_norm(x: torch.Tensor, pre_weight: Optional[torch.Tensor], eps: f
     may be the residual itself). x FP32 or BF16 [T, H], residual BF16 [T, H], gate
     BF16 [T, H] or [H]; rows may be strided."""
     fn = "w4a16_block_norm"
+    device = _device_of(fn, "x", x)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return w4a16_block_norm(x, pre_weight, eps, post_weight, gate, residual, branch_scale,
+                                    residual_scale, weight_offset, fp8_group, bf16_out, out,
+                                    stream)
+    rows, hidden = shape = x.shape
     f32 = x.dtype is _F32
-    x_at, rows, hidden, x_stride = _rows(fn, "x", x, _F32 if f32 else _BF16)
-    shape, groups = (rows, hidden), (rows, 0)
-
-    def weight(what, t):
-        return None if t is None else _need(fn, what, t, _BF16, (hidden,))
-
-    def same_rows(what, t):
-        at, *size, stride = _rows(fn, what, t)
-        if (*size,) != shape:
-            _refuse(fn, f"{what} {tuple(t.shape)} for x {tuple(x.shape)}")
-        return at, stride
-
-    post_at, pre_at = weight("post_weight", post_weight), weight("pre_weight", pre_weight)
-    r_at = g_at = None
+    x_at, x_stride = _place_rows(fn, "x", x, _F32 if f32 else _BF16, shape, device)
+    post_at = pre_at = r_at = g_at = None
     r_stride = g_stride = 0
+    if post_weight is not None:
+        post_at = _place(fn, "post_weight", post_weight, _BF16, (hidden,), device)
+    if pre_weight is not None:
+        pre_at = _place(fn, "pre_weight", pre_weight, _BF16, (hidden,), device)
     if residual is not None:
-        r_at, r_stride = same_rows("residual", residual)
+        r_at, r_stride = _place_rows(fn, "residual", residual, _BF16, shape, device)
     if gate is not None:
         if gate.dim() == 1:
-            g_at = weight("gate", gate)
+            g_at = _place(fn, "gate", gate, _BF16, (hidden,), device)
         else:
-            g_at, g_stride = same_rows("gate", gate)
+            g_at, g_stride = _place_rows(fn, "gate", gate, _BF16, shape, device)
+    groups = 0
     if fp8_group != W4A16_FP8_NONE:
         if fp8_group not in (W4A16_FP8_ROW, W4A16_FP8_GROUP):
             raise W4A16Error(fn, W4A16_ERR_UNSUPPORTED, f"fp8_group {fp8_group}")
-        groups = (rows, 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP))
-    with _one_device(fn, x, post_weight, pre_weight, residual, gate, *(out or ())):
-        if out is None:
-            normed = pre_weight is not None
-            kinds = ((shape, _BF16, bf16_out and normed), (shape, _BF16, True),
-                     (shape, _E4M3, fp8_group), (groups, _F32, fp8_group))
-            with on_stream(stream):
-                out = tuple(torch.empty(size, dtype=dtype, device=x.device) if wanted else None
-                            for size, dtype, wanted in kinds)
-        y, h, y8, scales = out
-        _check(fn, load_library().w4a16_block_norm(
-            x_at, W4A16_DTYPE_F32 if f32 else W4A16_DTYPE_BF16, x_stride, post_at, g_at, g_stride,
-            r_at, r_stride, pre_at, weight_offset, branch_scale, residual_scale, eps, rows, hidden,
-            None if y is None else _need(fn, "out", y, _BF16, shape),
-            None if h is None else _need(fn, "h_out", h, _BF16, shape),
-            None if y8 is None else _need(fn, "out_fp8", y8, _E4M3, shape),
-            None if scales is None else _need(fn, "scales", scales, _F32, groups),
-            fp8_group, _raw_stream(x, stream)))
+        groups = 1 if fp8_group == W4A16_FP8_ROW else -(-hidden // W4A16_FP8_GROUP)
+    if out is None:
+        normed = pre_weight is not None
+        kinds = ((shape, _BF16, bf16_out and normed), (shape, _BF16, True),
+                 (shape, _E4M3, fp8_group), ((rows, groups), _F32, fp8_group))
+        with on_stream(stream):
+            out = tuple(torch.empty(size, dtype=dtype, device=x.device) if wanted else None
+                        for size, dtype, wanted in kinds)
+    y, h, y8, scales = out
+    _check(fn, load_library().w4a16_block_norm(
+        x_at, W4A16_DTYPE_F32 if f32 else W4A16_DTYPE_BF16, x_stride, post_at, g_at, g_stride,
+        r_at, r_stride, pre_at, weight_offset, branch_scale, residual_scale, eps, rows, hidden,
+        None if y is None else _place(fn, "out", y, _BF16, shape, device),
+        None if h is None else _place(fn, "h_out", h, _BF16, shape, device),
+        None if y8 is None else _place(fn, "out_fp8", y8, _E4M3, shape, device),
+        None if scales is None else _place(fn, "scales", scales, _F32, (rows, groups), device),
+        fp8_group, _current_stream(device) if stream is None else stream.cuda_stream))
     return out
 
 
