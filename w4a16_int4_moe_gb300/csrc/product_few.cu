@@ -8,10 +8,16 @@
 // launch, a first load and the sums' way out. Every warp copies its own steps of
 // 64 columns into slots of its own (no barrier between warps before the sums),
 // several steps ahead, and multiplies with m16n8k16 MMAs whose M side are the
-// weight rows. A packed code enters as the BF16 number 16 + q, exact, one shift
-// and one three-input logic operation for two; the 24 too much comes off through
-// two more MMAs a group of 32; the scale is applied to the group's FP32 sum. So
-// no weight is rounded.
+// weight rows. The packed codes become BF16 numbers q - 8, and a group's scale is
+// applied to its FP32 sum, so no weight is rounded.
+//
+// One token, in a graph: BF16, 4096 x 7168 gated 10.7 us, 5.5 TB/s (0.81 of the
+// copy rate); INT4, the same 6.8 us for 16.5 MB, 7168 x 2048 4.4 us, where launch,
+// first load and sums are some 3 us; 16384 x 7168 16.4 us, 4.0 TB/s: the ALU pipe
+// (a shift and an AND-OR for two codes, at half rate) is busy two thirds of the
+// time, and 256 blocks on 152 SMs leave a sixth of it out. 32 tokens of 16384 x
+// 7168 32.6 us: 64 cycles of MMAs for 512 codes a scheduler, 15 us at their full
+// rate, which two warps a scheduler (176 registers) do not reach.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -24,6 +30,10 @@
 namespace w4a16 {
 
 namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxSmem = 232448;
 
 // d = a . b + c, BF16 operands
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -62,11 +72,34 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
   return static_cast<uint32_t>(row * 128 + ((c ^ (row & 1) << 2) << 4));
 }
 
+// Two codes, in bits 3 to 6 of each half word, as BF16 numbers q - 8: in those bits
+// of the number 16 a code is 16 + q, and both steps are exact. (sixteens is an
+// argument so that the compiler keeps one three-input operation: with two
+// constants it makes two of them, and 16384 x 7168 takes 18.8 instead of 16.1 us
+// for one token.)
+__device__ __forceinline__ uint32_t code_pair(uint32_t shifted, uint32_t sixteens) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(shifted), "r"(0x00780078u), "r"(sixteens));
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x41C041C0u));
+  return r;
+}
+
+// d0 += s * c0, d1 += s * c1 in one operation
+__device__ __forceinline__ void fma_pair(float& d0, float& d1, float s, float c0, float c1) {
+  asm("{\n\t.reg .b64 c, s, d;\n\t"
+      "mov.b64 c, {%3, %4};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 d, {%0, %1};\n\t"
+      "fma.rn.f32x2 d, s, c, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(s), "f"(c0), "f"(c1));
+}
+
 struct FewProduct {
   ProductArgs a;
-  int split;       // CTAs of a cluster, which share the columns
-  int steps;       // of 64 columns
-  int slot_bytes;  // of a warp's step
+  int blocks;         // of a cluster's rows
+  int split;          // CTAs of a cluster, which share the columns
+  int steps;          // of 64 columns
+  int slot_bytes;     // of a warp's step
+  uint32_t sixteens;  // 16 as two BF16 numbers
 };
 
 // Bytes of a step of 64 columns of a warp's rows and of the tokens.
@@ -74,53 +107,59 @@ constexpr int step_bytes(bool int4, int rows) { return rows * (int4 ? 36 : 128);
 
 }  // namespace
 
-// A cluster has 16 * kMt weight rows, a CTA of it a share of the columns, of
-// which its warps take steps of 64 by turns. A warp copies its steps (the
-// weights, and the tokens' columns) into slots of its own, kDepth ahead. The sums
-// of the warps meet in shared memory, those of the CTAs through the cluster's.
-template <bool kInt4, bool kGated, int kMt, int kNt, int kWarps, int kDepth>
-__global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const FewProduct p) {
-  constexpr int kThreads = kWarps * 32;
+// A cluster has blocks of 16 * kMt weight rows, one after the other, a CTA of it a
+// share of their columns, of which its warps take steps of 64 by turns. A warp
+// copies its steps (the weights, and the tokens' columns) into slots of its own,
+// kDepth ahead and on into the next block. The sums of the warps meet in shared
+// memory, those of the CTAs through the cluster's.
+template <bool kInt4, bool kGated, int kMt, int kNt, int kDepth>
+__global__ void __launch_bounds__(kThreads) w4a16_product_few_kernel(const FewProduct p) {
   constexpr int kRows = 16 * kMt;
   constexpr int kTokens = 8 * kNt;
   constexpr int kPitch = kRows + 4;  // of a token's sums
   static_assert(kMt % 2 == 0, "gate and up rows by sixteens, codes by 32 rows");
   extern __shared__ __align__(128) uint8_t smem[];
-  float* part = reinterpret_cast<float*>(smem);  // [kWarps][kTokens][kPitch], in the slots' place
   const ProductArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int block = static_cast<int>(blockIdx.x) / p.split;
+  const int begin = static_cast<int>(blockIdx.x) / p.split, stride = static_cast<int>(gridDim.x) / p.split;
   const int columns = kGated ? a.n / 2 : a.n;
   const int first = p.steps * rank / p.split + warp, last = p.steps * (rank + 1) / p.split;
   const uint32_t slots = smem_u32(smem) + static_cast<uint32_t>(warp * kDepth * p.slot_bytes);
+  float* part = reinterpret_cast<float*>(smem + kWarps * kDepth * p.slot_bytes);  // [kWarps / 2][kTokens][kPitch]
   constexpr uint32_t kWeightBytes = step_bytes(kInt4, kRows);
   // This lane's sources in the step that it fetches next. (k is a multiple of 8,
   // and a packed step is whole: only chunks of x, and of BF16 weights, can lie
   // behind the row's end.)
   constexpr int kWeightCopies = kInt4 ? kRows / 16 : kRows / 4;
   const uint8_t* w_from[kInt4 ? 2 : kWeightCopies];
-  if constexpr (kInt4) {
-    const int r0 = block * kRows;
-    const uint8_t* from = static_cast<const uint8_t*>(a.weight) +
-                          (static_cast<long long>(r0 / kTileRows) * p.steps + first) * kStepBytes;
-    w_from[0] = from + (r0 % kTileRows + lane) * 16;  // codes of row `lane`
-    w_from[1] = from + kStepQBytes + lane / (kRows / 8) * (kTileRows * 2) + r0 % kTileRows * 2 +
-                lane % (kRows / 8) * 16;
-  } else {
+  const uint16_t* x_from;
+  int c_from, next_block = first < last ? begin : p.blocks, next_step;
+  const auto point = [&](int block) {
+    if constexpr (kInt4) {
+      const int r0 = block * kRows;
+      const uint8_t* from = static_cast<const uint8_t*>(a.weight) +
+                            (static_cast<long long>(r0 / kTileRows) * p.steps + first) * kStepBytes;
+      w_from[0] = from + (r0 % kTileRows + lane) * 16;  // codes of row `lane`
+      w_from[1] = from + kStepQBytes + lane / (kRows / 8) * (kTileRows * 2) + r0 % kTileRows * 2 +
+                  lane % (kRows / 8) * 16;
+    } else {
 #pragma unroll
-    for (int j = 0; j < kWeightCopies; ++j) {
-      const int r = 4 * j + (lane >> 3);
-      int q = min(block * kRows + r, columns - 1);  // weight row
-      if constexpr (kGated)
-        q = min(block * (kRows / 2) + r / 32 * 16 + r % 16, columns - 1) + r / 16 % 2 * columns;
-      w_from[j] = static_cast<const uint8_t*>(a.weight) +
-                  (static_cast<long long>(q) * a.k + first * kKStep + (lane & 7) * 8) * 2;
+      for (int j = 0; j < kWeightCopies; ++j) {
+        const int r = 4 * j + (lane >> 3);
+        int q = min(block * kRows + r, columns - 1);  // weight row
+        if constexpr (kGated)
+          q = min(block * (kRows / 2) + r / 32 * 16 + r % 16, columns - 1) + r / 16 % 2 * columns;
+        w_from[j] = static_cast<const uint8_t*>(a.weight) +
+                    (static_cast<long long>(q) * a.k + first * kKStep + (lane & 7) * 8) * 2;
+      }
     }
-  }
-  const uint16_t* x_from = a.x + min(lane >> 3, a.tokens - 1) * a.x_stride + first * kKStep + (lane & 7) * 8;
-  int c_from = first * kKStep + (lane & 7) * 8;
+    next_step = first;
+    c_from = first * kKStep + (lane & 7) * 8;
+    x_from = a.x + min(lane >> 3, a.tokens - 1) * a.x_stride + c_from;
+  };
+  point(begin);
   grid_dependency_wait();
   grid_dependents_go();
 
@@ -128,6 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
   const long long x_four = 4 * a.x_stride;
   const int x_last = a.tokens - 1 - (lane >> 3);
   const auto fetch = [&](uint32_t slot) {
+    if (next_block >= p.blocks) return;
     const int bytes = c_from < a.k ? 16 : 0;
     if constexpr (kInt4) {
 #pragma unroll
@@ -151,9 +191,14 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
       if (4 * j <= x_last) copy16_of(slot + x_to + j * 512, from, bytes);
     x_from += kWarps * kKStep;
     c_from += kWarps * kKStep;
+    next_step += kWarps;
+    if (next_step >= last) {
+      next_block += stride;
+      if (next_block < p.blocks) point(next_block);
+    }
   };
 
-  float acc[kMt][kNt][4] = {};
+  float acc[kMt][kNt][4];
   uint32_t x_row[kNt][2];
 #pragma unroll
   for (int nt = 0; nt < kNt; ++nt)
@@ -176,17 +221,6 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt) x[nt] = load_shared16(slot + x_row[nt][h]);
       if constexpr (kInt4) {
-        // a code in bits 3 to 6 of the BF16 number 16 is 16 + q: 24 too much,
-        // which two MMAs take off all rows' sums at once
-        constexpr uint32_t kCodes = 0x00780078u, k16 = 0x41804180u, kMinus24 = 0xC1C0C1C0u;
-        const uint32_t minus[4] = {kMinus24, kMinus24, kMinus24, kMinus24};
-        const float none[4] = {};
-        float base[kNt][4];
-#pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) {
-          mma16816(base[nt], minus, x[nt].x, x[nt].y, none);
-          mma16816(base[nt], minus, x[nt].z, x[nt].w, base[nt]);
-        }
 #pragma unroll
         for (int j = 0; j < kMt / 2; ++j) {
           uint32_t w[4];
@@ -195,21 +229,19 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
           for (int i = 0; i < 2; ++i) {
             const int mt = 2 * j + i;
             const uint32_t w0 = w[2 * i], w1 = w[2 * i + 1];
-            const uint32_t a0[4] = {(w0 << 3 & kCodes) | k16, (w1 << 3 & kCodes) | k16,
-                                    (w0 >> 1 & kCodes) | k16, (w1 >> 1 & kCodes) | k16};
-            const uint32_t a1[4] = {(w0 >> 5 & kCodes) | k16, (w1 >> 5 & kCodes) | k16,
-                                    (w0 >> 9 & kCodes) | k16, (w1 >> 9 & kCodes) | k16};
+            const auto code = [&](uint32_t v) { return code_pair(v, p.sixteens); };
+            const uint32_t a0[4] = {code(w0 << 3), code(w1 << 3), code(w0 >> 1), code(w1 >> 1)};
+            const uint32_t a1[4] = {code(w0 >> 5), code(w1 >> 5), code(w0 >> 9), code(w1 >> 9)};
             const uint32_t pair = sc[j][2 * h + i];
             const float s0 = __uint_as_float(pair << 16), s1 = __uint_as_float(pair & 0xFFFF0000u);
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt) {
+              const float none[4] = {};
               float c[4];
-              mma16816(c, a0, x[nt].x, x[nt].y, base[nt]);
+              mma16816(c, a0, x[nt].x, x[nt].y, none);
               mma16816(c, a1, x[nt].z, x[nt].w, c);
-              acc[mt][nt][0] = fmaf(s0, c[0], acc[mt][nt][0]);
-              acc[mt][nt][1] = fmaf(s0, c[1], acc[mt][nt][1]);
-              acc[mt][nt][2] = fmaf(s1, c[2], acc[mt][nt][2]);
-              acc[mt][nt][3] = fmaf(s1, c[3], acc[mt][nt][3]);
+              fma_pair(acc[mt][nt][0], acc[mt][nt][1], s0, c[0], c[1]);
+              fma_pair(acc[mt][nt][2], acc[mt][nt][3], s1, c[2], c[3]);
             }
           }
         }
@@ -232,130 +264,154 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
   // a group of copies a slot, also an empty one
 #pragma unroll 1
   for (int d = 0; d < kDepth; ++d) {
-    if (first + d * kWarps < last) fetch(slots + d * p.slot_bytes);
+    fetch(slots + d * p.slot_bytes);
     copies_commit();
   }
   uint32_t slot = slots;
 #pragma unroll 1
-  for (int step = first; step < last; step += kWarps) {
-    copies_wait<kDepth - 1>();
-    __syncwarp();
-    multiply(slot);
-    __syncwarp();
-    if (step + kDepth * kWarps < last) fetch(slot);
-    copies_commit();
-    slot += p.slot_bytes;
-    if (slot == slots + kDepth * p.slot_bytes) slot = slots;
-  }
-  copies_wait<0>();
-  __syncthreads();
-
-  // [warp][token][row]
+  for (int block = begin; block < p.blocks; block += stride) {
 #pragma unroll
-  for (int mt = 0; mt < kMt; ++mt)
+    for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < kNt; ++nt)
+      for (int nt = 0; nt < kNt; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        part[(warp * kTokens + 8 * nt + 2 * t + (i & 1)) * kPitch + mt * 16 + g + (i >> 1) * 8] =
-            acc[mt][nt][i];
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.tokens * kRows; i += kThreads) {
-    const int at = i / kRows * kPitch + i % kRows;
-    float v = part[at];
-#pragma unroll
-    for (int s = 1; s < kWarps; ++s) v += part[s * kTokens * kPitch + at];
-    part[at] = v;
-  }
-  if (p.split > 1)
-    cluster_sync_all();
-  else
-    __syncthreads();
-  // every CTA of the cluster writes its share of the outputs
-  constexpr int kOut = kGated ? kRows / 2 : kRows;  // columns of the cluster
-  const int c0 = block * kOut;
-  for (int i = rank * kThreads + static_cast<int>(threadIdx.x); i < kOut * a.tokens;
-       i += p.split * kThreads) {
-    const int tok = i / kOut, c = i % kOut;
-    if (c0 + c >= columns) continue;
-    const auto sum = [&](int row) {
-      const float* at = part + tok * kPitch + row;
-      if (p.split == 1) return *at;
-      float v = 0.f;
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < p.split) v += ld_cluster_f32(map_to_cta(smem_u32(at), static_cast<uint32_t>(r)));
-      return v;
-    };
-    float v;
-    if constexpr (kGated) {
-      const int row = c / 16 * 32 + c % 16;
-      const float gate = sum(row);
-      v = gate / (1.f + expf(-gate)) * sum(row + 16);
-    } else {
-      v = sum(c);
+        for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
+#pragma unroll 1
+    for (int step = first; step < last; step += kWarps) {
+      copies_wait<kDepth - 1>();
+      __syncwarp();
+      multiply(slot);
+      __syncwarp();
+      fetch(slot);
+      copies_commit();
+      slot += p.slot_bytes;
+      if (slot == slots + kDepth * p.slot_bytes) slot = slots;
     }
-    const long long at = static_cast<long long>(tok) * columns + c0 + c;
-    if (a.addend != nullptr) v += a.addend[at];
-    if (a.f32_out)
-      static_cast<float*>(a.out)[at] = v;
+    // the sums of the upper half of the warps, on to those of the lower half
+    const auto each = [&](auto use) {
+      float* mine = part + ((warp % (kWarps / 2)) * kTokens + 2 * t) * kPitch + g;
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            use(mine[(8 * nt + (i & 1)) * kPitch + mt * 16 + (i >> 1) * 8], acc[mt][nt][i]);
+    };
+    __syncthreads();  // the block before is out
+    if (warp >= kWarps / 2) each([](float& at, float v) { at = v; });
+    __syncthreads();
+    if (warp < kWarps / 2) each([](float& at, float v) { at += v; });
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.tokens * kRows; i += kThreads) {
+      const int at = i / kRows * kPitch + i % kRows;
+      float v = part[at];
+#pragma unroll
+      for (int s = 1; s < kWarps / 2; ++s) v += part[s * kTokens * kPitch + at];
+      part[at] = v;
+    }
+    if (p.split > 1)
+      cluster_sync_all();
     else
-      static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+      __syncthreads();
+    // every CTA of the cluster writes its share of the outputs
+    constexpr int kOut = kGated ? kRows / 2 : kRows;  // columns of the cluster
+    const int c0 = block * kOut;
+    for (int i = rank * kThreads + static_cast<int>(threadIdx.x); i < kOut * a.tokens;
+         i += p.split * kThreads) {
+      const int tok = i / kOut, c = i % kOut;
+      if (c0 + c >= columns) continue;
+      const auto sum = [&](int row) {
+        const float* at = part + tok * kPitch + row;
+        if (p.split == 1) return *at;
+        float v = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < p.split) v += ld_cluster_f32(map_to_cta(smem_u32(at), static_cast<uint32_t>(r)));
+        return v;
+      };
+      float v;
+      if constexpr (kGated) {
+        const int row = c / 16 * 32 + c % 16;
+        const float gate = sum(row);
+        v = gate / (1.f + expf(-gate)) * sum(row + 16);
+      } else {
+        v = sum(c);
+      }
+      const long long at = static_cast<long long>(tok) * columns + c0 + c;
+      if (a.addend != nullptr) v += a.addend[at];
+      if (a.f32_out)
+        static_cast<float*>(a.out)[at] = v;
+      else
+        static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+    }
+    if (p.split > 1) cluster_sync_all();  // the sums stay until all have read them
   }
-  if (p.split > 1) cluster_sync_all();  // the sums stay until all have read them
 }
 
 namespace {
 
-template <bool kInt4, bool kGated, int kMt, int kNt, int kWarps, int kDepth>
+template <bool kInt4, bool kGated, int kMt, int kNt, int kDepth>
 cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
   constexpr int kRows = 16 * kMt;
-  const auto kernel = w4a16_product_few_kernel<kInt4, kGated, kMt, kNt, kWarps, kDepth>;
+  const auto kernel = w4a16_product_few_kernel<kInt4, kGated, kMt, kNt, kDepth>;
   FewProduct p;
   p.a = args;
+  p.sixteens = 0x41804180u;
+  p.blocks = ceil_div(args.n, kRows);
   p.steps = ceil_div(args.k, kKStep);
   p.slot_bytes = step_bytes(kInt4, kRows) + args.tokens * 128;
-  const int sums = kWarps * 8 * kNt * (kRows + 4) * 4;
-  const int smem = std::max(kWarps * kDepth * p.slot_bytes, sums);
+  const int smem = kWarps * kDepth * p.slot_bytes + kWarps / 2 * 8 * kNt * (kRows + 4) * 4;
   const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
-  const int blocks = ceil_div(args.n, kRows);
   // a cluster of two, four or eight where all CTAs still find an SM and every
   // warp a step. (Eights that want an SM each do not all find a place at once: 512
   // rows of 7168 in BF16 7.6 us, in fours 4.5.)
   const int most = smem > 100 << 10 ? 4 : 8;
   p.split = 1;
-  while (p.split < most && 2 * blocks * p.split <= sms && p.steps >= 2 * p.split * kWarps)
+  while (p.split < most && 2 * p.blocks * p.split <= sms && p.steps >= 2 * p.split * kWarps)
     p.split *= 2;
-  return launch_dependent(kernel, blocks * p.split, kWarps * 32, static_cast<size_t>(smem),
-                          p.split, stream, p);
+  // as many CTAs as the SMs hold
+  const int an_sm = std::min(4, kMaxSmem / smem);
+  const int clusters = p.split > 1 ? p.blocks : std::min(p.blocks, an_sm * sms);
+  return launch_dependent(kernel, clusters * p.split, kThreads, static_cast<size_t>(smem), p.split,
+                          stream, p);
 }
 
 }  // namespace
 
-// Rows of a CTA and steps in flight, us in a graph (weights not in L2): 32 rows
-// as long as the SMs have one CTA each, deeper then; with more rows than that
-// shallower slots, so that two CTAs fit an SM, or twice the rows.
+// Rows of a block and steps in flight by the tokens, and by whether blocks of 32
+// rows are at most one an SM (us in a graph, weights not in L2, hidden 7168 unless
+// said):
+//   INT4, one token, 16384 rows: 32 x 5 17.7, 64 x 4 16.4; 4096 rows 6.8, 7.6
+//   INT4, 16 tokens, 16384 rows: 32 x 4 23.7, 64 x 5 22.1; 4096 rows 7.8, 8.9
+//   INT4, 32 tokens, 4096 rows: 32 x 2 11.0, 64 x 3 12.0; 7168 x 2048 8.8, 7.5
+//   BF16, one token, 4096 rows: 32 x 5 10.7, 32 x 3 11.2; 7168 x 2048 7.3, 6.7
+//   BF16, 16 tokens, 4096 rows: 32 x 4 11.4, 32 x 2 12.9; 7168 x 2048 8.3, 7.2
+//   BF16, 32 tokens, 4096 rows: 32 x 3 12.6, 64 x 2 14.9; 7168 x 2048 9.5, 9.1
 template <bool kInt4, bool kGated>
 cudaError_t few(const ProductArgs& args, int sms, cudaStream_t stream) {
-  const bool one = args.n <= 32 * sms;  // 32-row CTAs: at most one an SM
+  const bool one = args.n <= 32 * sms;
   if constexpr (kInt4) {
-    if (args.tokens <= 8) {
-      if (args.n <= 64 * sms) return run<kInt4, kGated, 2, 1, 8, 5>(args, sms, stream);
-      return run<kInt4, kGated, 4, 1, 8, 4>(args, sms, stream);
-    }
-    if (args.tokens <= 16) return run<kInt4, kGated, 2, 2, 8, 4>(args, sms, stream);
-    return run<kInt4, kGated, 4, 4, 8, 3>(args, sms, stream);
+    const bool wide = args.n > 64 * sms;
+    if (args.tokens <= 8)
+      return wide ? run<kInt4, kGated, 4, 1, 4>(args, sms, stream)
+                  : run<kInt4, kGated, 2, 1, 5>(args, sms, stream);
+    if (args.tokens <= 16)
+      return wide ? run<kInt4, kGated, 4, 2, 5>(args, sms, stream)
+                  : run<kInt4, kGated, 2, 2, 4>(args, sms, stream);
+    return one ? run<kInt4, kGated, 2, 4, 2>(args, sms, stream)
+               : run<kInt4, kGated, 4, 4, 3>(args, sms, stream);
   } else {
     if (args.tokens <= 8)
-      return one ? run<kInt4, kGated, 2, 1, 8, 5>(args, sms, stream)
-                 : run<kInt4, kGated, 2, 1, 8, 3>(args, sms, stream);
+      return one ? run<kInt4, kGated, 2, 1, 5>(args, sms, stream)
+                 : run<kInt4, kGated, 2, 1, 3>(args, sms, stream);
     if (args.tokens <= 16)
-      return one ? run<kInt4, kGated, 2, 2, 8, 3>(args, sms, stream)
-                 : run<kInt4, kGated, 2, 2, 8, 2>(args, sms, stream);
-    return one ? run<kInt4, kGated, 2, 4, 8, 3>(args, sms, stream)
-               : run<kInt4, kGated, 4, 4, 8, 2>(args, sms, stream);
+      return one ? run<kInt4, kGated, 2, 2, 4>(args, sms, stream)
+                 : run<kInt4, kGated, 2, 2, 2>(args, sms, stream);
+    return one ? run<kInt4, kGated, 2, 4, 3>(args, sms, stream)
+               : run<kInt4, kGated, 4, 4, 2>(args, sms, stream);
   }
 }
 
