@@ -24,8 +24,14 @@ namespace {
 constexpr int kTileM = 128;      // tokens of a CTA
 constexpr int kSumWarps = 8;     // two a TMEM quarter, half of the columns each
 constexpr int kWarpCopy = kSumWarps, kWarpMma = kSumWarps + 1;
-constexpr int kDenseThreads = 32 * (kSumWarps + 2);
+constexpr int kDenseThreads = 32 * (kSumWarps + 4);  // whole warpgroups: two warps do nothing
 constexpr int kMaxSlots = 8;
+// The tensor core cuts its running sums off instead of rounding them: 1.5e-6 of an
+// FP32 output after the 128 additions that 2048 columns are. So for those an
+// accumulator's sums go after 512 columns to FP32 sums in registers: 3.4e-7 (a plain
+// FP32 product: 2.8e-7), for 169 instead of 146 us of 8192 x 2048 x 7168; after
+// 256 columns 1.7e-7 and 183 us.
+constexpr int kRun = 8;
 constexpr int kChunk = 32;       // output columns of an epilogue warp at a time
 constexpr int kTileBytes = 32 * kChunk * 4;  // of its 32 tokens
 constexpr int kTilesBytes = kSumWarps * 2 * kTileBytes;
@@ -49,6 +55,7 @@ struct DenseArgs {
   int out_cols;      // output columns of a tile
   int m_tiles, n_tiles, k_steps;
   int slots;
+  int run;           // steps of an accumulator before its sums are added in registers
   int split;         // CTAs of a cluster that share a tile's columns of x (split kernel)
 };
 
@@ -83,24 +90,25 @@ struct Ring {
   }
 };
 
-__device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
-  uint32_t w[16];
-  tmem_ld_32x32b_x16(at, w);
-  tmem_ld_wait_for(w);
+// The sums of a lane: kGroups groups of 16 columns, group g those from the
+// accumulator's column at(g) on, taken over (fresh) or added, kAtOnce groups in
+// flight. Groups from `used` on are left out (none where it is kGroups).
+constexpr int kGroups = 8;
+template <int kAtOnce, typename At>
+__device__ __forceinline__ void take_sums(float (&sum)[kGroups][16], bool fresh, int used, At at) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
-}
-
-__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
-  uint32_t lo[16], hi[16];
-  tmem_ld_32x32b_x16(at, lo);
-  tmem_ld_32x32b_x16(at + 16, hi);
-  tmem_ld_wait_for(lo);
-  tmem_ld_wait_for(hi);
+  for (int g = 0; g < kGroups; g += kAtOnce) {
+    if (g >= used) break;
+    uint32_t v[kAtOnce][16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i] = __uint_as_float(lo[i]);
-    v[16 + i] = __uint_as_float(hi[i]);
+    for (int i = 0; i < kAtOnce; ++i) tmem_ld_32x32b_x16(at(g + i), v[i]);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      tmem_ld_wait_for(v[i]);
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        sum[g + i][c] = __uint_as_float(v[i][c]) + (fresh ? 0.f : sum[g + i][c]);
+    }
   }
 }
 
@@ -126,6 +134,10 @@ __device__ __forceinline__ float4 load_addend(const DenseArgs& p, int token, int
     if (c + i < p.columns) f[i] = at[i];
   return make_float4(f[0], f[1], f[2], f[3]);
 }
+__device__ __forceinline__ uint2 bf16x4(float4 v) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
 __device__ __forceinline__ void store_out(const DenseArgs& p, int token, int c, float4 v) {
   if (token >= p.a.tokens || c >= p.columns) return;
   const long long at = static_cast<long long>(token) * p.columns + c;
@@ -142,9 +154,7 @@ __device__ __forceinline__ void store_out(const DenseArgs& p, int token, int c, 
   } else {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + at;
     if (p.columns % 4 == 0) {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
-      *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                  *reinterpret_cast<const uint32_t*>(&hi));
+      *reinterpret_cast<uint2*>(out) = bf16x4(v);
       return;
     }
 #pragma unroll
@@ -215,146 +225,181 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     *m = group * kGroup8 + rest - *n * height;
   };
 
-  if (warp == kWarpCopy) {
-    if (elect_one()) {
-      Ring r;
-      bool ok = true;
-      int issued = 0;
-      for (int tile = cluster; tile < tiles && ok; tile += clusters) {
-        int m, n;
-        place(tile, &m, &n);
-        const int m0 = first_token((2 * m + static_cast<int>(rank)) * kTileM, p.a.tokens);
-        const int w0 = p.a.gated ? n * p.half + static_cast<int>(rank) * p.columns
-                                 : (2 * n + static_cast<int>(rank)) * p.half;
-        for (int k = 0; k < p.k_steps; ++k) {
-          ok = dense_wait<true>(empty + 8 * r.slot, r.phase ^ 1u, failed);
-          if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(full + 8 * r.slot, 2 * slot_bytes);
-          const uint32_t bar = map_to_cta(full + 8 * r.slot, leader);
-          const uint32_t to = ring + r.slot * slot_bytes;
-          tma_load_2d_pair(to, &p.x, k * kKStep, m0, bar);
-          tma_load_2d_pair(to + a_bytes, &p.weight, k * kKStep, w0, bar);
-          ++issued;
-          r.next(p.slots);
-        }
-      }
-      if (!ok && rank == 0)  // copies in flight land before the CTAs end
-        for (int i = std::max(0, issued - p.slots); i < issued; ++i) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait_cluster_now(full + 8 * (i % p.slots), i / p.slots & 1) &&
-                 clock64() - t0 < kGiveUpCycles) {
-          }
-        }
-    }
-  } else if (warp == kWarpMma) {
-    if (rank == 0 && elect_one()) {
-      Ring r, acc;
-      const uint32_t idesc = idesc_bf16(2 * kTileM, static_cast<uint32_t>(2 * p.half));
-      bool ok = true;
-      for (int tile = cluster; tile < tiles && ok; tile += clusters) {
-        ok = dense_wait<true>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem + 256 * acc.slot;
-        for (int k = 0; k < p.k_steps; ++k) {
-          ok = dense_wait<true>(full + 8 * r.slot, r.phase, failed);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t from = ring + r.slot * slot_bytes;
-          const uint64_t ad = smem_desc_sw128_kmajor(from);
-          const uint64_t bd = smem_desc_sw128_kmajor(from + a_bytes);
-#pragma unroll
-          for (int j = 0; j < kKStep / 16; ++j)  // 32 bytes further along k
-            mma_bf16_ss_pair(d, ad + 2 * j, bd + 2 * j, idesc, k > 0 || j > 0);
-          tc_commit_pair_mc(empty + 8 * r.slot, 3u);
-          r.next(p.slots);
-        }
-        if (ok) tc_commit_pair_mc(summed + 8 * acc.slot, 3u);
-        acc.next(2);
-      }
-    }
-  } else {
-    // lane + 32 (warp % 4) = token of the CTA, half of the columns
-    // in two tiles of 32 x 32 by turns, into which the addend is copied two
-    // chunks ahead (a load that is waited for takes its turn behind the operands'
-    // copies: 4000 cycles)
+  // 384 threads have 168 registers each: the sums' 256 threads take 208, the others
+  // keep 88 (256 * 208 + 128 * 88 = 384 * 168)
+  if (warp < kSumWarps) {
+    registers_up<208>();
+    // lane + 32 (warp % 4) = token of the CTA, half of the output's columns: its sums
+    // in registers, then 32 columns at a time through two tiles of 32 x 32 by
+    // turns, into which the addend is copied two ahead (a load that is waited for
+    // takes its turn behind the operands' copies: 4000 cycles)
     float* tiles_at = reinterpret_cast<float*>(smem + kRingBytes) + warp * (2 * 32 * kChunk);
-    const int quarter = warp % 4, side = warp / 4;
-    const int chunks = (p.out_cols + kChunk - 1) / kChunk;
-    const int first = side == 0 ? 0 : (chunks + 1) / 2, last = side == 0 ? (chunks + 1) / 2 : chunks;
+    const int quarter = warp % 4, cols = p.out_cols / 2, side = warp / 4 * cols;
     const int row = lane >> 3, quad = lane & 7;  // of a store: four rows at a time
     const bool ahead = p.a.addend != nullptr && p.columns % 4 == 0;
+    const int runs = (p.k_steps + p.run - 1) / p.run;
     Ring acc;
     for (int tile = cluster; tile < tiles; tile += clusters) {
       int m, n;
       place(tile, &m, &n);
       const int m0 = (2 * m + static_cast<int>(rank)) * kTileM;  // its own tokens from here on
       const int t0 = first_token(m0, p.a.tokens) + quarter * 32 + row;
-      const int c0 = n * p.out_cols + quad * 4;
-      const auto fetch = [&](int c) {
-        if (ahead && c < last) {
-          const uint32_t to = smem_u32(tiles_at + (c - first & 1) * (32 * kChunk));
-          const int column = c0 + c * kChunk;
+      const int c0 = n * p.out_cols + side + quad * 4;
+      // the rows of a store, four further on each, that are this CTA's own
+      const long long at0 = static_cast<long long>(t0) * p.columns + c0, four = 4LL * p.columns;
+      uint32_t own = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int token = t0 + 4 * i;
-            const bool in = token >= m0 && token < p.a.tokens && column < p.columns;
-            copy16_of(to + tile_at(4 * i + row, quad) * 4,
-                      p.a.addend + (in ? static_cast<long long>(token) * p.columns + column : 0),
-                      in ? 16 : 0);
-          }
+      for (int i = 0; i < 8; ++i)
+        own |= static_cast<uint32_t>(t0 + 4 * i >= m0 && t0 + 4 * i < p.a.tokens) << i;
+      const auto fetch = [&](int c) {
+        if (ahead && c * kChunk < cols) {
+          const uint32_t to = smem_u32(tiles_at + (c & 1) * (32 * kChunk));
+          const bool in = c0 + c * kChunk < p.columns;
+          const float* from = p.a.addend + at0 + c * kChunk;
+#pragma unroll
+          for (int i = 0; i < 8; ++i, from += four)
+            copy16_of(to + tile_at(4 * i + row, quad) * 4, from, in && (own >> i & 1u) ? 16 : 0);
         }
         copies_commit();
       };
-      fetch(first);
-      fetch(first + 1);
-      const bool ok = __all_sync(0xffffffffu, dense_wait<true>(summed + 8 * acc.slot, acc.phase, failed));
-      tc_fence_after();
-      const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 * acc.slot;
-#pragma unroll 1
-      for (int c = first; c < last; ++c) {
-        float* here = tiles_at + (c - first & 1) * (32 * kChunk);
-        float v[32];
-        tmem_load32(at + c * kChunk, v);
-        if (p.a.gated) {
-          float up[32];
-          tmem_load32(at + p.half + c * kChunk, up);
+      fetch(0);
+      fetch(1);
+      float sum[kGroups][16];
+      bool ok = true;
+      for (int run = 0; run < runs; ++run) {
+        ok = __all_sync(0xffffffffu, dense_wait<true>(summed + 8 * acc.slot, acc.phase, failed)) && ok;
+        tc_fence_after();
+        const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 * acc.slot + side;
+        // gated: gates in the first groups, ups in the last. (Columns that a narrow
+        // tile does not have are read as well, and not used.)
+        const uint32_t up = p.a.gated ? static_cast<uint32_t>(p.half) : kGroups / 2 * 16;
+        take_sums<1>(sum, run == 0, kGroups, [&](int g) {
+          return at + g / (kGroups / 2) * up + g % (kGroups / 2) * 16;
+        });
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * acc.slot, leader));
+        acc.next(2);
+      }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = silu_times(v[i], up[i]);
-        }
-        if (c == last - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * acc.slot, leader));
-        }
+      for (int c = 0; c < kGroups / 2; ++c) {
+        if (c * kChunk >= cols) break;
+        float* here = tiles_at + (c & 1) * (32 * kChunk);
         copies_wait<1>();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          float v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int g = 2 * c + i / 4, at = i % 4 * 4 + j;
+            v[j] = sum[g][at];
+            if (c < kGroups / 4 && p.a.gated)
+              v[j] = silu_times(v[j], sum[(g + kGroups / 2) % kGroups][at]);
+          }
           float4* at4 = reinterpret_cast<float4*>(here + tile_at(lane, i));
-          float4 sum = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          if (ahead) sum = add4(sum, *at4);
+          float4 out = make_float4(v[0], v[1], v[2], v[3]);
+          if (ahead) out = add4(out, *at4);
           const float nan = __uint_as_float(0x7FC00000u);
-          *at4 = ok ? sum : make_float4(nan, nan, nan, nan);
+          *at4 = ok ? out : make_float4(nan, nan, nan, nan);
         }
         __syncwarp();
-        const bool in = c * kChunk + quad * 4 < p.out_cols;  // (else the next tile's)
+        const int column = c0 + c * kChunk;
+        const bool in = c * kChunk + quad * 4 < cols && column < p.columns;
+        const uint32_t rows = in ? own : 0u;
+        const auto value = [&](int i) {
+          return *reinterpret_cast<const float4*>(here + tile_at(4 * i + row, quad));
+        };
+        if (p.columns % 4 != 0) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i)
+            if (rows >> i & 1u)
+              store_out(p, t0 + 4 * i, column, add4(value(i), load_addend(p, t0 + 4 * i, column)));
+        } else if (p.a.f32_out) {
+          float* to = static_cast<float*>(p.a.out) + at0 + c * kChunk;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float4 sum = *reinterpret_cast<const float4*>(here + tile_at(4 * i + row, quad));
-          const int token = t0 + 4 * i, column = c0 + c * kChunk;
-          if (token < m0 || !in) continue;
-          if (!ahead) sum = add4(sum, load_addend(p, token, column));
-          store_out(p, token, column, sum);
+          for (int i = 0; i < 8; ++i, to += four)
+            if (rows >> i & 1u) *reinterpret_cast<float4*>(to) = value(i);
+        } else {
+          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.a.out) + at0 + c * kChunk;
+#pragma unroll
+          for (int i = 0; i < 8; ++i, to += four)
+            if (rows >> i & 1u) *reinterpret_cast<uint2*>(to) = bf16x4(value(i));
         }
         __syncwarp();
         fetch(c + 2);
       }
-      if (first == last) {  // no columns for this side
-        tc_fence_before();
-        if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * acc.slot, leader));
+    }
+  } else {
+    registers_down<88>();
+    if (warp == kWarpCopy) {
+      if (elect_one()) {
+        Ring r;
+        bool ok = true;
+        int issued = 0;
+        for (int tile = cluster; tile < tiles && ok; tile += clusters) {
+          int m, n;
+          place(tile, &m, &n);
+          const int m0 = first_token((2 * m + static_cast<int>(rank)) * kTileM, p.a.tokens);
+          const int w0 = p.a.gated ? n * p.half + static_cast<int>(rank) * p.columns
+                                   : (2 * n + static_cast<int>(rank)) * p.half;
+          for (int k = 0; k < p.k_steps; ++k) {
+            ok = dense_wait<true>(empty + 8 * r.slot, r.phase ^ 1u, failed);
+            if (!ok) break;
+            if (rank == 0) mbar_arrive_expect_tx(full + 8 * r.slot, 2 * slot_bytes);
+            const uint32_t bar = map_to_cta(full + 8 * r.slot, leader);
+            const uint32_t to = ring + r.slot * slot_bytes;
+            tma_load_2d_pair(to, &p.x, k * kKStep, m0, bar);
+            tma_load_2d_pair(to + a_bytes, &p.weight, k * kKStep, w0, bar);
+            ++issued;
+            r.next(p.slots);
+          }
+        }
+        if (!ok && rank == 0)  // copies in flight land before the CTAs end
+          for (int i = std::max(0, issued - p.slots); i < issued; ++i) {
+            const long long t0 = clock64();
+            while (!mbar_try_wait_cluster_now(full + 8 * (i % p.slots), i / p.slots & 1) &&
+                   clock64() - t0 < kGiveUpCycles) {
+            }
+          }
       }
-      acc.next(2);
+    } else if (warp == kWarpMma) {
+      if (rank == 0 && elect_one()) {
+        Ring r, acc;
+        const uint32_t idesc = idesc_bf16(2 * kTileM, static_cast<uint32_t>(2 * p.half));
+        bool ok = true;
+        for (int tile = cluster; tile < tiles && ok; tile += clusters) {
+          uint32_t d = 0;
+          int left = 0;  // steps of this accumulator (a counter: a remainder takes 100 cycles of a step)
+          for (int k = 0; k < p.k_steps; ++k) {
+            const bool fresh = left == 0;
+            if (fresh) {
+              if (k > 0) {
+                tc_commit_pair_mc(summed + 8 * acc.slot, 3u);
+                acc.next(2);
+              }
+              ok = dense_wait<true>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
+              if (!ok) break;
+              d = tmem + 256 * acc.slot;
+              left = p.run;
+            }
+            --left;
+            ok = dense_wait<true>(full + 8 * r.slot, r.phase, failed);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t from = ring + r.slot * slot_bytes;
+            const uint64_t ad = smem_desc_sw128_kmajor(from);
+            const uint64_t bd = smem_desc_sw128_kmajor(from + a_bytes);
+#pragma unroll
+            for (int j = 0; j < kKStep / 16; ++j)  // 32 bytes further along k
+              mma_bf16_ss_pair(d, ad + 2 * j, bd + 2 * j, idesc, !fresh || j > 0);
+            tc_commit_pair_mc(empty + 8 * r.slot, 3u);
+            r.next(p.slots);
+          }
+          if (ok) tc_commit_pair_mc(summed + 8 * acc.slot, 3u);
+          acc.next(2);
+        }
+      }
     }
   }
   tc_fence_before();
@@ -374,13 +419,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bars[2 * kMaxSlots + 1];
+  __shared__ uint64_t bars[2 * kMaxSlots + 4];
   __shared__ uint32_t tmem_at;
   __shared__ int failed_word;
   volatile int* failed = &failed_word;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots, summed = full + 16 * kMaxSlots;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots, summed = full + 16 * kMaxSlots, drained = summed + 16;
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
   const uint32_t slot_bytes = a_bytes + 2 * b_bytes;
@@ -389,14 +434,17 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const int m = tile % p.m_tiles, n = tile / p.m_tiles;
   const int m0 = first_token(m * kTileM, p.a.tokens), skip = m * kTileM - m0;
   const int k0 = p.k_steps * rank / p.split, k1 = p.k_steps * (rank + 1) / p.split;
-  const uint32_t tmem_cols = p.half <= 16 ? 32 : p.half <= 32 ? 64 : p.half <= 64 ? 128 : 256;
+  const uint32_t acc_cols = p.half <= 32 ? 64 : p.half <= 64 ? 128 : 256, tmem_cols = 2 * acc_cols;
   if (warp == kWarpMma) {
     if (lane == 0) {
       for (int i = 0; i < p.slots; ++i) {
         mbar_init(full + 8 * i, 1);
         mbar_init(empty + 8 * i, 1);
       }
-      mbar_init(summed, 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(summed + 8 * i, 1);
+        mbar_init(drained + 8 * i, kSumWarps);
+      }
       *failed = 0;
       fence_mbar_init();
     }
@@ -437,9 +485,21 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     }
   } else if (warp == kWarpMma) {
     if (elect_one()) {
-      Ring r;
+      Ring r, acc;
       const uint32_t idesc = idesc_bf16(kTileM, static_cast<uint32_t>(2 * p.half));
+      int left = 0;  // steps of this accumulator
       for (int k = k0; k < k1; ++k) {
+        const bool fresh = left == 0;
+        if (fresh) {
+          if (k > k0) {
+            tc_commit(summed + 8 * acc.slot);
+            acc.next(2);
+          }
+          ok = dense_wait<false>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
+          if (!ok) break;
+          left = p.run;
+        }
+        --left;
         ok = dense_wait<false>(full + 8 * r.slot, r.phase, failed);
         if (!ok) break;
         tc_fence_after();
@@ -448,30 +508,42 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const uint64_t bd = smem_desc_sw128_kmajor(from + a_bytes);
 #pragma unroll
         for (int j = 0; j < kKStep / 16; ++j)
-          mma_bf16_ss(tmem, ad + 2 * j, bd + 2 * j, idesc, k > k0 || j > 0);
+          mma_bf16_ss(tmem + acc.slot * acc_cols, ad + 2 * j, bd + 2 * j, idesc, !fresh || j > 0);
         tc_commit(empty + 8 * r.slot);
         r.next(p.slots);
       }
-      if (ok) tc_commit(summed);
+      if (ok) tc_commit(summed + 8 * acc.slot);
     }
   } else if (warp < kSumWarps) {
-    ok = __all_sync(0xffffffffu, dense_wait<false>(summed, 0, failed));
-    tc_fence_after();
-    // (nothing reads the ring any more: all of its copies were multiplied)
-    const int quarter = warp % 4, side = warp / 4, pitch = 2 * p.half + 4;
-    float* row = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * pitch;
-    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const bool live = m0 + quarter * 32 < p.a.tokens;  // (whole warps)
-    for (int c = side * 16; live && c < 2 * p.half; c += 32) {
-      float v[16];
-      tmem_load16(at + c, v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(row + c + 4 * i) =
-            ok ? make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3])
-               : make_float4(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u),
-                             __uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
+    // lane + 32 (warp % 4) = token of the tile, half of the weight rows
+    const int quarter = warp % 4, side = warp / 4 * p.half, pitch = 2 * p.half + 4;
+    const int runs = (k1 - k0 + p.run - 1) / p.run;
+    float sum[kGroups][16];
+    Ring acc;
+    for (int run = 0; run < runs; ++run) {
+      ok = __all_sync(0xffffffffu, dense_wait<false>(summed + 8 * acc.slot, acc.phase, failed)) && ok;
+      tc_fence_after();
+      const uint32_t at =
+          tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc.slot * acc_cols + side;
+      take_sums<1>(sum, run == 0, p.half / 16, [&](int g) { return at + g * 16; });
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(drained + 8 * acc.slot);
+      acc.next(2);
     }
+    // (nothing reads the ring any more: all of its copies were multiplied)
+    float* row = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * pitch + side;
+    if (m0 + quarter * 32 < p.a.tokens)  // (whole warps)
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+        if (g * 16 < p.half)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float nan = __uint_as_float(0x7FC00000u);
+            *reinterpret_cast<float4*>(row + g * 16 + i) =
+                ok ? make_float4(sum[g][i], sum[g][i + 1], sum[g][i + 2], sum[g][i + 3])
+                   : make_float4(nan, nan, nan, nan);
+          }
   }
   tc_fence_before();
   __syncwarp();
@@ -556,6 +628,7 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
     c.out_cols = a.gated ? c.half : tile_n;
     c.n_tiles = ceil_div(columns, c.out_cols);
     c.k_steps = steps;
+    c.run = a.f32_out ? kRun : steps;
     const double gate = a.gated ? tile_n * 0.01 : 0;
 
     c.m_tiles = ceil_div(a.tokens, 2 * kTileM);

@@ -225,6 +225,17 @@ __device__ __forceinline__ void grid_dependents_go() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Registers of each thread of a warpgroup (all of its warps take part), out of
+// those that the block was launched with: the shares' sum must not exceed them.
+template <int kRegisters>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegisters));
+}
+template <int kRegisters>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegisters));
+}
+
 // True in one lane of the (whole, converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t mine;
