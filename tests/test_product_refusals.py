@@ -113,6 +113,8 @@ class Placed:
     def dim(self):
         return len(self.shape)
 
+    is_cuda = True
+
     def is_contiguous(self):
         return True
 

@@ -362,9 +362,11 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
   p.steps = ceil_div(args.k, kKStep);
   p.slot_bytes = step_bytes(kInt4, kRows) + args.tokens * 128;
   const int smem = kWarps * kDepth * p.slot_bytes + kWarps / 2 * 8 * kNt * (kRows + 4) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 << 10) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
   // a cluster of two, four or eight where all CTAs still find an SM and every
   // warp a step. (Eights that want an SM each do not all find a place at once: 512
   // rows of 7168 in BF16 7.6 us, in fours 4.5.)

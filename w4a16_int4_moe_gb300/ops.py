@@ -606,33 +606,42 @@ def _place_rows(fn: str, what: str, t: torch.Tensor, dtype, shape, device: int):
                 f"{dtype} {tuple(shape)} on GPU {device}")
 
 
-def _device_of(fn: str, what: str, t: torch.Tensor) -> int:
-    """The GPU that t, a matrix, is on."""
-    device = t.get_device()
-    if device < 0 or t.dim() != 2:
-        _refuse(fn, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}")
-    return device
-
-
-def _product(fn: str, call, x, device: int, n: int, k: int, gated: bool, addend, out, out_dtype,
-             stream, weight_at, last):
-    """What both products share: x's rows, addend, output and the call. last: the
-    weight's arguments behind its address."""
-    shape = (x.shape[0], n // 2 if gated else n)
-    x_at, x_stride = _place_rows(fn, "x", x, _BF16, (shape[0], k), device)
+def _product(fn: str, call, x, device: int, tokens: int, k: int, columns: int, addend, out,
+             out_dtype, stream, weight_at, *last):
+    """What both products share: the rows of x [tokens, k], addend and output
+    [tokens, columns], and the call. last: the weight's arguments behind its address."""
+    if x.dtype is not _BF16:
+        _refuse(fn, f"x: {x.dtype}")
+    x_stride = k
+    if not x.is_contiguous():
+        x_stride, step = x.stride()
+        if step != 1 and k > 1:
+            _refuse(fn, f"x: strides {x.stride()}")
+        if tokens <= 1:
+            x_stride = max(x_stride, k)
+    shape = (tokens, columns)
     if out is None:
         with on_stream(stream):
             out = torch.empty(shape, dtype=out_dtype, device=x.device)
     dtype = out.dtype
     if dtype is not _F32 and dtype is not _BF16:
         _refuse(fn, f"out: {dtype}")
-    _check(fn, call(
-        weight_at, *last, x_at, x_stride, shape[0],
+    status = call(
+        weight_at, *last, x.data_ptr(), x_stride, tokens,
         None if addend is None else _place(fn, "addend", addend, _F32, shape, device),
         _place(fn, "out", out, dtype, shape, device),
         W4A16_DTYPE_F32 if dtype is _F32 else W4A16_DTYPE_BF16,
-        _current_stream(device) if stream is None else stream.cuda_stream))
+        _current_stream(device) if stream is None else stream.cuda_stream)
+    if status != W4A16_OK:
+        _check(fn, status)
     return out
+
+
+def _elsewhere(fn: str, x: torch.Tensor):
+    """x is not on the current device: the context in which its GPU is."""
+    if not x.is_cuda:
+        _refuse(fn, f"x: {x.dtype} {tuple(x.shape)} on {x.device}")
+    return torch.cuda.device(x.get_device())
 
 
 def w4a16_linear_few_tokens(x: torch.Tensor, packed: torch.Tensor, n: int,
@@ -645,18 +654,20 @@ def w4a16_linear_few_tokens(x: torch.Tensor, packed: torch.Tensor, n: int,
     x BF16 [T, k], rows may be strided. out (or out_dtype): FP32 or BF16; out may
     be addend."""
     fn = "w4a16_linear_few_tokens"
-    device = _device_of(fn, "x", x)
-    if device != _current_device():
-        with torch.cuda.device(device):
+    device = x.get_device()
+    if device < 0 or device != _current_device():
+        with _elsewhere(fn, x):
             return w4a16_linear_few_tokens(x, packed, n, layout, addend, out_dtype, out, stream)
-    k = x.shape[1]
+    if x.dim() != 2:
+        _refuse(fn, f"x {tuple(x.shape)}")
+    tokens, k = x.shape
     # 128-row tiles of 64-column steps, 4608 bytes each
     at = _blob(fn, "packed", packed, -(-n // 128) * -(-k // 64) * 4608)
     if packed.get_device() != device:
         _refuse(fn, f"x on {x.device}, packed on {packed.device}")
-    return _product(fn, load_library().w4a16_linear_few_tokens, x, device, n, k,
-                    layout == W4A16_LAYOUT_KTILE64_GLU16, addend, out, out_dtype, stream, at,
-                    (layout, n, k))
+    return _product(fn, load_library().w4a16_linear_few_tokens, x, device, tokens, k,
+                    n // 2 if layout == W4A16_LAYOUT_KTILE64_GLU16 else n, addend, out, out_dtype,
+                    stream, at, layout, n, k)
 
 
 def w4a16_dense(x: torch.Tensor, weight: torch.Tensor, gated: bool = False,
@@ -667,16 +678,20 @@ def w4a16_dense(x: torch.Tensor, weight: torch.Tensor, gated: bool = False,
     silu(x . Wgate^T) * (x . Wup^T), [T, n/2]. x BF16 [T, k], rows may be
     strided. out (or out_dtype): FP32 or BF16; out may be addend."""
     fn = "w4a16_dense"
-    device = _device_of(fn, "x", x)
-    if device != _current_device():
-        with torch.cuda.device(device):
+    device = x.get_device()
+    if device < 0 or device != _current_device():
+        with _elsewhere(fn, x):
             return w4a16_dense(x, weight, gated, addend, out_dtype, out, stream)
-    if weight.dim() != 2:
-        _refuse(fn, f"weight {tuple(weight.shape)}")
-    n, k = size = weight.shape
-    return _product(fn, load_library().w4a16_dense, x, device, n, k, gated, addend, out, out_dtype,
-                    stream, _place(fn, "weight", weight, _BF16, size, device),
-                    (n, k, 1 if gated else 0))
+    size = weight.shape
+    if x.dim() != 2 or len(size) != 2:
+        _refuse(fn, f"x {tuple(x.shape)}, weight {tuple(size)}")
+    tokens, columns = x.shape
+    n, k = size
+    if columns != k:
+        _refuse(fn, f"x {tuple(x.shape)}, weight {tuple(size)}")
+    return _product(fn, load_library().w4a16_dense, x, device, tokens, k, n // 2 if gated else n,
+                    addend, out, out_dtype, stream,
+                    _place(fn, "weight", weight, _BF16, size, device), n, k, 1 if gated else 0)
 
 
 def w4a16_block_norm(x: torch.Tensor, pre_weight: Optional[torch.Tensor], eps: float = 1e-6,
@@ -696,12 +711,14 @@ def w4a16_block_norm(x: torch.Tensor, pre_weight: Optional[torch.Tensor], eps: f
     may be the residual itself). x FP32 or BF16 [T, H], residual BF16 [T, H], gate
     BF16 [T, H] or [H]; rows may be strided."""
     fn = "w4a16_block_norm"
-    device = _device_of(fn, "x", x)
-    if device != _current_device():
-        with torch.cuda.device(device):
+    device = x.get_device()
+    if device < 0 or device != _current_device():
+        with _elsewhere(fn, x):
             return w4a16_block_norm(x, pre_weight, eps, post_weight, gate, residual, branch_scale,
                                     residual_scale, weight_offset, fp8_group, bf16_out, out,
                                     stream)
+    if x.dim() != 2:
+        _refuse(fn, f"x {tuple(x.shape)}")
     rows, hidden = shape = x.shape
     f32 = x.dtype is _F32
     x_at, x_stride = _place_rows(fn, "x", x, _F32 if f32 else _BF16, shape, device)
@@ -731,14 +748,16 @@ def w4a16_block_norm(x: torch.Tensor, pre_weight: Optional[torch.Tensor], eps: f
             out = tuple(torch.empty(size, dtype=dtype, device=x.device) if wanted else None
                         for size, dtype, wanted in kinds)
     y, h, y8, scales = out
-    _check(fn, load_library().w4a16_block_norm(
+    status = load_library().w4a16_block_norm(
         x_at, W4A16_DTYPE_F32 if f32 else W4A16_DTYPE_BF16, x_stride, post_at, g_at, g_stride,
         r_at, r_stride, pre_at, weight_offset, branch_scale, residual_scale, eps, rows, hidden,
         None if y is None else _place(fn, "out", y, _BF16, shape, device),
         None if h is None else _place(fn, "h_out", h, _BF16, shape, device),
         None if y8 is None else _place(fn, "out_fp8", y8, _E4M3, shape, device),
         None if scales is None else _place(fn, "scales", scales, _F32, (rows, groups), device),
-        fp8_group, _current_stream(device) if stream is None else stream.cuda_stream))
+        fp8_group, _current_stream(device) if stream is None else stream.cuda_stream)
+    if status != W4A16_OK:
+        _check(fn, status)
     return out
 
 
