@@ -643,6 +643,7 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
     c.slots = std::min(kMaxSlots, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
     const double rows = std::min(a.tokens, kTileM);
     for (c.split = 1; c.split <= kMaxSplit && c.split <= steps; c.split *= 2) {
+      if (static_cast<long long>(c.m_tiles) * c.n_tiles * c.split > 0x7fffffffLL) break;
       const double waves = std::ceil(static_cast<double>(c.m_tiles) * c.n_tiles /
                                      split_clusters_at_once(c.split, sms, device, error));
       const double sums = rows / kTileM * (1 + tile_n * 0.012 + gate) / (c.split > 1 ? 1.5 : 1);
@@ -677,7 +678,6 @@ cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) 
     return launch_dependent(w4a16_dense_pair_kernel, 2 * clusters, kDenseThreads, kSmemBytes, 2,
                             stream, p);
   }
-  if (tiles * p.split > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int smem = 1024 + std::max(p.slots * (kTileM + 2 * p.half) * kKStep * 2,
                                    kTileM * (2 * p.half + 4) * 4);
   return launch_dependent(w4a16_dense_split_kernel, static_cast<int>(tiles) * p.split, kDenseThreads,
