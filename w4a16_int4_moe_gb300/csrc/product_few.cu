@@ -12,7 +12,7 @@
 // applied to its FP32 sum, so no weight is rounded.
 //
 // One token, in a graph: BF16, 4096 x 7168 gated 10.7 us, 5.5 TB/s (0.81 of the
-// copy rate); INT4, the same 6.8 us for 16.5 MB, 7168 x 2048 4.4 us, where launch,
+// copy rate); INT4, the same 6.3 us for 16.5 MB, 7168 x 2048 4.4 us, where launch,
 // first load and sums are some 3 us; 16384 x 7168 16.4 us, 4.0 TB/s: the ALU pipe
 // (a shift and an AND-OR for two codes, at half rate) is busy two thirds of the
 // time, and 256 blocks on 152 SMs leave a sixth of it out. 32 tokens of 16384 x
@@ -31,8 +31,6 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxSmem = 232448;
 
 // d = a . b + c, BF16 operands
@@ -112,8 +110,9 @@ constexpr int step_bytes(bool int4, int rows) { return rows * (int4 ? 36 : 128);
 // copies its steps (the weights, and the tokens' columns) into slots of its own,
 // kDepth ahead and on into the next block. The sums of the warps meet in shared
 // memory, those of the CTAs through the cluster's.
-template <bool kInt4, bool kGated, int kMt, int kNt, int kDepth>
-__global__ void __launch_bounds__(kThreads) w4a16_product_few_kernel(const FewProduct p) {
+template <bool kInt4, bool kGated, int kMt, int kNt, int kDepth, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const FewProduct p) {
+  constexpr int kThreads = kWarps * 32;
   constexpr int kRows = 16 * kMt;
   constexpr int kTokens = 8 * kNt;
   constexpr int kPitch = kRows + 4;  // of a token's sums
@@ -351,10 +350,10 @@ __global__ void __launch_bounds__(kThreads) w4a16_product_few_kernel(const FewPr
 
 namespace {
 
-template <bool kInt4, bool kGated, int kMt, int kNt, int kDepth>
+template <bool kInt4, bool kGated, int kMt, int kNt, int kDepth, int kWarps = 8>
 cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
   constexpr int kRows = 16 * kMt;
-  const auto kernel = w4a16_product_few_kernel<kInt4, kGated, kMt, kNt, kDepth>;
+  const auto kernel = w4a16_product_few_kernel<kInt4, kGated, kMt, kNt, kDepth, kWarps>;
   FewProduct p;
   p.a = args;
   p.sixteens = 0x41804180u;
@@ -377,7 +376,7 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
   // as many CTAs as the SMs hold
   const int an_sm = std::min(4, kMaxSmem / smem);
   const int clusters = p.split > 1 ? p.blocks : std::min(p.blocks, an_sm * sms);
-  return launch_dependent(kernel, clusters * p.split, kThreads, static_cast<size_t>(smem), p.split,
+  return launch_dependent(kernel, clusters * p.split, kWarps * 32, static_cast<size_t>(smem), p.split,
                           stream, p);
 }
 
@@ -386,7 +385,8 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
 // Rows of a block and steps in flight by the tokens, and by whether blocks of 32
 // rows are at most one an SM (us in a graph, weights not in L2, hidden 7168 unless
 // said):
-//   INT4, one token, 16384 rows: 32 x 5 17.7, 64 x 4 16.4; 4096 rows 6.8, 7.6
+//   INT4, one token, 16384 rows: 32 x 5 17.7, 64 x 4 16.4; 4096 rows 6.8, 7.6, and
+//     with 16 warps for eight 32 x 3 6.3 (7168 x 2048: 4.4 with eight, 4.5)
 //   INT4, 16 tokens, 16384 rows: 32 x 4 23.7, 64 x 5 22.1; 4096 rows 7.8, 8.9
 //   INT4, 32 tokens, 4096 rows: 32 x 2 11.0, 64 x 3 12.0; 7168 x 2048 8.8, 7.5
 //   BF16, one token, 4096 rows: 32 x 5 10.7, 32 x 3 11.2; 7168 x 2048 7.3, 6.7
@@ -397,6 +397,8 @@ cudaError_t few(const ProductArgs& args, int sms, cudaStream_t stream) {
   const bool one = args.n <= 32 * sms;
   if constexpr (kInt4) {
     const bool wide = args.n > 64 * sms;
+    if (args.tokens <= 8 && one && args.n > 16 * sms)  // (no cluster either)
+      return run<kInt4, kGated, 2, 1, 3, 16>(args, sms, stream);
     if (args.tokens <= 8)
       return wide ? run<kInt4, kGated, 4, 1, 4>(args, sms, stream)
                   : run<kInt4, kGated, 2, 1, 5>(args, sms, stream);
