@@ -559,8 +559,9 @@ w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed
  * group's FP32 sum, sums are FP32, and the result is rounded once.
  *   packed  w4a16_prepack's blob of one expert, [1, n, k] in `layout`;
  *   x       BF16 [tokens, k], row stride x_stride elements;
- *   addend  FP32 [tokens, n] or NULL (it may be out itself; gated: NULL);
- *   out     out_dtype (W4A16_DTYPE_F32 or W4A16_DTYPE_BF16), rows contiguous.
+ *   addend  FP32 [tokens, n] or NULL (gated: NULL);
+ *   out     out_dtype (W4A16_DTYPE_F32 or W4A16_DTYPE_BF16), rows contiguous; it
+ *           overlaps no input but addend, which it may be.
  * tokens at most W4A16_FEW_TOKENS_MAX, k a multiple of 32, n at least 1 (GLU16: a
  * multiple of 128), both at most 2^20 (else W4A16_ERR_UNSUPPORTED); x_stride a
  * multiple of 8 and at least k, pointers 16-byte aligned (else
@@ -580,9 +581,9 @@ w4a16_status w4a16_linear_few_tokens(const void* packed, int layout, int n, int 
  * FP32 sums, one rounding of the result.
  *   weight  BF16 [n, k]; gated: n/2 gate rows, then n/2 up rows;
  *   x       BF16 [tokens, k], row stride x_stride elements;
- *   addend  FP32 [tokens, n] or NULL (it may be out itself; gated: NULL);
+ *   addend  FP32 [tokens, n] or NULL (gated: NULL);
  *   out     out_dtype (W4A16_DTYPE_F32 or W4A16_DTYPE_BF16) [tokens, n], gated
- *           [tokens, n/2].
+ *           [tokens, n/2]; it overlaps no input but addend, which it may be.
  * k a multiple of 8, n at least 1 (gated: even), both at most 2^20, tokens at
  * most 2^24 (else W4A16_ERR_UNSUPPORTED); x_stride a multiple of 8, at least k and below 2^31,
  * pointers 16-byte aligned (else W4A16_ERR_INVALID_ARG). The order of the

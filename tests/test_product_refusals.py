@@ -24,7 +24,8 @@ def test_linear_few_tokens_refusals(lib):
     for bad in (dict(n=0), dict(n=-1), dict(k=0), dict(t=-1), dict(layout=2), dict(layout=-1),
                 dict(w=None), dict(x=None), dict(out=None), dict(dt=FP8), dict(dt=7),
                 dict(xs=248), dict(xs=260), dict(xs=1 << 31), dict(w=P + 8), dict(x=P + 2),
-                dict(out=P + 4), dict(add=P + 4), dict(layout=GLU), dict(add=P, out=P, dt=BF16)):
+                dict(out=P + 4), dict(add=P + 4), dict(layout=GLU), dict(add=P, out=P, dt=BF16),
+                dict(out=P), dict(w=2 * P, out=P), dict(x=2 * P, out=P)):
         assert call(**bad) == INV, bad
     for bad in (dict(k=240), dict(k=8), dict(t=33), dict(n=(1 << 20) + 1),
                 dict(k=(1 << 20) + 32, xs=1 << 21), dict(layout=GLU, n=192, add=None)):
@@ -43,7 +44,7 @@ def test_dense_refusals(lib):
     for bad in (dict(n=0), dict(k=0), dict(k=-8), dict(t=-1), dict(w=None), dict(x=None),
                 dict(out=None), dict(dt=FP8), dict(xs=248), dict(xs=257), dict(xs=1 << 31),
                 dict(w=P + 2), dict(x=P + 8), dict(out=P + 8), dict(add=P + 4), dict(gated=1),
-                dict(add=P, out=P, dt=BF16)):
+                dict(add=P, out=P, dt=BF16), dict(w=2 * P, out=P), dict(x=2 * P, out=P)):
         assert call(**bad) == INV, bad
     for bad in (dict(k=252), dict(n=(1 << 20) + 1), dict(k=(1 << 20) + 8, xs=1 << 21),
                 dict(t=(1 << 24) + 1), dict(gated=1, n=255, add=None)):
@@ -176,6 +177,9 @@ def test_shared_experts_that_do_not_fit_are_refused(lib):
     expert = moe.PackedSharedExpert(glu, packed, 8)
     with pytest.raises(ValueError):
         expert.forward(torch.zeros(9, 96, dtype=bf))
+    for e in (expert, moe.SharedExpert(gu, dn)):   # nothing to add to
+        with pytest.raises(ValueError):
+            e.forward(torch.zeros(1, 96, dtype=bf), add=True)
     for bad in ((moe.PackedExperts(blob, 1, 128, 96), packed), (glu, moe.PackedExperts(blob, 1, 96, 96)),
                 (moe.PackedExperts(blob, 2, 128, 96, GLU), packed),
                 (glu, moe.PackedExperts(blob, 2, 96, 64))):

@@ -937,6 +937,7 @@ static w4a16_status check_product(const ProductArgs& a, int out_dtype) {
   if (a.x == nullptr || a.out == nullptr) return W4A16_ERR_INVALID_ARG;
   if (!aligned16(a.x) || !aligned16(a.out) || !aligned16(a.addend)) return W4A16_ERR_INVALID_ARG;
   if (a.addend == a.out && out_dtype != W4A16_DTYPE_F32) return W4A16_ERR_INVALID_ARG;
+  if (a.out == a.x || a.out == a.weight) return W4A16_ERR_INVALID_ARG;  // others still read them
   return W4A16_OK;
 }
 

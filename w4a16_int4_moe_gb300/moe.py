@@ -308,6 +308,8 @@ class SharedExpert:
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, add: bool = False,
                 stream=None) -> torch.Tensor:
         """x BF16 [T, H] -> fp32 [T, H]; add: onto what out holds."""
+        if add and out is None:
+            raise ValueError("add needs what it adds to")
         act = ops.w4a16_dense(x, self.gate_up, gated=True, stream=stream)
         return ops.w4a16_dense(act, self.down, addend=out if add else None,
                                out_dtype=torch.float32, out=out, stream=stream)
@@ -338,6 +340,8 @@ class PackedSharedExpert:
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, add: bool = False,
                 stream=None) -> torch.Tensor:
         """x BF16 [T, H] -> fp32 [T, H]; add: onto what out holds."""
+        if add and out is None:
+            raise ValueError("add needs what it adds to")
         tokens = x.shape[0]
         if tokens > self.max_tokens:
             raise ValueError("more tokens than the expert was planned for")
