@@ -605,11 +605,14 @@ int pairs_at_once(int device, cudaError_t* error) {
 }
 
 // The faster kernel and its tile by an estimate in us: rounds of tiles times the
-// steps of 64 columns of each, which the operands' way into an SM bounds (50 bytes
-// a cycle: 16 KB of tokens and 128 bytes a weight row), plus what a launch, the
-// ring's first fill and the last tile's sums take. Measured (gated, hidden 7168 x
-// 4096, 64 / 576 / 2048 tokens): split by 4 14.6 / 63 / 179, pairs of 192 44 / 38 /
-// 92, pairs of 256 48 / 41 / 74 us.
+// steps of 64 columns of each, plus what a launch, the ring's first fill and the
+// last tile's sums take. A step of a pair takes 270, 421, 540 and 590 cycles at 64,
+// 128, 192 and 256 weight rows, its MMAs alone 128 to 512: what a CTA copies (16 KB
+// of tokens and 64 bytes a weight row) goes into shared memory and out again at
+// 128 to 150 bytes a cycle. (A second copying thread changes nothing, and L2 gives
+// every SM 80 bytes a cycle.) Measured (gated, hidden 7168 x 4096, 64 / 576 / 2048
+// tokens): split by 4 14.6 / 63 / 179, pairs of 192 44 / 38 / 92, pairs of 256 48 /
+// 41 / 74 us.
 bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cudaError_t* error) {
   const int columns = a.gated ? a.n / 2 : a.n;
   const int steps = ceil_div(a.k, kKStep);
