@@ -489,7 +489,7 @@ w4a16_status w4a16_router_logits(const uint16_t* x, long long x_stride, const ui
                                  int tokens, int hidden, int num_experts, float* logits,
                                  void* stream);
 
-/* Most tokens of one w4a16_moe_few_tokens call. */
+/* Most tokens of one w4a16_moe_few_tokens or w4a16_linear_few_tokens call. */
 enum { W4A16_FEW_TOKENS_MAX = 32 };
 
 /* Device workspace bytes of w4a16_moe_few_tokens for up to `tokens` tokens (0
@@ -564,7 +564,7 @@ w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed
  *           overlaps no input but addend, which it may be.
  * tokens at most W4A16_FEW_TOKENS_MAX, k a multiple of 32, n at least 1 (GLU16: a
  * multiple of 128), both at most 2^20 (else W4A16_ERR_UNSUPPORTED); x_stride a
- * multiple of 8 and at least k, pointers 16-byte aligned (else
+ * multiple of 8, at least k and below 2^31, pointers 16-byte aligned (else
  * W4A16_ERR_INVALID_ARG). The order of the additions depends on the sizes and
  * on the device: repeated calls give the same bits. More tokens: the GEMM
  * calls, with one expert. No workspace, no host synchronisation: graph-capturable.

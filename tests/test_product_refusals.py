@@ -180,7 +180,8 @@ def test_shared_experts_that_do_not_fit_are_refused(lib):
     for e in (expert, moe.SharedExpert(gu, dn)):   # nothing to add to
         with pytest.raises(ValueError):
             e.forward(torch.zeros(1, 96, dtype=bf), add=True)
-    for bad in ((moe.PackedExperts(blob, 1, 128, 96), packed), (glu, moe.PackedExperts(blob, 1, 96, 96)),
+    for bad in ((moe.PackedExperts(blob, 1, 128, 96), packed),
+                (glu, moe.PackedExperts(blob, 1, 96, 96)),
                 (moe.PackedExperts(blob, 2, 128, 96, GLU), packed),
                 (glu, moe.PackedExperts(blob, 2, 96, 64))):
         with pytest.raises(ValueError):

@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) w4a16_block_norm_kernel(const
   for (int c = 0; c < kChunks; ++c) {
     const int k = column(c);
     const bool inside = k < a.hidden;
-    res[c] = inside && a.residual != nullptr ? load(a.residual + row * a.residual_stride + k) : zero;
+    res[c] =
+        inside && a.residual != nullptr ? load(a.residual + row * a.residual_stride + k) : zero;
     gate[c] = inside && a.gate != nullptr ? load(a.gate + row * a.gate_stride + k) : zero;
     w[c] = inside && a.post_weight != nullptr
                ? __ldg(reinterpret_cast<const uint4*>(a.post_weight + k))

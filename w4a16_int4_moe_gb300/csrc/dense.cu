@@ -91,24 +91,21 @@ struct Ring {
 };
 
 // The sums of a lane: kGroups groups of 16 columns, group g those from the
-// accumulator's column at(g) on, taken over (fresh) or added, kAtOnce groups in
-// flight. Groups from `used` on are left out (none where it is kGroups).
+// accumulator's column at(g) on, taken over (fresh) or added. Groups from `used` on
+// are left out (none where it is kGroups). One group at a time: more in flight are
+// no faster and need registers.
 constexpr int kGroups = 8;
-template <int kAtOnce, typename At>
+template <typename At>
 __device__ __forceinline__ void take_sums(float (&sum)[kGroups][16], bool fresh, int used, At at) {
 #pragma unroll
-  for (int g = 0; g < kGroups; g += kAtOnce) {
+  for (int g = 0; g < kGroups; ++g) {
     if (g >= used) break;
-    uint32_t v[kAtOnce][16];
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(at(g), v);
+    tmem_ld_wait_for(v);
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) tmem_ld_32x32b_x16(at(g + i), v[i]);
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      tmem_ld_wait_for(v[i]);
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        sum[g + i][c] = __uint_as_float(v[i][c]) + (fresh ? 0.f : sum[g + i][c]);
-    }
+    for (int c = 0; c < 16; ++c)
+      sum[g][c] = __uint_as_float(v[c]) + (fresh ? 0.f : sum[g][c]);
   }
 }
 
@@ -136,7 +133,8 @@ __device__ __forceinline__ float4 load_addend(const DenseArgs& p, int token, int
 }
 __device__ __forceinline__ uint2 bf16x4(float4 v) {
   const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                    *reinterpret_cast<const uint32_t*>(&hi));
 }
 __device__ __forceinline__ void store_out(const DenseArgs& p, int token, int c, float4 v) {
   if (token >= p.a.tokens || c >= p.columns) return;
@@ -186,7 +184,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots,
                  summed = full + 16 * kMaxSlots, drained = summed + 16;
   const uint32_t ring = smem_u32(smem);
-  const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
+  const uint32_t a_bytes = kTileM * kKStep * 2;
+  const uint32_t b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
   const uint32_t slot_bytes = a_bytes + b_bytes;
   const uint32_t rank = cluster_ctarank(), leader = 0;
   const int cluster = static_cast<int>(blockIdx.x) / 2, clusters = static_cast<int>(gridDim.x) / 2;
@@ -267,13 +266,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       float sum[kGroups][16];
       bool ok = true;
       for (int run = 0; run < runs; ++run) {
-        ok = __all_sync(0xffffffffu, dense_wait<true>(summed + 8 * acc.slot, acc.phase, failed)) && ok;
+        const bool there = dense_wait<true>(summed + 8 * acc.slot, acc.phase, failed);
+        ok = __all_sync(0xffffffffu, there) && ok;
         tc_fence_after();
-        const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 * acc.slot + side;
+        const uint32_t at =
+            tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 256 * acc.slot + side;
         // gated: gates in the first groups, ups in the last. (Columns that a narrow
         // tile does not have are read as well, and not used.)
         const uint32_t up = p.a.gated ? static_cast<uint32_t>(p.half) : kGroups / 2 * 16;
-        take_sums<1>(sum, run == 0, kGroups, [&](int g) {
+        take_sums(sum, run == 0, kGroups, [&](int g) {
           return at + g / (kGroups / 2) * up + g % (kGroups / 2) * 16;
         });
         tc_fence_before();
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         bool ok = true;
         for (int tile = cluster; tile < tiles && ok; tile += clusters) {
           uint32_t d = 0;
-          int left = 0;  // steps of this accumulator (a counter: a remainder takes 100 cycles of a step)
+          int left = 0;  // steps of this accumulator (a remainder would take 100 cycles of a step)
           for (int k = 0; k < p.k_steps; ++k) {
             const bool fresh = left == 0;
             if (fresh) {
@@ -425,9 +426,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   volatile int* failed = &failed_word;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots, summed = full + 16 * kMaxSlots, drained = summed + 16;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots,
+                 summed = full + 16 * kMaxSlots, drained = summed + 16;
   const uint32_t ring = smem_u32(smem);
-  const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
+  const uint32_t a_bytes = kTileM * kKStep * 2;
+  const uint32_t b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
   const uint32_t slot_bytes = a_bytes + 2 * b_bytes;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = static_cast<int>(blockIdx.x) / p.split;
@@ -521,11 +524,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     float sum[kGroups][16];
     Ring acc;
     for (int run = 0; run < runs; ++run) {
-      ok = __all_sync(0xffffffffu, dense_wait<false>(summed + 8 * acc.slot, acc.phase, failed)) && ok;
+      const bool there = dense_wait<false>(summed + 8 * acc.slot, acc.phase, failed);
+      ok = __all_sync(0xffffffffu, there) && ok;
       tc_fence_after();
       const uint32_t at =
           tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc.slot * acc_cols + side;
-      take_sums<1>(sum, run == 0, p.half / 16, [&](int g) { return at + g * 16; });
+      take_sums(sum, run == 0, p.half / 16, [&](int g) { return at + g * 16; });
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(drained + 8 * acc.slot);
@@ -557,7 +561,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   const int pitch = 2 * p.half + 4, quads = p.out_cols / 4;
   const int rows = min(kTileM, p.a.tokens - m * kTileM);
   const float* sums = reinterpret_cast<const float*>(smem);
-  const int begin = rank * kDenseThreads + static_cast<int>(threadIdx.x), stride = p.split * kDenseThreads;
+  const int begin = rank * kDenseThreads + static_cast<int>(threadIdx.x);
+  const int stride = p.split * kDenseThreads;
   const int r_step = stride / quads, q_step = stride - r_step * quads;
   int r = begin / quads + skip, q = begin % quads;
   for (; r < rows + skip; r += r_step, q += q_step) {
@@ -683,8 +688,8 @@ cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) 
   }
   const int smem = 1024 + std::max(p.slots * (kTileM + 2 * p.half) * kKStep * 2,
                                    kTileM * (2 * p.half + 4) * 4);
-  return launch_dependent(w4a16_dense_split_kernel, static_cast<int>(tiles) * p.split, kDenseThreads,
-                          static_cast<size_t>(smem), p.split, stream, p);
+  return launch_dependent(w4a16_dense_split_kernel, static_cast<int>(tiles) * p.split,
+                          kDenseThreads, static_cast<size_t>(smem), p.split, stream, p);
 }
 
 }  // namespace w4a16

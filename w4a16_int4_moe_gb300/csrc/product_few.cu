@@ -122,11 +122,13 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int begin = static_cast<int>(blockIdx.x) / p.split, stride = static_cast<int>(gridDim.x) / p.split;
+  const int begin = static_cast<int>(blockIdx.x) / p.split;
+  const int stride = static_cast<int>(gridDim.x) / p.split;
   const int columns = kGated ? a.n / 2 : a.n;
   const int first = p.steps * rank / p.split + warp, last = p.steps * (rank + 1) / p.split;
   const uint32_t slots = smem_u32(smem) + static_cast<uint32_t>(warp * kDepth * p.slot_bytes);
-  float* part = reinterpret_cast<float*>(smem + kWarps * kDepth * p.slot_bytes);  // [kWarps / 2][kTokens][kPitch]
+  // [kWarps / 2][kTokens][kPitch]
+  float* part = reinterpret_cast<float*>(smem + kWarps * kDepth * p.slot_bytes);
   constexpr uint32_t kWeightBytes = step_bytes(kInt4, kRows);
   // This lane's sources in the step that it fetches next. (k is a multiple of 8,
   // and a packed step is whole: only chunks of x, and of BF16 weights, can lie
@@ -376,8 +378,8 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
   // as many CTAs as the SMs hold
   const int an_sm = std::min(4, kMaxSmem / smem);
   const int clusters = p.split > 1 ? p.blocks : std::min(p.blocks, an_sm * sms);
-  return launch_dependent(kernel, clusters * p.split, kWarps * 32, static_cast<size_t>(smem), p.split,
-                          stream, p);
+  return launch_dependent(kernel, clusters * p.split, kWarps * 32, static_cast<size_t>(smem),
+                          p.split, stream, p);
 }
 
 }  // namespace
