@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libw4a16moe.so")
 
 SOURCES = ["api.cu", "moe_gemm.cu", "align.cu", "prepack.cu", "act.cu", "noalloc.cu", "permute.cu",
            "topk.cu", "det.cu", "norm.cu", "router.cu", "moe_few.cu", "dense.cu", "product_few.cu",
-           "block_norm.cu"]
+           "product_tmem.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -15,6 +15,7 @@
 #include <cmath>
 
 #include "internal.h"
+#include "pipe.cuh"
 #include "ptx.cuh"
 
 namespace w4a16 {
@@ -37,7 +38,6 @@ constexpr int kTileBytes = 32 * kChunk * 4;  // of its 32 tokens
 constexpr int kTilesBytes = kSumWarps * 2 * kTileBytes;
 constexpr int kRingBytes = 160 << 10;
 constexpr int kSmemBytes = 1024 + kRingBytes + kTilesBytes;
-constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
 
 // The tokens that a CTA multiplies when it has those from m0 on: 128 whole ones,
 // the last 128 where fewer (or none) are left. It writes only its own. (Rows that
@@ -57,37 +57,6 @@ struct DenseArgs {
   int slots;
   int run;           // steps of an accumulator before its sums are added in registers
   int split;         // CTAs of a cluster that share a tile's columns of x (split kernel)
-};
-
-__device__ __forceinline__ bool give_up(volatile int* failed, long long t0) {
-  if (*failed) return true;
-  if (clock64() - t0 <= kGiveUpCycles) return false;
-  *failed = 1;
-  return true;
-}
-// kRemote: threads of other CTAs of the cluster arrive as well.
-template <bool kRemote>
-__device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
-  const auto done = [&] {
-    return kRemote ? mbar_try_wait_cluster_now(bar, parity) : mbar_try_wait(bar, parity);
-  };
-  if (done()) return true;
-  const long long t0 = clock64();
-  while (!done())
-    if (give_up(failed, t0)) return false;
-  return true;
-}
-
-// A position in a ring of slots.
-struct Ring {
-  int slot = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int slots) {
-    if (++slot == slots) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
 };
 
 // The sums of a lane: kGroups groups of 16 columns, group g those from the
@@ -266,7 +235,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       float sum[kGroups][16];
       bool ok = true;
       for (int run = 0; run < runs; ++run) {
-        const bool there = dense_wait<true>(summed + 8 * acc.slot, acc.phase, failed);
+        const bool there = ring_wait<true>(summed + 8 * acc.slot, acc.phase, failed);
         ok = __all_sync(0xffffffffu, there) && ok;
         tc_fence_after();
         const uint32_t at =
@@ -345,7 +314,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           const int w0 = p.a.gated ? n * p.half + static_cast<int>(rank) * p.columns
                                    : (2 * n + static_cast<int>(rank)) * p.half;
           for (int k = 0; k < p.k_steps; ++k) {
-            ok = dense_wait<true>(empty + 8 * r.slot, r.phase ^ 1u, failed);
+            ok = ring_wait<true>(empty + 8 * r.slot, r.phase ^ 1u, failed);
             if (!ok) break;
             if (rank == 0) mbar_arrive_expect_tx(full + 8 * r.slot, 2 * slot_bytes);
             const uint32_t bar = map_to_cta(full + 8 * r.slot, leader);
@@ -379,13 +348,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                 tc_commit_pair_mc(summed + 8 * acc.slot, 3u);
                 acc.next(2);
               }
-              ok = dense_wait<true>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
+              ok = ring_wait<true>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
               if (!ok) break;
               d = tmem + 256 * acc.slot;
               left = p.run;
             }
             --left;
-            ok = dense_wait<true>(full + 8 * r.slot, r.phase, failed);
+            ok = ring_wait<true>(full + 8 * r.slot, r.phase, failed);
             if (!ok) break;
             tc_fence_after();
             const uint32_t from = ring + r.slot * slot_bytes;
@@ -469,7 +438,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       const int w0 = p.a.gated ? n * p.half : 2 * n * p.half;
       const int w1 = w0 + (p.a.gated ? p.columns : p.half);
       for (; k < k1; ++k) {
-        ok = dense_wait<false>(empty + 8 * r.slot, r.phase ^ 1u, failed);
+        ok = ring_wait<false>(empty + 8 * r.slot, r.phase ^ 1u, failed);
         if (!ok) break;
         const uint32_t to = ring + r.slot * slot_bytes, bar = full + 8 * r.slot;
         mbar_arrive_expect_tx(bar, slot_bytes);
@@ -498,12 +467,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             tc_commit(summed + 8 * acc.slot);
             acc.next(2);
           }
-          ok = dense_wait<false>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
+          ok = ring_wait<false>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
           if (!ok) break;
           left = p.run;
         }
         --left;
-        ok = dense_wait<false>(full + 8 * r.slot, r.phase, failed);
+        ok = ring_wait<false>(full + 8 * r.slot, r.phase, failed);
         if (!ok) break;
         tc_fence_after();
         const uint32_t from = ring + r.slot * slot_bytes;
@@ -524,7 +493,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     float sum[kGroups][16];
     Ring acc;
     for (int run = 0; run < runs; ++run) {
-      const bool there = dense_wait<false>(summed + 8 * acc.slot, acc.phase, failed);
+      const bool there = ring_wait<false>(summed + 8 * acc.slot, acc.phase, failed);
       ok = __all_sync(0xffffffffu, there) && ok;
       tc_fence_after();
       const uint32_t at =

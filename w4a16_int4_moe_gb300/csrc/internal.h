@@ -326,6 +326,8 @@ constexpr int kProductMaxSize = 1 << 20;    // n and k
 constexpr int kDenseMaxTokens = 1 << 24;
 // A packed INT4 weight (GLU16 layout when gated) and up to 32 tokens, or a BF16 one.
 cudaError_t launch_linear_few(const ProductArgs& args, int sms, cudaStream_t stream);
+// The same INT4 product for 17 to 32 tokens and many rows (product_tmem.cu).
+cudaError_t launch_linear_tmem(const ProductArgs& args, int sms, cudaStream_t stream);
 constexpr int kDenseFewTokens = 32;  // launch_dense hands them to launch_dense_few
 cudaError_t launch_dense_few(const ProductArgs& args, int sms, cudaStream_t stream);
 cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream);

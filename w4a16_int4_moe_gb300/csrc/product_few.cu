@@ -1,5 +1,5 @@
 // product_few.cu -- products with one weight, packed INT4 or BF16, for up to 32
-// tokens, plain or gated:
+// tokens (but INT4 ones of many rows for more than 16), plain or gated:
 //
 //   out[t, r] = addend[t, r] + x[t] . w[r]^T
 //   out[t, i] = silu(x[t] . wgate[i]^T) * (x[t] . wup[i]^T)
@@ -15,9 +15,7 @@
 // copy rate); INT4, the same 6.3 us for 16.5 MB, 7168 x 2048 4.4 us, where launch,
 // first load and sums are some 3 us; 16384 x 7168 16.4 us, 4.0 TB/s: the ALU pipe
 // (a shift and an AND-OR for two codes, at half rate) is busy two thirds of the
-// time, and 256 blocks on 152 SMs leave a sixth of it out. 32 tokens of 16384 x
-// 7168 32.6 us: 64 cycles of MMAs for 512 codes a scheduler, 15 us at their full
-// rate, which two warps a scheduler (176 registers) do not reach.
+// time, and 256 blocks on 152 SMs leave a sixth of it out.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -25,13 +23,12 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "product_out.cuh"
 #include "ptx.cuh"
 
 namespace w4a16 {
 
 namespace {
-
-constexpr int kMaxSmem = 232448;
 
 // d = a . b + c, BF16 operands
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -55,40 +52,11 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&w)[4
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ uint4 load_shared16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 
 // Rows of 128 bytes, 16-byte chunks c of odd rows in the other half, so that the
 // eight lanes of two rows that load at a time meet all banks.
 __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
   return static_cast<uint32_t>(row * 128 + ((c ^ (row & 1) << 2) << 4));
-}
-
-// Two codes, in bits 3 to 6 of each half word, as BF16 numbers q - 8: in those bits
-// of the number 16 a code is 16 + q, and both steps are exact. (sixteens is an
-// argument so that the compiler keeps one three-input operation: with two
-// constants it makes two of them, and 16384 x 7168 takes 18.8 instead of 16.1 us
-// for one token.)
-__device__ __forceinline__ uint32_t code_pair(uint32_t shifted, uint32_t sixteens) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(shifted), "r"(0x00780078u), "r"(sixteens));
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x41C041C0u));
-  return r;
-}
-
-// d0 += s * c0, d1 += s * c1 in one operation
-__device__ __forceinline__ void fma_pair(float& d0, float& d1, float s, float c0, float c1) {
-  asm("{\n\t.reg .b64 c, s, d;\n\t"
-      "mov.b64 c, {%3, %4};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 d, {%0, %1};\n\t"
-      "fma.rn.f32x2 d, s, c, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "+f"(d0), "+f"(d1)
-      : "f"(s), "f"(c0), "f"(c1));
 }
 
 struct FewProduct {
@@ -115,7 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
   constexpr int kThreads = kWarps * 32;
   constexpr int kRows = 16 * kMt;
   constexpr int kTokens = 8 * kNt;
-  constexpr int kPitch = kRows + 4;  // of a token's sums
+  constexpr int kPitch = kRows + kSumPad;  // of a token's sums
   static_assert(kMt % 2 == 0, "gate and up rows by sixteens, codes by 32 rows");
   extern __shared__ __align__(128) uint8_t smem[];
   const ProductArgs& a = p.a;
@@ -316,36 +284,8 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
     else
       __syncthreads();
     // every CTA of the cluster writes its share of the outputs
-    constexpr int kOut = kGated ? kRows / 2 : kRows;  // columns of the cluster
-    const int c0 = block * kOut;
-    for (int i = rank * kThreads + static_cast<int>(threadIdx.x); i < kOut * a.tokens;
-         i += p.split * kThreads) {
-      const int tok = i / kOut, c = i % kOut;
-      if (c0 + c >= columns) continue;
-      const auto sum = [&](int row) {
-        const float* at = part + tok * kPitch + row;
-        if (p.split == 1) return *at;
-        float v = 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < p.split) v += ld_cluster_f32(map_to_cta(smem_u32(at), static_cast<uint32_t>(r)));
-        return v;
-      };
-      float v;
-      if constexpr (kGated) {
-        const int row = c / 16 * 32 + c % 16;
-        const float gate = sum(row);
-        v = gate / (1.f + expf(-gate)) * sum(row + 16);
-      } else {
-        v = sum(c);
-      }
-      const long long at = static_cast<long long>(tok) * columns + c0 + c;
-      if (a.addend != nullptr) v += a.addend[at];
-      if (a.f32_out)
-        static_cast<float*>(a.out)[at] = v;
-      else
-        static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
-    }
+    write_products<kGated, kRows>(a, part, block, rank * kThreads + static_cast<int>(threadIdx.x),
+                                  p.split * kThreads, p.split);
     if (p.split > 1) cluster_sync_all();  // the sums stay until all have read them
   }
 }
@@ -362,7 +302,7 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
   p.blocks = ceil_div(args.n, kRows);
   p.steps = ceil_div(args.k, kKStep);
   p.slot_bytes = step_bytes(kInt4, kRows) + args.tokens * 128;
-  const int smem = kWarps * kDepth * p.slot_bytes + kWarps / 2 * 8 * kNt * (kRows + 4) * 4;
+  const int smem = kWarps * kDepth * p.slot_bytes + kWarps / 2 * 8 * kNt * (kRows + kSumPad) * 4;
   if (smem > 48 << 10) {
     const cudaError_t e = cudaFuncSetAttribute(
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
@@ -394,6 +334,12 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
 //   BF16, one token, 4096 rows: 32 x 5 10.7, 32 x 3 11.2; 7168 x 2048 7.3, 6.7
 //   BF16, 16 tokens, 4096 rows: 32 x 4 11.4, 32 x 2 12.9; 7168 x 2048 8.3, 7.2
 //   BF16, 32 tokens, 4096 rows: 32 x 3 12.6, 64 x 2 14.9; 7168 x 2048 9.5, 9.1
+// INT4 rows more than 64 an SM and more than 16 tokens go to tcgen05 (us of mma.sync
+// and of tcgen05, 32 tokens; with 17 both are 3 % faster): 12288 rows 32.5, 23.1;
+// 16384 32.8, 23.8; 32768 63.6, 45.1; 16384 x 2048 13.5, 10.0. With fewer rows blocks
+// of 128 are on half of the SMs or fewer: 9728 rows 17.4, 16.4, but 9728 x 2048 7.7,
+// 8.9, and 4096 rows 10.5, 10.7. 16 tokens are half of the MMAs: 16384 rows 22.2,
+// 20.9, but 65536 71.6, 75.9.
 template <bool kInt4, bool kGated>
 cudaError_t few(const ProductArgs& args, int sms, cudaStream_t stream) {
   const bool one = args.n <= 32 * sms;
@@ -407,6 +353,7 @@ cudaError_t few(const ProductArgs& args, int sms, cudaStream_t stream) {
     if (args.tokens <= 16)
       return wide ? run<kInt4, kGated, 4, 2, 5>(args, sms, stream)
                   : run<kInt4, kGated, 2, 2, 4>(args, sms, stream);
+    if (wide) return launch_linear_tmem(args, sms, stream);
     return one ? run<kInt4, kGated, 2, 4, 2>(args, sms, stream)
                : run<kInt4, kGated, 4, 4, 3>(args, sms, stream);
   } else {
