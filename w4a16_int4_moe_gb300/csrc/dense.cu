@@ -647,8 +647,9 @@ cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) 
       !encode_rows_tmap(&p.weight, args.weight, args.n, args.k, args.k, p.half))
     return cudaErrorInvalidValue;
   const long long tiles = static_cast<long long>(p.m_tiles) * p.n_tiles;
-  e = cudaFuncSetAttribute(pair ? w4a16_dense_pair_kernel : w4a16_dense_split_kernel,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static Devices known[2];
+  e = allow_smem(pair ? w4a16_dense_pair_kernel : w4a16_dense_split_kernel, kSmemBytes,
+                 known[pair ? 1 : 0]);
   if (e != cudaSuccess) return e;
   if (pair) {
     const int clusters = static_cast<int>(std::min<long long>(tiles, pairs_at_once(device, &e)));

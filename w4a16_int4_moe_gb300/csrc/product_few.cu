@@ -304,8 +304,8 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
   p.slot_bytes = step_bytes(kInt4, kRows) + args.tokens * 128;
   const int smem = kWarps * kDepth * p.slot_bytes + kWarps / 2 * 8 * kNt * (kRows + kSumPad) * 4;
   if (smem > 48 << 10) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    static Devices known{0};
+    const cudaError_t e = allow_smem(kernel, kMaxSmem, known);
     if (e != cudaSuccess) return e;
   }
   // a cluster of two, four or eight where all CTAs still find an SM and every

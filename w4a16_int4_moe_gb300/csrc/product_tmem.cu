@@ -271,8 +271,8 @@ cudaError_t launch_linear_tmem(const ProductArgs& args, int sms, cudaStream_t st
   p.sixteens = 0x41804180u;
   p.blocks = ceil_div(args.n, kTileRows);
   p.steps = ceil_div(args.k, kKStep);
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTmemSmem);
+  static Devices known[2];
+  const cudaError_t e = allow_smem(kernel, kTmemSmem, known[args.gated ? 1 : 0]);
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, std::min(p.blocks, sms), kTmemThreads, kTmemSmem, 1, stream, p);
 }
