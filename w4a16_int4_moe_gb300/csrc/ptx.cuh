@@ -90,6 +90,20 @@ __device__ __forceinline__ void copy16_of(uint32_t to, const void* from, int byt
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
                : "memory");
 }
+// A line, a range (16-byte aligned, of a multiple of 16 bytes) or a box of a 2-D
+// tensor map sets out for L2. Nothing is read by that: a kernel may ask for its
+// weights so before what it depends on, and might write them, has ended.
+__device__ __forceinline__ void prefetch_l2(const void* at) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(at) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2_range(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2_2d(const void* map, int col, int row) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map),
+               "r"(col), "r"(row)
+               : "memory");
+}
 // What was copied since the last one is a group.
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
