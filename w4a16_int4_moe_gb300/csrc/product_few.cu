@@ -322,19 +322,24 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
   p.blocks = ceil_div(args.n, kRows);
   p.steps = ceil_div(args.k, kKStep);
   p.slot_bytes = step_bytes(kInt4, kRows) + args.tokens * 128;
-  const int smem = kWarps * kDepth * p.slot_bytes + kWarps / 2 * 8 * kNt * (kRows + kSumPad) * 4;
+  // a cluster of two, four or eight where all CTAs still find an SM and every warp a
+  // step; eights, which do not all find a place at once, on half of the SMs. (One
+  // token and 7168 columns, BF16: 128 rows in eights 2.7 us, in fours 3.3; 32 tokens
+  // and 512 rows, INT4: 8.2 in eights, 4.9 in fours.)
+  p.split = 1;
+  while (p.split < 8 && (p.split < 4 ? 2 : 4) * p.blocks * p.split <= sms &&
+         p.steps >= 2 * p.split * kWarps)
+    p.split *= 2;
+  // Where every CTA has an SM of its own, no two of them may share one: those of the
+  // next launch, which come early, would crowd into the SMs that this one leaves out
+  // (launches one after another of 4096 x 7168, INT4, one token: 6.2 -> 5.7 us).
+  int smem = kWarps * kDepth * p.slot_bytes + kWarps / 2 * 8 * kNt * (kRows + kSumPad) * 4;
+  if (p.blocks <= sms) smem = std::max(smem, kMaxSmem / 2 + 1);
   if (smem > 48 << 10) {
     static Devices known{0};
     const cudaError_t e = allow_smem(kernel, kMaxSmem, known);
     if (e != cudaSuccess) return e;
   }
-  // a cluster of two, four or eight where all CTAs still find an SM and every
-  // warp a step. (Eights that want an SM each do not all find a place at once: 512
-  // rows of 7168 in BF16 7.6 us, in fours 4.5.)
-  const int most = smem > 100 << 10 ? 4 : 8;
-  p.split = 1;
-  while (p.split < most && 2 * p.blocks * p.split <= sms && p.steps >= 2 * p.split * kWarps)
-    p.split *= 2;
   // as many CTAs as the SMs hold
   const int an_sm = std::min(4, kMaxSmem / smem);
   const int clusters = p.split > 1 ? p.blocks : std::min(p.blocks, an_sm * sms);
