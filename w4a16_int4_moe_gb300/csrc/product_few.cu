@@ -11,9 +11,9 @@
 // weight rows. The packed codes become BF16 numbers q - 8, and a group's scale is
 // applied to its FP32 sum, so no weight is rounded.
 //
-// One token, in a graph: BF16, 4096 x 7168 gated 10.7 us, 5.5 TB/s (0.81 of the
-// copy rate); INT4, the same 6.3 us for 16.5 MB, 7168 x 2048 4.4 us, where launch,
-// first load and sums are some 3 us; 16384 x 7168 16.4 us, 4.0 TB/s: the ALU pipe
+// One token, in a graph: BF16, 4096 x 7168 gated 10.0 us, 5.9 TB/s (0.86 of the
+// copy rate); INT4, the same 5.7 us for 16.5 MB, 7168 x 2048 4.0 us, where launch,
+// first load and sums are some 3 us; 16384 x 7168 15.2 us, 4.3 TB/s: the ALU pipe
 // (a shift and an AND-OR for two codes, at half rate) is busy two thirds of the
 // time, and 256 blocks on 152 SMs leave a sixth of it out.
 
@@ -352,13 +352,17 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
 // Rows of a block and steps in flight by the tokens, and by whether blocks of 32
 // rows are at most one an SM (us in a graph, weights not in L2, hidden 7168 unless
 // said):
-//   INT4, one token, 16384 rows: 32 x 5 17.7, 64 x 4 16.4; 4096 rows 6.8, 7.6, and
-//     with 16 warps for eight 32 x 3 6.3 (7168 x 2048: 4.4 with eight, 4.5)
-//   INT4, 16 tokens, 16384 rows: 32 x 4 23.7, 64 x 5 22.1; 4096 rows 7.8, 8.9
-//   INT4, 32 tokens, 4096 rows: 32 x 2 11.0, 64 x 3 12.0; 7168 x 2048 8.8, 7.5
+//   INT4, one token, 9728 rows: 32 x 5 12.2, 64 x 4 10.3; 16384 rows 18.0, 15.9; 7168 x
+//     2048 4.0, 3.9; 4096 rows 6.2, 6.8, and with 16 warps for eight 32 x 3 5.5 (1024
+//     rows: 3.6 with eight, 3.7)
+//   INT4, 16 tokens, 9728 rows: 32 x 4 12.9, 64 x 5 12.3; 16384 rows 23.6, 22.2; 4096
+//     rows 7.6, 8.2
+//   INT4, 32 tokens, 4096 rows: 32 x 2 10.3, 32 x 3 10.1, 64 x 3 11.2; 9728 rows 20.2,
+//     19.2, 17.1
 //   BF16, one token, 4096 rows: 32 x 5 10.7, 32 x 3 11.2; 7168 x 2048 7.3, 6.7
 //   BF16, 16 tokens, 4096 rows: 32 x 4 11.4, 32 x 2 12.9; 7168 x 2048 8.3, 7.2
 //   BF16, 32 tokens, 4096 rows: 32 x 3 12.6, 64 x 2 14.9; 7168 x 2048 9.5, 9.1
+// (BF16 before the first weights set out early, which takes off 0.4 to 0.7.)
 // INT4 rows more than 64 an SM and more than 16 tokens go to tcgen05 (us of mma.sync
 // and of tcgen05, 32 tokens; with 17 both are 3 % faster): 12288 rows 32.5, 23.1;
 // 16384 32.8, 23.8; 32768 63.6, 45.1; 16384 x 2048 13.5, 10.0. With fewer rows blocks
@@ -369,17 +373,16 @@ template <bool kInt4, bool kGated>
 cudaError_t few(const ProductArgs& args, int sms, cudaStream_t stream) {
   const bool one = args.n <= 32 * sms;
   if constexpr (kInt4) {
-    const bool wide = args.n > 64 * sms;
     if (args.tokens <= 8 && one && args.n > 16 * sms)  // (no cluster either)
       return run<kInt4, kGated, 2, 1, 3, 16>(args, sms, stream);
     if (args.tokens <= 8)
-      return wide ? run<kInt4, kGated, 4, 1, 4>(args, sms, stream)
-                  : run<kInt4, kGated, 2, 1, 5>(args, sms, stream);
+      return one ? run<kInt4, kGated, 2, 1, 5>(args, sms, stream)
+                 : run<kInt4, kGated, 4, 1, 4>(args, sms, stream);
     if (args.tokens <= 16)
-      return wide ? run<kInt4, kGated, 4, 2, 5>(args, sms, stream)
-                  : run<kInt4, kGated, 2, 2, 4>(args, sms, stream);
-    if (wide) return launch_linear_tmem(args, sms, stream);
-    return one ? run<kInt4, kGated, 2, 4, 2>(args, sms, stream)
+      return one ? run<kInt4, kGated, 2, 2, 4>(args, sms, stream)
+                 : run<kInt4, kGated, 4, 2, 5>(args, sms, stream);
+    if (args.n > 64 * sms) return launch_linear_tmem(args, sms, stream);
+    return one ? run<kInt4, kGated, 2, 4, 3>(args, sms, stream)
                : run<kInt4, kGated, 4, 4, 3>(args, sms, stream);
   } else {
     if (args.tokens <= 8)
