@@ -594,7 +594,9 @@ int pairs_at_once(int device, cudaError_t* error) {
 // 128 to 150 bytes a cycle. (A second copying thread changes nothing, and L2 gives
 // every SM 80 bytes a cycle.) Measured (gated, hidden 7168 x 4096, 64 / 576 / 2048
 // tokens): split by 4 14.6 / 63 / 179, pairs of 192 44 / 38 / 92, pairs of 256 48 /
-// 41 / 74 us.
+// 41 / 74 us. Pairs take widths in steps of 32 (2048 tokens: 224 rows 68 us, 256 73;
+// 700 tokens, 7168 x 18432: 139 and 159), the split kernel, whose estimate is too low at
+// 224 (400 tokens 31 us, pairs of 128 29), in steps of 64.
 bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cudaError_t* error) {
   const int columns = a.gated ? a.n / 2 : a.n;
   const int steps = ceil_div(a.k, kKStep);
@@ -606,7 +608,7 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
     pair = is_pair;
     *best = c;
   };
-  for (int tile_n = 64; tile_n <= 256; tile_n += 64) {
+  for (int tile_n = 64; tile_n <= 256; tile_n += 32) {
     DenseArgs c = {};
     c.columns = columns;
     c.half = tile_n / 2;
@@ -624,6 +626,7 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
     consider(c, true, rounds * std::max(steps * (0.095 + tile_n * 0.00085), 2.0 + tile_n * 0.008) +
                           5 + tile_n * 0.01 + gate);
 
+    if (tile_n % 64 != 0) continue;
     c.m_tiles = ceil_div(a.tokens, kTileM);
     c.slots = std::min(kMaxSlots, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
     const double rows = std::min(a.tokens, kTileM);
