@@ -13,23 +13,23 @@
 
 using namespace w4a16;
 
-namespace {
-
-constexpr int kMaxDynSmem = 232448;  // 227 KB per CTA on sm_103a
-constexpr long long kDefaultTimeoutCycles = 2000000000LL;  // about a second
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-w4a16_status cuda_status(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
-
-long long wait_timeout_cycles() {
+long long w4a16::wait_timeout_cycles() {
+  constexpr long long kDefault = 2000000000LL;  // about a second
   const char* s = std::getenv("W4A16_WAIT_TIMEOUT_CYCLES");
   if (s != nullptr) {
     const long long v = std::atoll(s);
     if (v > 0) return v;
   }
-  return kDefaultTimeoutCycles;
+  return kDefault;
 }
+
+namespace {
+
+constexpr int kMaxDynSmem = 232448;  // 227 KB per CTA on sm_103a
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+w4a16_status cuda_status(cudaError_t e) { return e == cudaSuccess ? W4A16_OK : W4A16_ERR_CUDA; }
 
 int round_up(int x, int m) { return (x + m - 1) / m * m; }
 

@@ -57,6 +57,7 @@ struct DenseArgs {
   int slots;
   int run;           // steps of an accumulator before its sums are added in registers
   int split;         // CTAs of a cluster that share a tile's columns of x (split kernel)
+  long long wait_limit;  // cycles
 };
 
 // The sums of a lane: kGroups groups of 16 columns, group g those from the
@@ -144,14 +145,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bars[2 * kMaxSlots + 4];
+  __shared__ uint64_t bars[2 * kMaxSlots + 5];
   __shared__ uint32_t tmem_at;
-  __shared__ int failed_word;
+  __shared__ int failed_word, copied, given_up;  // steps copied; the first CTA's failed_word
   volatile int* failed = &failed_word;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots,
-                 summed = full + 16 * kMaxSlots, drained = summed + 16;
+                 summed = full + 16 * kMaxSlots, drained = summed + 16,
+                 idle = drained + 16;
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2;
   const uint32_t b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
@@ -169,7 +171,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         mbar_init(summed + 8 * i, 1);
         mbar_init(drained + 8 * i, 2 * kSumWarps);
       }
+      mbar_init(idle, 1);
       *failed = 0;
+      given_up = 0;
       fence_mbar_init();
     }
     __syncwarp();
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       float sum[kGroups][16];
       bool ok = true;
       for (int run = 0; run < runs; ++run) {
-        const bool there = ring_wait<true>(summed + 8 * acc.slot, acc.phase, failed);
+        const bool there = ring_wait<true>(summed + 8 * acc.slot, acc.phase, failed, p.wait_limit);
         ok = __all_sync(0xffffffffu, there) && ok;
         tc_fence_after();
         const uint32_t at =
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         });
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * acc.slot, leader));
+        if (ok && lane == 0) mbar_arrive_remote_relaxed(map_to_cta(drained + 8 * acc.slot, leader));
         acc.next(2);
       }
 #pragma unroll
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           const int w0 = p.a.gated ? n * p.half + static_cast<int>(rank) * p.columns
                                    : (2 * n + static_cast<int>(rank)) * p.half;
           for (int k = 0; k < p.k_steps; ++k) {
-            ok = ring_wait<true>(empty + 8 * r.slot, r.phase ^ 1u, failed);
+            ok = ring_wait<true>(empty + 8 * r.slot, r.phase ^ 1u, failed, p.wait_limit);
             if (!ok) break;
             if (rank == 0) mbar_arrive_expect_tx(full + 8 * r.slot, 2 * slot_bytes);
             const uint32_t bar = map_to_cta(full + 8 * r.slot, leader);
@@ -325,13 +329,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             r.next(p.slots);
           }
         }
-        if (!ok && rank == 0)  // copies in flight land before the CTAs end
-          for (int i = std::max(0, issued - p.slots); i < issued; ++i) {
-            const long long t0 = clock64();
-            while (!mbar_try_wait_cluster_now(full + 8 * (i % p.slots), i / p.slots & 1) &&
-                   clock64() - t0 < kGiveUpCycles) {
-            }
-          }
+        copied = issued;
       }
     } else if (warp == kWarpMma) {
       if (rank == 0 && elect_one()) {
@@ -348,13 +346,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
                 tc_commit_pair_mc(summed + 8 * acc.slot, 3u);
                 acc.next(2);
               }
-              ok = ring_wait<true>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
+              ok = ring_wait<true>(drained + 8 * acc.slot, acc.phase ^ 1u, failed, p.wait_limit);
               if (!ok) break;
               d = tmem + 256 * acc.slot;
               left = p.run;
             }
             --left;
-            ok = ring_wait<true>(full + 8 * r.slot, r.phase, failed);
+            ok = ring_wait<true>(full + 8 * r.slot, r.phase, failed, p.wait_limit);
             if (!ok) break;
             tc_fence_after();
             const uint32_t from = ring + r.slot * slot_bytes;
@@ -369,14 +367,38 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           if (ok) tc_commit_pair_mc(summed + 8 * acc.slot, 3u);
           acc.next(2);
         }
+        tc_commit_pair_mc(idle, 3u);
+        drain<true>(idle, 0);  // (behind the last sums it is as good as done)
       }
     }
   }
   tc_fence_before();
   __syncwarp();
   __syncthreads();
+  if (rank == 0 && threadIdx.x == 0 && *failed) {
+    given_up = 1;
+    st_cluster_s32(map_to_cta(smem_u32(&given_up), 1), 1);
+  }
   cluster_sync_all();  // nothing reaches across any more
+  if (given_up) {
+    // (else every copy has been multiplied.) The two may have stopped at different
+    // steps: the first CTA, to which all copies report, expects what only the other
+    // has copied, counts what that has not, and all that is under way lands.
+    if (rank == 0 && threadIdx.x == 0) {
+      const int other = ld_cluster_s32(map_to_cta(smem_u32(&copied), 1));
+      const int end = max(copied, other);
+      for (int i = max(0, end - p.slots); i < end; ++i) {
+        const uint32_t bar = full + 8 * (i % p.slots);
+        if (i >= copied) mbar_arrive_expect_tx(bar, slot_bytes);
+        if (i >= other) mbar_complete_tx(bar, slot_bytes);
+        drain<true>(bar, i / p.slots & 1);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
   if (warp == kWarpMma) {
+    drain<true>(idle, 0);  // also of the second CTA: the last that the first sends it
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
@@ -389,14 +411,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bars[2 * kMaxSlots + 4];
+  __shared__ uint64_t bars[2 * kMaxSlots + 5];
   __shared__ uint32_t tmem_at;
   __shared__ int failed_word;
   volatile int* failed = &failed_word;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots,
-                 summed = full + 16 * kMaxSlots, drained = summed + 16;
+                 summed = full + 16 * kMaxSlots, drained = summed + 16,
+                 idle = drained + 16;
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2;
   const uint32_t b_bytes = static_cast<uint32_t>(p.half) * kKStep * 2;
@@ -427,6 +450,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         mbar_init(summed + 8 * i, 1);
         mbar_init(drained + 8 * i, kSumWarps);
       }
+      mbar_init(idle, 1);
       *failed = 0;
       fence_mbar_init();
     }
@@ -446,7 +470,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       Ring r;
       int k = k0;
       for (; k < k1; ++k) {
-        ok = ring_wait<false>(empty + 8 * r.slot, r.phase ^ 1u, failed);
+        ok = ring_wait<false>(empty + 8 * r.slot, r.phase ^ 1u, failed, p.wait_limit);
         if (!ok) break;
         const uint32_t to = ring + r.slot * slot_bytes, bar = full + 8 * r.slot;
         mbar_arrive_expect_tx(bar, slot_bytes);
@@ -455,13 +479,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         tma_load_2d(to, &p.x, k * kKStep, m0, bar);
         r.next(p.slots);
       }
-      if (!ok)  // copies in flight land before the CTA ends
-        for (int i = std::max(0, k - k0 - p.slots); i < k - k0; ++i) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(full + 8 * (i % p.slots), i / p.slots & 1) &&
-                 clock64() - t0 < kGiveUpCycles) {
-          }
-        }
+      // copies in flight land before the CTA ends (they have, where all were multiplied)
+      for (int i = max(0, k - k0 - p.slots); i < k - k0; ++i)
+        drain<false>(full + 8 * (i % p.slots), i / p.slots & 1);
     }
   } else if (warp == kWarpMma) {
     if (elect_one()) {
@@ -475,12 +495,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
             tc_commit(summed + 8 * acc.slot);
             acc.next(2);
           }
-          ok = ring_wait<false>(drained + 8 * acc.slot, acc.phase ^ 1u, failed);
+          ok = ring_wait<false>(drained + 8 * acc.slot, acc.phase ^ 1u, failed, p.wait_limit);
           if (!ok) break;
           left = p.run;
         }
         --left;
-        ok = ring_wait<false>(full + 8 * r.slot, r.phase, failed);
+        ok = ring_wait<false>(full + 8 * r.slot, r.phase, failed, p.wait_limit);
         if (!ok) break;
         tc_fence_after();
         const uint32_t from = ring + r.slot * slot_bytes;
@@ -493,6 +513,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         r.next(p.slots);
       }
       if (ok) tc_commit(summed + 8 * acc.slot);
+      tc_commit(idle);
+      drain<false>(idle, 0);
     }
   } else if (warp < kSumWarps) {
     // lane + 32 (warp % 4) = token of the tile, half of the weight rows
@@ -501,7 +523,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     float sum[kGroups][16];
     Ring acc;
     for (int run = 0; run < runs; ++run) {
-      const bool there = ring_wait<false>(summed + 8 * acc.slot, acc.phase, failed);
+      const bool there = ring_wait<false>(summed + 8 * acc.slot, acc.phase, failed, p.wait_limit);
       ok = __all_sync(0xffffffffu, there) && ok;
       tc_fence_after();
       const uint32_t at =
@@ -509,22 +531,19 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       take_sums(sum, run == 0, p.half / 16, [&](int g) { return at + g * 16; });
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(drained + 8 * acc.slot);
+      if (ok && lane == 0) mbar_arrive(drained + 8 * acc.slot);
       acc.next(2);
     }
     // (nothing reads the ring any more: all of its copies were multiplied)
     float* row = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * pitch + side;
-    if (m0 + quarter * 32 < p.a.tokens)  // (whole warps)
+    if (ok && m0 + quarter * 32 < p.a.tokens)  // (whole warps)
 #pragma unroll
       for (int g = 0; g < kGroups; ++g)
         if (g * 16 < p.half)
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float nan = __uint_as_float(0x7FC00000u);
+          for (int i = 0; i < 16; i += 4)
             *reinterpret_cast<float4*>(row + g * 16 + i) =
-                ok ? make_float4(sum[g][i], sum[g][i + 1], sum[g][i + 2], sum[g][i + 3])
-                   : make_float4(nan, nan, nan, nan);
-          }
+                make_float4(sum[g][i], sum[g][i + 1], sum[g][i + 2], sum[g][i + 3]);
   }
   tc_fence_before();
   __syncwarp();
@@ -533,9 +552,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, tmem_cols);
   }
+  const int pitch = 2 * p.half + 4, quads = p.out_cols / 4;
+  if (*failed) {  // (only now that no copy is under way into this memory)
+    for (int i = threadIdx.x; i < kTileM * pitch; i += kDenseThreads)
+      reinterpret_cast<float*>(smem)[i] = __uint_as_float(0x7FC00000u);
+    __syncthreads();
+  }
   if (p.split > 1) cluster_sync_all();
   // every CTA of the cluster finishes a share of the tile, four columns a thread
-  const int pitch = 2 * p.half + 4, quads = p.out_cols / 4;
   const int rows = min(kTileM, p.a.tokens - m * kTileM);
   const float* sums = reinterpret_cast<const float*>(smem);
   const int begin = rank * kDenseThreads + static_cast<int>(threadIdx.x);
@@ -654,6 +678,7 @@ cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) 
   const bool pair = dense_shape(args, sms, device, &p, &e);
   if (e != cudaSuccess) return e;
   p.a = args;
+  p.wait_limit = wait_timeout_cycles();
   if (!encode_rows_tmap(&p.x, args.x, args.tokens, args.k, args.x_stride, kTileM) ||
       !encode_rows_tmap(&p.weight, args.weight, args.n, args.k, args.k, p.half))
     return cudaErrorInvalidValue;

@@ -227,6 +227,9 @@ cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int threads, s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
+// After how many cycles a kernel's waits give up (W4A16_WAIT_TIMEOUT_CYCLES).
+long long wait_timeout_cycles();
+
 // How many clusters of a kernel run at once, by device (0: not asked yet).
 constexpr int kMaxDevices = 64;
 using ClustersAtOnce = std::atomic<int>[kMaxDevices];

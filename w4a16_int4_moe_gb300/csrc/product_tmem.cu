@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
   // The sums of the step whose scales lie at `scales`, once its MMAs are done: 16
   // columns at a time, while the next ones are on their way.
   const auto add = [&](uint32_t scales) {
-    const bool there = ring_wait<false>(done, phase, failed);
+    const bool there = ring_wait<false>(done, phase, failed, kDrainCycles);
     ok = __all_sync(0xffffffffu, there) && ok;
     phase ^= 1u;
     tc_fence_after();
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
     uint32_t under = 0;  // scales of the step under way
     for (int unit = group; unit < units; unit += kGroups, r.next(kRing)) {
       const uint32_t slot = ring + r.slot * kUnitBytes;
-      const bool there = ring_wait<false>(full + 8 * r.slot, r.phase, failed);
+      const bool there = ring_wait<false>(full + 8 * r.slot, r.phase, failed, kDrainCycles);
       ok = __all_sync(0xffffffffu, there) && ok;
       uint4 w[kUnit][2];
 #pragma unroll
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
     for (int i = std::max(0, fetched - kRing); i < fetched; ++i) {
       const long long t0 = clock64();
       while (!mbar_try_wait(full + 8 * (i % kRing), i / kRing & 1) &&
-             clock64() - t0 < kGiveUpCycles) {
+             clock64() - t0 < kDrainCycles) {
       }
     }
   tc_fence_before();
