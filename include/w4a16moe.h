@@ -558,7 +558,8 @@ w4a16_status w4a16_moe_few_tokens(const void* packed_gate_up, const void* packed
  * The codes and x enter the products exactly, the scale is applied to a
  * group's FP32 sum, sums are FP32, and the result is rounded once. A group's sum
  * is finite for |x| below 2^120, whatever its scale. A device-side wait that gives
- * up after about two seconds leaves NaN in the outputs that waited.
+ * up (W4A16_WAIT_TIMEOUT_CYCLES, about a second) leaves NaN in the outputs that
+ * waited.
  *   packed  w4a16_prepack's blob of one expert, [1, n, k] in `layout`;
  *   x       BF16 [tokens, k], row stride x_stride elements;
  *   addend  FP32 [tokens, n] or NULL (gated: NULL);

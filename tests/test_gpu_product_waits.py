@@ -9,16 +9,18 @@ import pytest
 import torch
 
 from helpers import Guarded
-from test_gpu_products import Dense, _rows
+from test_gpu_products import Dense, Int4, _rows
 
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
 # (kind, tokens, n, k, gated, f32): CTA pairs that go over several tiles each, with one
-# and with several accumulators a tile; clusters that split the columns.
+# and with several accumulators a tile; clusters that split the columns; the packed
+# weight's tcgen05 kernel, with blocks that come round again.
 CASES = [(Dense, 8192, 7168, 2048, False, True), (Dense, 8192, 4096, 1096, True, False),
          (Dense, 5000, 7168, 64, False, False),
-         (Dense, 100, 2002, 2088, True, False), (Dense, 200, 1000, 7168, False, True)]
+         (Dense, 100, 2002, 2088, True, False), (Dense, 200, 1000, 7168, False, True),
+         (Int4, 20, 20001, 1568, False, True), (Int4, 32, 39168, 1056, True, False)]
 
 
 def _case(dev, kind, tokens, n, k, gated, f32):

@@ -9,7 +9,7 @@
 // own there, which times the group's scale are added up in FP32 registers, so no
 // weight is rounded.
 //
-// 32 tokens of 16384 x 7168 in a graph: 23.8 us, 2.8 TB/s of the weight; with
+// 32 tokens of 16384 x 7168 in a graph: 23.5 us, 2.8 TB/s of the weight; with
 // mma.sync, whose accumulators go through the same FP32 additions, 32.8: beside
 // them a scheduler starts an MMA in 12.8 cycles instead of 8.5. Here a step takes a
 // scheduler 330 cycles, in which it issues 220 instructions, 96 of them for the
@@ -37,6 +37,9 @@ constexpr int kGroupThreads = 128;  // a weight row, and a TMEM lane, each
 constexpr int kTmemThreads = kGroups * kGroupThreads;
 constexpr int kUnit = 2;            // steps of a slot of the ring, each with a buffer in TMEM
 constexpr int kRing = 3;            // slots of a group
+// Barriers of a group: slots that are full, MMAs that are done, and for each issuing
+// warp that its last MMAs are over.
+constexpr int kBars = kRing + 1 + kUnit;
 constexpr int kPitch = kTileRows + kSumPad;  // of a token's sums
 // A group's columns of TMEM: the sums of a step's two halves, then the buffers.
 constexpr int kGroupColumns = 512 / kGroups, kNumbersAt = 2 * kTokens, kNumbers = kKStep / 2;
@@ -54,14 +57,20 @@ struct TmemProduct {
   int blocks;         // of 128 weight rows
   int steps;          // of 64 columns
   uint32_t sixteens;  // 16 as two BF16 numbers
+  long long wait_limit;  // cycles
 };
 
-// The warps of a group meet where one of them goes on for all.
-__device__ __forceinline__ void group_wait(int group) {
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
+// The warps of a group meet where one of them goes on for all, at two barriers by
+// turns. None comes to a barrier again before all have left it: one that arrives and
+// goes on waits next for the MMAs that are issued behind the barrier, and one of which
+// a wait gave up, and which waits for nothing else any more, stays at every barrier
+// until all are there. (Else its arrivals would stand in for those of others, and who
+// stays would stay for ever.)
+__device__ __forceinline__ void group_wait(int barrier) {
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(kGroupThreads) : "memory");
 }
-__device__ __forceinline__ void group_arrive(int group) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory");
+__device__ __forceinline__ void group_arrive(int barrier) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(barrier), "n"(kGroupThreads) : "memory");
 }
 
 }  // namespace
@@ -77,18 +86,19 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* part = reinterpret_cast<float*>(smem + kGroups * kRing * kUnitBytes);  // [kTokens][kPitch]
-  __shared__ uint64_t bars[kGroups * (kRing + 1)];
+  __shared__ uint64_t bars[kGroups * kBars];
   __shared__ uint32_t tmem_at;
   __shared__ int failed_word;
   volatile int* failed = &failed_word;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const int group = warp / 4, row = warp % 4 * 32 + lane;
-  const uint32_t full = smem_u32(bars + group * (kRing + 1)), done = full + 8 * kRing;
+  const uint32_t full = smem_u32(bars + group * kBars), done = full + 8 * kRing,
+                 idle = done + 8;
   const uint32_t ring = smem_u32(smem) + group * (kRing * kUnitBytes);
   const int begin = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
   const int units = (p.steps + kUnit - 1) / kUnit;
-  // The first weights set out while the kernel before is at work (23.1 -> 22.8 us).
+  // The first weights set out while the kernel before is at work (0.3 us less).
   if (warp % 4 == 1 && elect_one())
     for (int i = 0; i < kRing && group + i * kGroups < units; ++i) {
       const int step = (group + i * kGroups) * kUnit;
@@ -99,7 +109,7 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
   __syncwarp();
   if (warp == 0) {
     if (lane == 0) {
-      for (int i = 0; i < kGroups * (kRing + 1); ++i) mbar_init(smem_u32(bars + i), 1);
+      for (int i = 0; i < kGroups * kBars; ++i) mbar_init(smem_u32(bars + i), 1);
       *failed = 0;
       fence_mbar_init();
     }
@@ -147,7 +157,7 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
     for (int i = 0; i < kRing; ++i) fetch();
   Ring r;
   uint32_t phase = 0;
-  bool ok = true;  // (after a wait that gave up all go on, and end, without waiting)
+  bool ok = true;  // no wait of this warp has given up
   float sum[kTokens];
   // A step's codes into buffer j.
   const auto convert = [&](const uint4 (&codes)[2], int j) {
@@ -166,10 +176,10 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
     }
   };
   // The sums of the step whose scales lie at `scales`, once its MMAs are done: 16
-  // columns at a time, while the next ones are on their way.
+  // columns at a time, while the next ones are on their way. False if they never are.
   const auto add = [&](uint32_t scales) {
-    const bool there = ring_wait<false>(done, phase, failed, kDrainCycles);
-    ok = __all_sync(0xffffffffu, there) && ok;
+    const bool there = ring_wait<false>(done, phase, failed, p.wait_limit);
+    if (!__all_sync(0xffffffffu, there)) return false;
     phase ^= 1u;
     tc_fence_after();
     uint32_t v[2][16];
@@ -185,18 +195,22 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
         fma_pair(sum[t0 + c], sum[t0 + c + 1], scale[i * 16 / kTokens],
                  __uint_as_float(v[i % 2][c]), __uint_as_float(v[i % 2][c + 1]));
     }
+    return true;
   };
   // The MMAs of buffer j, by one warp (another one for each j) once all four have
   // converted their rows and read the sums of before; the others go on. Then the
   // slot of the unit before is free.
+  int barrier = 2 + 2 * group;  // and the next one (0 is that of the whole CTA)
   const auto multiply = [&](uint32_t x_at, int j, bool refill) {
     tmem_st_wait();
     tc_fence_before();
+    const int here = barrier;
+    barrier ^= 1;
     if (warp % 4 != j) {
-      group_arrive(group);
+      group_arrive(here);
       return;
     }
-    group_wait(group);
+    group_wait(here);
     tc_fence_after();
     if (elect_one()) {
       const uint64_t x = smem_desc_sw128_kmajor(x_at);
@@ -207,17 +221,28 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
       tc_commit(done);
     }
     __syncwarp();
-    if (j == 0 && refill && ok) fetch();
+    if (j == 0 && refill) fetch();
   };
   const uint32_t codes_at = kCodes + row * 16, scales_at = kCodes + kStepQBytes + row * 2;
+  // the group's steps of a block
+  const int steps = units <= group ? 0 : (units - 1 - group) / kGroups * kUnit + kUnit -
+                                             ((units - 1 - group) % kGroups == 0 && p.steps % kUnit);
   for (int block = begin; block < p.blocks; block += stride) {
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) sum[i] = 0.f;
     uint32_t under = 0;  // scales of the step under way
-    for (int unit = group; unit < units; unit += kGroups, r.next(kRing)) {
+    int left = ok ? 0 : steps;  // that this warp takes no part in
+    for (int unit = ok ? group : units; unit < units; unit += kGroups, r.next(kRing)) {
+      const auto give_up_at = [&](int j) {  // with step j of this unit
+        ok = false;
+        left = steps - (unit - group) / kGroups * kUnit - j;
+      };
       const uint32_t slot = ring + r.slot * kUnitBytes;
-      const bool there = ring_wait<false>(full + 8 * r.slot, r.phase, failed, kDrainCycles);
-      ok = __all_sync(0xffffffffu, there) && ok;
+      const bool there = ring_wait<false, true>(full + 8 * r.slot, r.phase, failed, p.wait_limit);
+      if (!__all_sync(0xffffffffu, there)) {
+        give_up_at(0);
+        break;
+      }
       uint4 w[kUnit][2];
 #pragma unroll
       for (int j = 0; j < kUnit; ++j)  // (behind the last step: not used)
@@ -225,17 +250,24 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
         for (int h = 0; h < 2; ++h)
           w[j][h] = load_shared16(slot + codes_at + j * kStepBytes + h * (kTileRows * 16));
       convert(w[0], 0);
-      if (under != 0) add(under);
+      if (under != 0 && !add(under)) {
+        give_up_at(0);
+        break;
+      }
       multiply(slot, 0, under != 0);
       under = slot + scales_at;
       if (unit * kUnit + 1 < p.steps) {
         convert(w[1], 1);
-        add(under);
+        if (!add(under)) {
+          give_up_at(1);
+          break;
+        }
         multiply(slot + kXBytes, 1, false);
         under += kStepBytes;
       }
     }
-    if (under != 0) add(under);
+    if (ok && under != 0) ok = add(under);
+    for (tmem_st_wait(); left > 0; --left, barrier ^= 1) group_wait(barrier);
     // the sums of one group on to those of the others
     const float nan = __uint_as_float(0x7FC00000u);
     float* mine = part + row;
@@ -255,13 +287,16 @@ __global__ void __launch_bounds__(kTmemThreads, 1)
     write_products<kGated, kTileRows>(p.a, part, block, static_cast<int>(threadIdx.x),
                                       kTmemThreads, 1);
   }
-  if (!ok && warp % 4 == 0)  // copies in flight land before the CTA ends
-    for (int i = std::max(0, fetched - kRing); i < fetched; ++i) {
-      const long long t0 = clock64();
-      while (!mbar_try_wait(full + 8 * (i % kRing), i / kRing & 1) &&
-             clock64() - t0 < kDrainCycles) {
-      }
-    }
+  // Copies and MMAs in flight are over before the CTA ends. (Where no wait gave up all
+  // were waited for, and from then on no more are copied.)
+  if (!ok && warp % 4 == 0)
+    for (int i = max(0, fetched - kRing); i < fetched; ++i)
+      drain<false>(full + 8 * (i % kRing), i / kRing & 1);
+  if (!ok && warp % 4 < kUnit && elect_one()) {
+    tc_commit(idle + 8 * (warp % 4));  // of this thread's MMAs
+    drain<false>(idle + 8 * (warp % 4), 0);
+  }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -278,6 +313,7 @@ cudaError_t launch_linear_tmem(const ProductArgs& args, int sms, cudaStream_t st
     return cudaErrorInvalidValue;
   p.a = args;
   p.sixteens = 0x41804180u;
+  p.wait_limit = wait_timeout_cycles();
   p.blocks = ceil_div(args.n, kTileRows);
   p.steps = ceil_div(args.k, kKStep);
   static Devices known[2];
