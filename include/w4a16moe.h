@@ -382,8 +382,8 @@ w4a16_status w4a16_silu_and_mul(const uint16_t* in, int rows, int inter, uint16_
  * output is incomplete). *detail (optional) receives the raw word:
  * 0x1000 | code of the wait that gave up.
  * The bound, in SM clock cycles, is read from the environment variable
- * W4A16_WAIT_TIMEOUT_CYCLES at each GEMM call (default 2e9); lowering it
- * makes the failure path testable without any GPU fault.
+ * W4A16_WAIT_TIMEOUT_CYCLES at each call of a GEMM or a product (default 2e9);
+ * lowering it makes the failure path testable without any GPU fault.
  */
 w4a16_status w4a16_read_device_status(void* workspace, int* detail, void* stream);
 
@@ -581,7 +581,8 @@ w4a16_status w4a16_linear_few_tokens(const void* packed, int layout, int n, int 
  * layers of a model), for any number of tokens:
  *   out[t, r] = addend[t, r] + x[t] . weight[r]^T              (gated == 0)
  *   out[t, i] = silu(x[t] . weight[i]^T) * (x[t] . weight[n/2 + i]^T)  (gated != 0)
- * FP32 sums, one rounding of the result.
+ * FP32 sums, one rounding of the result. A device-side wait that gives up
+ * (W4A16_WAIT_TIMEOUT_CYCLES, about a second) leaves NaN in the outputs that waited.
  *   weight  BF16 [n, k]; gated: n/2 gate rows, then n/2 up rows;
  *   x       BF16 [tokens, k], row stride x_stride elements;
  *   addend  FP32 [tokens, n] or NULL (gated: NULL);

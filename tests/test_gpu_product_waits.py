@@ -43,3 +43,20 @@ def test_waits_that_give_up_end_the_call_in_order(cuda_dev, monkeypatch, kind, t
         again = weight(x, out_dtype=want.dtype)   # right behind it, on the same SMs
         out.check(f"limit {limit}")
         assert torch.equal(again, want)
+
+
+@pytest.mark.parametrize("kind,tokens,n,k,gated,f32", CASES)
+def test_outputs_are_nan_once_a_wait_gave_up(cuda_dev, monkeypatch, kind, tokens, n, k, gated, f32):
+    # (the accumulators hold sums of other calls by then, which must not come out)
+    weight, x, want, out = _case(cuda_dev, kind, tokens, n, k, gated, f32)
+    other = weight(-2 * x, out_dtype=want.dtype)
+    for limit in (1, 500, 3000, 10000):
+        out.t.copy_(other)
+        monkeypatch.setenv("W4A16_WAIT_TIMEOUT_CYCLES", str(limit))
+        weight(x, out=out.t)
+        monkeypatch.delenv("W4A16_WAIT_TIMEOUT_CYCLES")
+        gone = torch.isnan(out.t)
+        wrong = ~gone & (out.t != want)
+        assert not wrong.any(), (limit, int(wrong.sum()), int(gone.sum()), out.t.numel())
+        if limit == 1:
+            assert gone.any()

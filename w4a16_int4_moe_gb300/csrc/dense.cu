@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
     const bool ahead = p.a.addend != nullptr && p.columns % 4 == 0;
     const int runs = (p.k_steps + p.run - 1) / p.run;
     Ring acc;
+    bool ok = true;  // (for good: an accumulator's last phase but one looks like its next)
     for (int tile = cluster; tile < tiles; tile += clusters) {
       int m, n;
       place(tile, &m, &n);
@@ -237,7 +238,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       fetch(0);
       fetch(1);
       float sum[kGroups][16];
-      bool ok = true;
       for (int run = 0; run < runs; ++run) {
         const bool there = ring_wait<true>(summed + 8 * acc.slot, acc.phase, failed, p.wait_limit);
         ok = __all_sync(0xffffffffu, there) && ok;
