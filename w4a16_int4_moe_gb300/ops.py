@@ -652,7 +652,7 @@ def w4a16_linear_few_tokens(x: torch.Tensor, packed: torch.Tensor, n: int,
     packed INT4 weight [n, k] (w4a16_prepack of one expert), or, with
     W4A16_LAYOUT_KTILE64_GLU16, silu(x . Wgate^T) * (x . Wup^T), [T, n/2].
     x BF16 [T, k], rows may be strided. out (or out_dtype): FP32 or BF16; out may
-    be addend."""
+    be addend. A blob of another size than [n, k] has is refused."""
     fn = "w4a16_linear_few_tokens"
     device = x.get_device()
     if device < 0 or device != _current_device():
@@ -661,8 +661,12 @@ def w4a16_linear_few_tokens(x: torch.Tensor, packed: torch.Tensor, n: int,
     if x.dim() != 2:
         _refuse(fn, f"x {tuple(x.shape)}")
     tokens, k = x.shape
-    # 128-row tiles of 64-column steps, 4608 bytes each
-    at = _blob(fn, "packed", packed, -(-n // 128) * -(-k // 64) * 4608)
+    # 128-row tiles of 64-column steps, 4608 bytes each; with rows that have more or
+    # fewer columns than the weight the tiles would be sought at other places
+    size = -(-n // 128) * -(-k // 64) * 4608
+    at = _blob(fn, "packed", packed, size)
+    if packed.numel() != size:
+        _refuse(fn, f"packed: {packed.numel()} bytes, a weight [{n}, {k}] has {size}")
     if packed.get_device() != device:
         _refuse(fn, f"x on {x.device}, packed on {packed.device}")
     return _product(fn, load_library().w4a16_linear_few_tokens, x, device, tokens, k,
