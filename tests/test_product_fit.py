@@ -47,3 +47,45 @@ def test_a_blob_of_another_weight_is_refused(on_device_0):
         with pytest.raises(ops.W4A16Error) as e:
             _call(n, k, blob, layout)
         assert e.value.status == INV, (n, k, blob)
+
+
+# Shared experts of 96 columns, of which 64 are as many steps of a blob, for 8 and (the
+# GEMM path) for 40 tokens.
+
+def _expert(max_tokens):
+    from w4a16_int4_moe_gb300 import moe
+    blob = torch.zeros(16, dtype=torch.uint8)
+    expert = moe.PackedSharedExpert(moe.PackedExperts(blob, 1, 128, 96, GLU),
+                                    moe.PackedExperts(blob, 1, 96, 64), min(max_tokens, 32))
+    expert.max_tokens = max_tokens
+    return expert
+
+
+class Reached(Exception):
+    pass
+
+
+class Layer:
+    """Stands for the routed experts' path."""
+    def align(self, ids, stream=None):
+        raise Reached
+
+
+@pytest.mark.parametrize("tokens", [8, 40])
+def test_rows_that_are_not_the_packed_shared_experts_are_refused(lib, monkeypatch, tokens):
+    def product(*a, **kw):
+        raise Reached
+    monkeypatch.setattr(ops, "w4a16_linear_few_tokens", product)
+    expert = _expert(tokens)
+    expert.layer, expert.ids = Layer(), torch.zeros(tokens, 1, dtype=torch.int32)
+    with pytest.raises(Reached):
+        expert.forward(torch.zeros(tokens, 96, dtype=BF))
+    rows = torch.zeros(tokens, 96, dtype=BF)
+    for x in (rows[:, :64], rows.float(), rows[0], rows[:, None], torch.zeros(tokens, 128, dtype=BF)):
+        with pytest.raises(ValueError):
+            expert.forward(x)
+    if tokens > ops.W4A16_FEW_TOKENS_MAX:   # (the few-token product checks its output itself)
+        out = torch.zeros(tokens, 96)
+        for o in (out[:, :64], out[1:], out.to(BF), torch.zeros(tokens, 192)[:, :96]):
+            with pytest.raises(ValueError):
+                expert.forward(rows, out=o)

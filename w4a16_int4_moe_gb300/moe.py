@@ -343,6 +343,8 @@ class PackedSharedExpert:
         if add and out is None:
             raise ValueError("add needs what it adds to")
         tokens = x.shape[0]
+        if x.dtype is not torch.bfloat16 or x.shape != (tokens, self.hidden):
+            raise ValueError(f"x: {x.dtype} {tuple(x.shape)}, not BF16 rows of {self.hidden}")
         if tokens > self.max_tokens:
             raise ValueError("more tokens than the expert was planned for")
         if tokens <= ops.W4A16_FEW_TOKENS_MAX:
@@ -351,6 +353,10 @@ class PackedSharedExpert:
             return ops.w4a16_linear_few_tokens(act, self.down.packed, self.down.n,
                                                addend=out if add else None,
                                                out_dtype=torch.float32, out=out, stream=stream)
+        if out is not None and (out.dtype is not torch.float32 or out.shape != x.shape
+                                or out.device != x.device or not out.is_contiguous()):
+            raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, "
+                             f"not contiguous FP32 {tuple(x.shape)}")
         layer = self.layer
         layer.align(self.ids[:tokens], stream)
         layer.gate_up_act(x, tokens, stream)
