@@ -89,3 +89,22 @@ def test_rows_that_are_not_the_packed_shared_experts_are_refused(lib, monkeypatc
         for o in (out[:, :64], out[1:], out.to(BF), torch.zeros(tokens, 192)[:, :96]):
             with pytest.raises(ValueError):
                 expert.forward(rows, out=o)
+
+
+def test_strided_rows_reach_the_gemm_path_as_rows_in_line(lib, monkeypatch):
+    expert = _expert(40)
+    seen = []
+
+    class Seen(Layer):
+        def align(self, ids, stream=None):
+            pass
+
+        def gate_up_act(self, x, tokens, stream=None):
+            seen.append(x)
+            raise Reached
+    expert.layer, expert.ids = Seen(), torch.zeros(40, 1, dtype=torch.int32)
+    wide = torch.randn(40, 200).to(BF)
+    for x in (wide[:, 8:104], wide[:, :96], torch.randn(96, 40).to(BF).t()):
+        with pytest.raises(Reached):
+            expert.forward(x)
+        assert seen[-1].is_contiguous() and torch.equal(seen[-1], x)

@@ -339,7 +339,8 @@ class PackedSharedExpert:
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, add: bool = False,
                 stream=None) -> torch.Tensor:
-        """x BF16 [T, H] -> fp32 [T, H]; add: onto what out holds."""
+        """x BF16 [T, H] (rows that are strided are copied where the GEMM path runs)
+        -> fp32 [T, H]; add: onto what out holds."""
         if add and out is None:
             raise ValueError("add needs what it adds to")
         tokens = x.shape[0]
@@ -357,6 +358,9 @@ class PackedSharedExpert:
                                 or out.device != x.device or not out.is_contiguous()):
             raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, "
                              f"not contiguous FP32 {tuple(x.shape)}")
+        if not x.is_contiguous():   # (the GEMM path reads rows in line)
+            with ops.on_stream(stream):
+                x = x.contiguous()
         layer = self.layer
         layer.align(self.ids[:tokens], stream)
         layer.gate_up_act(x, tokens, stream)
