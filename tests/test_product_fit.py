@@ -108,3 +108,36 @@ def test_strided_rows_reach_the_gemm_path_as_rows_in_line(lib, monkeypatch):
         with pytest.raises(Reached):
             expert.forward(x)
         assert seen[-1].is_contiguous() and torch.equal(seen[-1], x)
+
+
+def test_the_gemm_path_runs_on_the_rows_device(lib, monkeypatch):
+    current = [0]
+    monkeypatch.setattr(ops, "_current_device", lambda: current[0])
+
+    class device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.d
+
+        def __exit__(self, *a):
+            current[0] = self.before
+    monkeypatch.setattr(torch.cuda, "device", device)
+    expert = _expert(40)
+    seen = []
+
+    class Seen(Layer):
+        def align(self, ids, stream=None):
+            seen.append(current[0])
+            raise Reached
+    expert.layer, expert.ids = Seen(), torch.zeros(40, 1, dtype=torch.int32)
+    expert.gate_up.packed = Bytes(1, (16,))
+    x = Placed(1, (40, 96))
+    with pytest.raises(Reached):
+        expert.forward(x)
+    assert seen == [1] and current == [0]
+    expert.gate_up.packed = Bytes(0, (16,))     # the weights are elsewhere
+    with pytest.raises(ValueError):
+        expert.forward(x)
+    assert seen == [1] and current == [0]

@@ -358,6 +358,11 @@ class PackedSharedExpert:
                                 or out.device != x.device or not out.is_contiguous()):
             raise ValueError(f"out: {out.dtype} {tuple(out.shape)} on {out.device}, "
                              f"not contiguous FP32 {tuple(x.shape)}")
+        if x.device != self.gate_up.packed.device:
+            raise ValueError(f"x on {x.device}, weights on {self.gate_up.packed.device}")
+        if x.is_cuda and x.get_device() != ops._current_device():
+            with torch.cuda.device(x.get_device()):   # (where the GEMM path launches)
+                return self.forward(x, out, add, stream)
         if not x.is_contiguous():   # (the GEMM path reads rows in line)
             with ops.on_stream(stream):
                 x = x.contiguous()
