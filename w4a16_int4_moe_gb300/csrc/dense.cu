@@ -17,6 +17,7 @@
 #include "internal.h"
 #include "pipe.cuh"
 #include "ptx.cuh"
+#include "silu.cuh"
 
 namespace w4a16 {
 
@@ -83,10 +84,6 @@ __device__ __forceinline__ void take_sums(float (&sum)[kGroups][16], bool fresh,
 // that both a column of rows and a row meet all banks.
 __device__ __forceinline__ int tile_at(int row, int quad) {
   return row * kChunk + ((quad ^ (row & 7)) << 2);
-}
-
-__device__ __forceinline__ float silu_times(float gate, float up) {
-  return __fdividef(gate, 1.f + __expf(-gate)) * up;
 }
 
 // Four adjacent output values of a token, the columns from c on.

@@ -6,6 +6,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "silu.cuh"
 
 namespace w4a16 {
 
@@ -74,8 +75,7 @@ __device__ __forceinline__ void write_products(const ProductArgs& a, const float
     float v;
     if constexpr (kGated) {
       const int row = c / 16 * 32 + c % 16;
-      const float gate = sum(row);
-      v = gate / (1.f + expf(-gate)) * sum(row + 16);
+      v = silu_times(sum(row), sum(row + 16));
     } else {
       v = sum(c);
     }

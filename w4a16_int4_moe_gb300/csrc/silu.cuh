@@ -1,0 +1,20 @@
+// silu.cuh -- the gated products' way out.
+#pragma once
+
+namespace w4a16 {
+
+namespace {
+
+// silu(gate) * up = gate / (1 + e^-gate) * up to within 8 steps of FP32 for any finite
+// gate. With e = e^(-|gate| / 2) no part of it leaves FP32's range before the result
+// does: e^-gate is past it for gates below -88, where silu is -1e-37 and an up may
+// be large. (The divisor is 1 to 2, where the quick division is off by two steps.)
+__device__ __forceinline__ float silu_times(float gate, float up) {
+  const float e = expf(-0.5f * fabsf(gate));
+  const float f = gate < 0.f ? e : 1.f;
+  return __fdividef(gate * f, fmaf(e, e, 1.f)) * (up * f);
+}
+
+}  // namespace
+
+}  // namespace w4a16
