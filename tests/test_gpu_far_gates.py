@@ -24,12 +24,17 @@ def _check(out, gate, up):
     # Steps of 2^-23, from the units in the last place that CUDA states for each
     # operation: the exponential 1; its square, one more and the sum 1.75; the division
     # 2; gate and up times the exponential 1.5 each; the last product 0.5. A result
-    # below FP32's normal range is off by a step of its own besides.
+    # below FP32's normal range is off by a step of its own besides. Where the result is
+    # rounded to BF16 and the gate is at least -80, 2^-16: the exponent is at most 116
+    # and rounded once, and its factor to 2^-26: 116 * (2^-24 + 2^-26) * ln 2 = 2^-17.3;
+    # exponential, sum, reciprocal and two products take 2^-21.
     g, u = gate.double(), up.double()
     want = (g * torch.sigmoid(g) * u).expand(out.shape[0], -1)
     bound = 8 * ref.STEP * want.abs() + 2.0 ** -149
     if out.dtype is BF:
-        bound = bound + (want.abs() + bound) * ref.BF16_HALF
+        bound = torch.where(g < -80, bound, 2.0 ** -16 * want.abs())
+        # (below its normal range BF16's steps are 2^-133, and a rounding half of one)
+        bound = bound + (want.abs() + bound) * ref.BF16_HALF + 2.0 ** -134
     ref.assert_within(out, want, bound)
 
 
@@ -43,6 +48,20 @@ def test_dense(cuda_dev, dtype, tokens, columns):
     x = torch.zeros(tokens, 72, dtype=BF, device=cuda_dev)
     x[:, 3] = 1
     _check(ops.w4a16_dense(x, weight, gated=True, out_dtype=dtype), gate, up)
+
+
+def test_whole_tiles_of_near_and_of_far_gates(cuda_dev):
+    # each 64 columns in another range, so that some warps have no far gate and some only such
+    columns = 4096
+    gate = torch.cat([torch.linspace(a, a + 16, 64, device=cuda_dev)
+                      for a in range(-140, 116, 4)]).to(BF)
+    up = (2.0 ** (20 + torch.arange(columns, device=cuda_dev) % 32)).to(BF)
+    weight = torch.zeros(2 * columns, 72, dtype=BF, device=cuda_dev)
+    weight[:columns, 3], weight[columns:, 3] = gate, up
+    x = torch.zeros(1000, 72, dtype=BF, device=cuda_dev)
+    x[:, 3] = 1
+    for dtype in (BF, F32):
+        _check(ops.w4a16_dense(x, weight, gated=True, out_dtype=dtype), gate, up)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])

@@ -255,6 +255,24 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 #pragma unroll
       for (int c = 0; c < kGroups / 2; ++c) {
         if (c * kChunk >= cols) break;
+        if (c < kGroups / 4 && p.a.gated) {
+          float least = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) least = fminf(least, sum[2 * c + i / 16][i % 16]);
+          // (8192 tokens of 8192 x 512: 73 us with the quick form, 81 with the other)
+          const bool quick = !p.a.f32_out && !__any_sync(0xffffffffu, least < kQuickGate);
+          const auto gated = [&](auto form) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float& v = sum[2 * c + i / 16][i % 16];
+              v = form(v, sum[(2 * c + i / 16 + kGroups / 2) % kGroups][i % 16]);
+            }
+          };
+          if (quick)
+            gated([](float g, float u) { return silu_times_quick(g, u); });
+          else
+            gated([](float g, float u) { return silu_times(g, u); });
+        }
         float* here = tiles_at + (c & 1) * (32 * kChunk);
         copies_wait<1>();
         __syncwarp();
@@ -262,12 +280,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         for (int i = 0; i < 8; ++i) {
           float v[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int g = 2 * c + i / 4, at = i % 4 * 4 + j;
-            v[j] = sum[g][at];
-            if (c < kGroups / 4 && p.a.gated)
-              v[j] = silu_times(v[j], sum[(g + kGroups / 2) % kGroups][at]);
-          }
+          for (int j = 0; j < 4; ++j) v[j] = sum[2 * c + i / 4][i % 4 * 4 + j];
           float4* at4 = reinterpret_cast<float4*>(here + tile_at(lane, i));
           float4 out = make_float4(v[0], v[1], v[2], v[3]);
           if (ahead) out = add4(out, *at4);
