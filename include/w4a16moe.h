@@ -581,7 +581,9 @@ w4a16_status w4a16_linear_few_tokens(const void* packed, int layout, int n, int 
  * layers of a model), for any number of tokens:
  *   out[t, r] = addend[t, r] + x[t] . weight[r]^T              (gated == 0)
  *   out[t, i] = silu(x[t] . weight[i]^T) * (x[t] . weight[n/2 + i]^T)  (gated != 0)
- * FP32 sums, one rounding of the result. A device-side wait that gives up
+ * FP32 sums, one rounding of the result. (The tensor core, which cuts off where a
+ * plain sum would round, keeps them for at most 512 columns, 1024 for BF16
+ * outputs; then they are added to sums outside.) A device-side wait that gives up
  * (W4A16_WAIT_TIMEOUT_CYCLES, about a second) leaves NaN in the outputs that waited.
  *   weight  BF16 [n, k]; gated: n/2 gate rows, then n/2 up rows;
  *   x       BF16 [tokens, k], row stride x_stride elements;

@@ -29,11 +29,15 @@ constexpr int kWarpCopy = kSumWarps, kWarpMma = kSumWarps + 1;
 constexpr int kDenseThreads = 32 * (kSumWarps + 4);  // whole warpgroups: two warps do nothing
 constexpr int kMaxSlots = 8;
 // The tensor core cuts its running sums off instead of rounding them: 1.5e-6 of an
-// FP32 output after the 128 additions that 2048 columns are. So for those an
-// accumulator's sums go after 512 columns to FP32 sums in registers: 3.4e-7 (a plain
-// FP32 product: 2.8e-7), for 169 instead of 146 us of 8192 x 2048 x 7168; after
-// 256 columns 1.7e-7 and 183 us.
-constexpr int kRun = 8;
+// FP32 output after the 128 additions that 2048 columns are, and more with every
+// column. So an accumulator's sums go to FP32 sums in registers, for FP32 outputs
+// after 512 columns: 3.4e-7 (a plain FP32 product: 2.8e-7), for 169 instead of 146 us
+// of 8192 x 2048 x 7168; after 256 columns 1.7e-7 and 183 us. For BF16 outputs, which
+// it moves over a border now and then, after 1024: 576 tokens of 4096 x 7168 gated
+// are 2.9e-4 off the rounded 64-bit result with one accumulator, 1.2e-4 with 2048
+// columns, 0.9e-4 with 1024 and 0.6e-4 with 512, which take 36.6, 36.6, 36.6 and 36.8
+// us; 8192 x 2048 x 7168 150, 150, 150 and 170.
+constexpr int kRun = 8, kRunRounded = 16;
 constexpr int kChunk = 32;       // output columns of an epilogue warp at a time
 constexpr int kTileBytes = 32 * kChunk * 4;  // of its 32 tokens
 constexpr int kTilesBytes = kSumWarps * 2 * kTileBytes;
@@ -649,7 +653,11 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
     c.out_cols = a.gated ? c.half : tile_n;
     c.n_tiles = ceil_div(columns, c.out_cols);
     c.k_steps = steps;
-    c.run = a.f32_out ? kRun : steps;
+    // (BF16 results: equal runs, 17 steps as 9 and 8)
+    const auto run = [&](int n) {
+      return a.f32_out ? kRun : ceil_div(n, ceil_div(n, kRunRounded));
+    };
+    c.run = run(steps);
     const double gate = a.gated ? tile_n * 0.01 : 0;
 
     c.m_tiles = ceil_div(a.tokens, 2 * kTileM);
@@ -668,6 +676,7 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
       if (static_cast<long long>(c.m_tiles) * c.n_tiles * c.split > 0x7fffffffLL) break;
       const double waves = std::ceil(static_cast<double>(c.m_tiles) * c.n_tiles /
                                      split_clusters_at_once(c.split, sms, device, error));
+      c.run = run(ceil_div(steps, c.split));
       const double sums = rows / kTileM * (1 + tile_n * 0.012 + gate) / (c.split > 1 ? 1.5 : 1);
       consider(c, false, waves * (ceil_div(steps, c.split) * (0.07 + tile_n * 0.00125) + 4.5 +
                                   (c.split > 1 ? 1.5 : 0) + sums));
