@@ -204,12 +204,15 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
 #pragma unroll
       for (int j = 0; j < kMt / 2; ++j) ldmatrix_x4_trans(scales + j * 64, sc[j]);
     }
+    uint4 x[2][kNt];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 x[kNt];
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) x[nt] = load_shared16(slot + x_row[nt][h]);
-      if constexpr (kInt4) {
+      for (int nt = 0; nt < kNt; ++nt) x[h][nt] = load_shared16(slot + x_row[nt][h]);
+    const float none[4] = {};
+    if constexpr (kInt4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < kMt / 2; ++j) {
           uint32_t w[4];
@@ -225,26 +228,37 @@ __global__ void __launch_bounds__(kWarps * 32) w4a16_product_few_kernel(const Fe
             const float s0 = __uint_as_float(pair << 16), s1 = __uint_as_float(pair & 0xFFFF0000u);
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt) {
-              const float none[4] = {};
               float c[4];
-              mma16816(c, a0, x[nt].x, x[nt].y, none);
-              mma16816(c, a1, x[nt].z, x[nt].w, c);
+              mma16816(c, a0, x[h][nt].x, x[h][nt].y, none);
+              mma16816(c, a1, x[h][nt].z, x[h][nt].w, c);
               fma_pair(acc[mt][nt][0], acc[mt][nt][1], s0, c[0], c[1]);
               fma_pair(acc[mt][nt][2], acc[mt][nt][3], s1, c[2], c[3]);
             }
           }
         }
-      } else {
+    } else {
+      // (a step's sum of its own: the tensor core cuts off at every addition, over a
+      // warp's share of 7168 columns 8.6e-7 of the result)
 #pragma unroll
-        for (int mt = 0; mt < kMt; ++mt) {
+      for (int mt = 0; mt < kMt; ++mt) {
+        uint32_t w[2][2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           const uint32_t at = slot + mt * 2048 + chunk_at(g, 4 * h + t);
           const uint4 w0 = load_shared16(at), w1 = load_shared16(at + 8 * 128);
           const uint32_t a0[4] = {w0.x, w1.x, w0.y, w1.y}, a1[4] = {w0.z, w1.z, w0.w, w1.w};
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            mma16816(acc[mt][nt], a0, x[nt].x, x[nt].y, acc[mt][nt]);
-            mma16816(acc[mt][nt], a1, x[nt].z, x[nt].w, acc[mt][nt]);
-          }
+          for (int i = 0; i < 4; ++i) w[h][0][i] = a0[i], w[h][1][i] = a1[i];
+        }
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) {
+          float c[4];
+          mma16816(c, w[0][0], x[0][nt].x, x[0][nt].y, none);
+          mma16816(c, w[0][1], x[0][nt].z, x[0][nt].w, c);
+          mma16816(c, w[1][0], x[1][nt].x, x[1][nt].y, c);
+          mma16816(c, w[1][1], x[1][nt].z, x[1][nt].w, c);
+          fma_pair(acc[mt][nt][0], acc[mt][nt][1], 1.f, c[0], c[1]);
+          fma_pair(acc[mt][nt][2], acc[mt][nt][3], 1.f, c[2], c[3]);
         }
       }
     }
