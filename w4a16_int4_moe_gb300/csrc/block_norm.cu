@@ -158,13 +158,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) w4a16_block_norm_kernel(const
 
 namespace {
 
-// Threads and chunks of a row: as few lanes without columns as can be, and
+// Threads and chunks of a row:
 //   * up to a row an SM: two chunks of up to 512 threads (152 rows of 7168: 4.3
 //     us on 448 x 2, 5.0 on 128 x 7);
-//   * more rows: seven chunks of 128 threads, three such rows an SM (8192 rows of
-//     7168: 88 us on 128 x 7, 99 on 448 x 2 or 256 x 4, which are two rows; 8192 of
-//     8192: 102 on 128 x 8, 160 on 512 x 2); longer rows 256 x 5 and 256 x 6 in
-//     128 registers, two rows an SM (8192 of 12288: 148 us, 203 with one);
+//   * more rows: chunks of 128 threads, of seven chunks three such rows an SM (8192
+//     rows of 7168: 88 us on 128 x 7, 99 on 448 x 2 or 256 x 4, which are two rows;
+//     8192 of 8192: 102 on 128 x 8, 160 on 512 x 2); longer rows 256 x 5 and 256 x 6
+//     in 128 registers, two rows an SM (8192 of 12288: 148 us, 203 with one);
+//   * of those, rows of up to three chunks take 96 threads where that leaves fewer
+//     lanes without columns (8192 rows of 768: 13.4 us on 96 x 1, 15.5 on 128 x 1; of
+//     1032 20.4 and 23.6, 1536 24.0 and 26.7, 2088 37.0 and 41.5; 300 to 2000 rows
+//     from 6 % less to 2 % more). With more chunks it may cost more than the lanes
+//     are worth: 8192 rows of 3840 64.8 and 60.5, of 5376 134 and 92;
 //   * behind those 512 x 4, one row an SM (8192 of 16384: 231 us, 256 x 8 256).
 template <bool kX32>
 cudaError_t launch(const BlockNormArgs& args, int sms, cudaStream_t stream) {
@@ -173,6 +178,7 @@ cudaError_t launch(const BlockNormArgs& args, int sms, cudaStream_t stream) {
     return launch_dependent(kernel, args.rows, threads, 0, 1, stream, args);
   };
   if (need <= 32) return run(w4a16_block_norm_kernel<kX32, 32, 1, 1>, 32);
+  if (args.rows > sms && need <= 96) return run(w4a16_block_norm_kernel<kX32, 96, 1, 1>, 96);
   if (need <= 128) return run(w4a16_block_norm_kernel<kX32, 128, 1, 1>, 128);
   if (args.rows <= sms) {
     if (need <= 256) return run(w4a16_block_norm_kernel<kX32, 256, 1, 1>, 256);
@@ -183,6 +189,7 @@ cudaError_t launch(const BlockNormArgs& args, int sms, cudaStream_t stream) {
     if (need <= 896) return run(w4a16_block_norm_kernel<kX32, 448, 2, 1>, 448);
     if (need <= 1024) return run(w4a16_block_norm_kernel<kX32, 512, 2, 1>, 512);
   } else {
+    if (need <= 192) return run(w4a16_block_norm_kernel<kX32, 96, 2, 1>, 96);
     if (need <= 256) return run(w4a16_block_norm_kernel<kX32, 128, 2, 1>, 128);
     if (need <= 288) return run(w4a16_block_norm_kernel<kX32, 96, 3, 1>, 96);
     if (need <= 384) return run(w4a16_block_norm_kernel<kX32, 128, 3, 1>, 128);
