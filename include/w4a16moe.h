@@ -601,6 +601,22 @@ w4a16_status w4a16_dense(const uint16_t* weight, int n, int k, int gated, const 
                          int out_dtype, void* stream);
 
 /*
+ * How w4a16_dense runs a product. Calls of the same sizes with the same info add in
+ * the same order.
+ *   at_once  how many pairs of CTAs, and clusters of 1, 2, 4 and 8 CTAs, a device
+ *            runs at once (five numbers above 0), or NULL: the current device's.
+ * Sizes as w4a16_dense takes them. Host only with at_once given.
+ */
+typedef struct {
+  int kernel;     /* 0 up to 32 tokens (the other fields 0), 1 clusters that split k, 2 pairs */
+  int tile_rows;  /* weight rows of a tile, half of them gate and half up rows if gated */
+  int split;      /* CTAs that share a tile's columns of x */
+  int run;        /* columns at most that the tensor core adds up before they are taken over */
+} w4a16_dense_info_t;
+w4a16_status w4a16_dense_info(int n, int k, int gated, int tokens, int out_dtype,
+                              const int* at_once, w4a16_dense_info_t* info);
+
+/*
  * What stands between a block (the experts) and the next one: the norm of the
  * block's output, its gate and scales, the residual, the next block's norm.
  *   p = x * rsqrt(mean(x^2) + eps) * (post_weight + weight_offset)

@@ -976,6 +976,33 @@ w4a16_status w4a16_dense(const uint16_t* weight, int n, int k, int gated, const 
   return cuda_status(launch_dense(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
+w4a16_status w4a16_dense_info(int n, int k, int gated, int tokens, int out_dtype,
+                              const int* at_once, w4a16_dense_info_t* info) {
+  if (n <= 0 || k <= 0 || tokens < 0 || info == nullptr) return W4A16_ERR_INVALID_ARG;
+  if (out_dtype != W4A16_DTYPE_F32 && out_dtype != W4A16_DTYPE_BF16) return W4A16_ERR_INVALID_ARG;
+  if (k % 8 != 0 || n > kProductMaxSize || k > kProductMaxSize || tokens > kDenseMaxTokens ||
+      (gated != 0 && n % 2 != 0))
+    return W4A16_ERR_UNSUPPORTED;
+  DenseRoom room = {};
+  if (at_once != nullptr) {
+    room.pairs = at_once[0];
+    for (int i = 1; i < 5; ++i) {
+      room.clusters[1 << (i - 1)] = at_once[i];
+      if (at_once[i] <= 0) return W4A16_ERR_INVALID_ARG;
+    }
+    if (room.pairs <= 0) return W4A16_ERR_INVALID_ARG;
+  } else {
+    const int sms = current_sm_count();
+    if (sms <= 0 || dense_room(sms, &room) != cudaSuccess) return W4A16_ERR_CUDA;
+  }
+  ProductArgs a = {};
+  a.n = n, a.k = k, a.gated = gated != 0, a.tokens = tokens;
+  a.f32_out = out_dtype == W4A16_DTYPE_F32;
+  const DenseShape s = dense_choice(a, room);
+  *info = {s.kernel, s.tile_rows, s.split, s.run};
+  return W4A16_OK;
+}
+
 w4a16_status w4a16_block_norm(const void* x, int x_dtype, long long x_stride,
                               const uint16_t* post_weight, const uint16_t* gate,
                               long long gate_stride, const uint16_t* residual,

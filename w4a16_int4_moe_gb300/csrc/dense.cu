@@ -610,10 +610,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 
 namespace {
 
-constexpr int kMaxSplit = 8;
-
 int split_clusters_at_once(int ctas, int sms, int device, cudaError_t* error) {
-  static ClustersAtOnce known[kMaxSplit + 1];
+  static ClustersAtOnce known[kMaxDenseSplit + 1];
   if (ctas == 1) return sms;
   return std::max(1, clusters_at_once(w4a16_dense_split_kernel, ctas, kDenseThreads, kSmemBytes,
                                       known[ctas], device, error));
@@ -635,7 +633,7 @@ int pairs_at_once(int device, cudaError_t* error) {
 // 41 / 74 us. Pairs take widths in steps of 32 (2048 tokens: 224 rows 68 us, 256 73;
 // 700 tokens, 7168 x 18432: 139 and 159), the split kernel, whose estimate is too low at
 // 224 (400 tokens 31 us, pairs of 128 29), in steps of 64.
-bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cudaError_t* error) {
+bool dense_shape(const ProductArgs& a, const DenseRoom& room, DenseArgs* best) {
   const int columns = a.gated ? a.n / 2 : a.n;
   const int steps = ceil_div(a.k, kKStep);
   double least = 0;
@@ -664,7 +662,7 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
     c.split = 1;
     c.slots = std::min(kMaxSlots, kRingBytes / ((kTileM + c.half) * kKStep * 2));
     const double rounds = std::ceil(static_cast<double>(c.m_tiles) * c.n_tiles /
-                                    pairs_at_once(device, error));
+                                    room.pairs);
     consider(c, true, rounds * std::max(steps * (0.095 + tile_n * 0.00085), 2.0 + tile_n * 0.008) +
                           5 + tile_n * 0.01 + gate);
 
@@ -672,10 +670,10 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
     c.m_tiles = ceil_div(a.tokens, kTileM);
     c.slots = std::min(kMaxSlots, kRingBytes / ((kTileM + tile_n) * kKStep * 2));
     const double rows = std::min(a.tokens, kTileM);
-    for (c.split = 1; c.split <= kMaxSplit && c.split <= steps; c.split *= 2) {
+    for (c.split = 1; c.split <= kMaxDenseSplit && c.split <= steps; c.split *= 2) {
       if (static_cast<long long>(c.m_tiles) * c.n_tiles * c.split > 0x7fffffffLL) break;
       const double waves = std::ceil(static_cast<double>(c.m_tiles) * c.n_tiles /
-                                     split_clusters_at_once(c.split, sms, device, error));
+                                     room.clusters[c.split]);
       c.run = run(ceil_div(steps, c.split));
       const double sums = rows / kTileM * (1 + tile_n * 0.012 + gate) / (c.split > 1 ? 1.5 : 1);
       consider(c, false, waves * (ceil_div(steps, c.split) * (0.07 + tile_n * 0.00125) + 4.5 +
@@ -687,15 +685,31 @@ bool dense_shape(const ProductArgs& a, int sms, int device, DenseArgs* best, cud
 
 }  // namespace
 
-cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) {
-  if (args.tokens <= kDenseFewTokens) return launch_dense_few(args, sms, stream);
+cudaError_t dense_room(int sms, DenseRoom* room) {
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   if (device >= kMaxDevices) return cudaErrorInvalidDevice;
+  room->pairs = pairs_at_once(device, &e);
+  for (int split = 1; split <= kMaxDenseSplit; split *= 2)
+    room->clusters[split] = split_clusters_at_once(split, sms, device, &e);
+  return e;
+}
+
+DenseShape dense_choice(const ProductArgs& args, const DenseRoom& room) {
+  if (args.tokens <= kDenseFewTokens) return {};
   DenseArgs p;
-  const bool pair = dense_shape(args, sms, device, &p, &e);
+  const bool pair = dense_shape(args, room, &p);
+  return {pair ? 2 : 1, 2 * p.half, p.split, p.run * kKStep};
+}
+
+cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) {
+  if (args.tokens <= kDenseFewTokens) return launch_dense_few(args, sms, stream);
+  DenseRoom room;
+  cudaError_t e = dense_room(sms, &room);
   if (e != cudaSuccess) return e;
+  DenseArgs p;
+  const bool pair = dense_shape(args, room, &p);
   p.a = args;
   p.wait_limit = wait_timeout_cycles();
   if (!encode_rows_tmap(&p.x, args.x, args.tokens, args.k, args.x_stride, kTileM) ||
@@ -707,7 +721,7 @@ cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream) 
                  known[pair ? 1 : 0]);
   if (e != cudaSuccess) return e;
   if (pair) {
-    const int clusters = static_cast<int>(std::min<long long>(tiles, pairs_at_once(device, &e)));
+    const int clusters = static_cast<int>(std::min<long long>(tiles, room.pairs));
     return launch_dependent(w4a16_dense_pair_kernel, 2 * clusters, kDenseThreads, kSmemBytes, 2,
                             stream, p);
   }

@@ -350,6 +350,18 @@ cudaError_t launch_linear_tmem(const ProductArgs& args, int sms, cudaStream_t st
 constexpr int kDenseFewTokens = 32;  // launch_dense hands them to launch_dense_few
 cudaError_t launch_dense_few(const ProductArgs& args, int sms, cudaStream_t stream);
 cudaError_t launch_dense(const ProductArgs& args, int sms, cudaStream_t stream);
+// What the current device runs at once of launch_dense's kernels for many tokens:
+// pairs of CTAs, and clusters of 1, 2, 4 and 8 CTAs.
+constexpr int kMaxDenseSplit = 8;
+struct DenseRoom {
+  int pairs, clusters[kMaxDenseSplit + 1];
+};
+cudaError_t dense_room(int sms, DenseRoom* room);
+// What launch_dense takes where it finds that room (w4a16_dense_info_t's fields).
+struct DenseShape {
+  int kernel, tile_rows, split, run;
+};
+DenseShape dense_choice(const ProductArgs& args, const DenseRoom& room);
 
 // The norms after and before a block (block_norm.cu).
 struct BlockNormArgs {

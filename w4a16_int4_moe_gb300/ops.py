@@ -54,6 +54,7 @@ EXPORTED = (
     "w4a16_moe_layer", "w4a16_moe_route_align", "w4a16_grouped_plan", "w4a16_plan_info",
     "w4a16_add_rms_norm", "w4a16_router_logits", "w4a16_moe_few_tokens_workspace_size",
     "w4a16_moe_few_tokens", "w4a16_linear_few_tokens", "w4a16_dense", "w4a16_block_norm",
+    "w4a16_dense_info",
 )
 
 
@@ -75,6 +76,11 @@ class PlanInfo(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class DenseInfo(ctypes.Structure):
+    """w4a16_dense_info_t."""
+    _fields_ = [(name, ctypes.c_int) for name in ("kernel", "tile_rows", "split", "run")]
 
 
 class W4A16Error(RuntimeError):
@@ -138,6 +144,7 @@ def load_library(path: Optional[str] = None):
                                       _P, _P, _P, _I, _P, _Z, _P]),
         "w4a16_linear_few_tokens": (_I, [_P, _I, _I, _I, _P, _L, _I, _P, _P, _I, _P]),
         "w4a16_dense": (_I, [_P, _I, _I, _I, _P, _L, _I, _P, _P, _I, _P]),
+        "w4a16_dense_info": (_I, [_I, _I, _I, _I, _I, _P, _P]),
         "w4a16_block_norm": (_I, [_P, _I, _L, _P, _P, _L, _P, _L, _P, _F, _F, _F, _F, _I, _I, _P,
                                   _P, _P, _P, _I, _P]),
     }
@@ -696,6 +703,18 @@ def w4a16_dense(x: torch.Tensor, weight: torch.Tensor, gated: bool = False,
     return _product(fn, load_library().w4a16_dense, x, device, tokens, k, n // 2 if gated else n,
                     addend, out, out_dtype, stream,
                     _place(fn, "weight", weight, _BF16, size, device), n, k, 1 if gated else 0)
+
+
+def w4a16_dense_info(tokens: int, n: int, k: int, gated: bool = False, out_dtype=torch.bfloat16,
+                     at_once=None) -> DenseInfo:
+    """How w4a16_dense runs this product on the current device, or on one that runs
+    at_once = (pairs, clusters of 1, 2, 4, 8 CTAs) at once."""
+    info = DenseInfo()
+    counts = None if at_once is None else (_I * 5)(*at_once)
+    _check("w4a16_dense_info", load_library().w4a16_dense_info(
+        n, k, 1 if gated else 0, tokens,
+        W4A16_DTYPE_F32 if out_dtype is _F32 else W4A16_DTYPE_BF16, counts, ctypes.byref(info)))
+    return info
 
 
 def w4a16_block_norm(x: torch.Tensor, pre_weight: Optional[torch.Tensor], eps: float = 1e-6,
