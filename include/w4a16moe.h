@@ -475,7 +475,8 @@ w4a16_status w4a16_add_rms_norm(const uint16_t* x, long long x_stride, const uin
 /*
  * The router's product: logits[t, e] = sum over c of x[t, c] * weight[e, c],
  * FP32 accumulation; the logits w4a16_topk_softmax, w4a16_moe_route_align and
- * w4a16_moe_few_tokens take.
+ * w4a16_moe_few_tokens take. A device-side wait that gives up
+ * (W4A16_WAIT_TIMEOUT_CYCLES, about a second) leaves NaN in the logits that waited.
  *   x      BF16 [tokens, hidden], row stride x_stride elements;
  *   weight BF16 [num_experts, hidden]; logits FP32 [tokens, num_experts].
  * hidden a multiple of 8, num_experts at most 1024 (else

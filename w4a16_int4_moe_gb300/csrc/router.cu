@@ -31,6 +31,7 @@
 #include <cmath>
 
 #include "internal.h"
+#include "pipe.cuh"
 #include "ptx.cuh"
 
 namespace w4a16 {
@@ -155,7 +156,6 @@ constexpr int kWarpCopy0 = kSumWarps, kWarpMma0 = kSumWarps + kDensePairs;
 // hands its accumulator to the epilogue warps, which add it to FP32 sums in
 // registers, and begins at zero: 4.8e-7, for 2 us of 50.
 constexpr int kChunk = 8;  // times kKStep columns
-constexpr long long kGiveUpCycles = 4000000000LL;  // about two seconds
 
 struct DenseArgs {
   CUtensorMap x, weight;
@@ -163,6 +163,7 @@ struct DenseArgs {
   int tokens, num_experts;
   int k_steps, sub;  // steps of sub * kKStep columns
   int tile_n, b_rows, n_tiles, split, slots, tmem_cols;
+  long long wait_limit;  // cycles
 };
 
 // Ring slots, a multiple of the threads that take turns: each slot then belongs
@@ -187,20 +188,6 @@ size_t dense_smem(const DenseArgs& a) {
   return 2048 + std::max(ring, sums);
 }
 
-// kRemote: threads of the other CTA of a pair arrive as well.
-template <bool kRemote = false>
-__device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
-  const long long t0 = clock64();
-  while (!(kRemote ? mbar_try_wait_cluster_now(bar, parity) : mbar_try_wait(bar, parity))) {
-    if (*failed) return false;
-    if (clock64() - t0 > kGiveUpCycles) {
-      *failed = 1;
-      return false;
-    }
-  }
-  return true;
-}
-
 }  // namespace
 
 // kPair: two CTAs multiply a tile of 256 tokens together. Each copies its own
@@ -209,7 +196,7 @@ __device__ __forceinline__ bool dense_wait(uint32_t bar, uint32_t parity, volati
 // every CTA keeps the sums of its tokens. Otherwise a tile has 128 tokens and
 // one CTA. a.split CTAs or pairs of a cluster share a tile by its columns.
 // A wait that gives up (none does unless the hardware fails) ends the CTA's
-// work in order and leaves NaN in its logits.
+// work in order, behind its copies and MMAs, and leaves NaN in its logits.
 // kSub * kKStep columns are a step (of a constant count: a loop over a variable
 // one cost the MMA threads 0.6 us of 777 tokens' 7.7).
 template <bool kPair, int kSub>
@@ -218,13 +205,15 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t bars[2 * kMaxRing + 2 * kDensePairs + 1];
+  __shared__ uint64_t bars[2 * kMaxRing + 3 * kDensePairs + 1];
   __shared__ uint32_t tmem_at;
-  __shared__ int failed_word;
+  // each copying thread's next step; a leader of the cluster has given up
+  __shared__ int failed_word, copied[kDensePairs], given_up;
   volatile int* failed = &failed_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxRing, done = full + 16 * kMaxRing,
-                 drained = done + 8 * kDensePairs, received = drained + 8 * kDensePairs;
+                 drained = done + 8 * kDensePairs, received = drained + 8 * kDensePairs,
+                 idle = received + 8;
   const uint32_t ring = smem_u32(smem);
   const uint32_t a_bytes = kTileM * kKStep * 2, b_bytes = static_cast<uint32_t>(a.b_rows) * kKStep * 2;
   const uint32_t sub_bytes = a_bytes + b_bytes, slot_bytes = sub_bytes * kSub;
@@ -246,9 +235,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       for (int i = 0; i < kDensePairs; ++i) {
         mbar_init(done + 8 * i, 1);
         mbar_init(drained + 8 * i, kPair ? 2 * kSumWarps : kSumWarps);
+        mbar_init(idle + 8 * i, 1);
       }
       mbar_init(received, 1);
       *failed = 0;
+      given_up = 0;
       fence_mbar_init();
     }
     __syncwarp();
@@ -275,7 +266,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       int issued = first;  // k step of this CTA
       for (; k0 + issued < k1; issued += kDensePairs) {
         const int slot = issued % a.slots, k = k0 + issued;
-        ok = dense_wait(empty + 8 * slot, (issued / a.slots & 1) ^ 1, failed);
+        ok = ring_wait<false>(empty + 8 * slot, (issued / a.slots & 1) ^ 1, failed, a.wait_limit);
         if (!ok) break;
         if (half == 0)
           mbar_arrive_expect_tx(full + 8 * slot, kPair ? 2 * slot_bytes : slot_bytes);
@@ -293,14 +284,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           }
         }
       }
-      if (!ok && half == 0)  // copies in flight land before the CTAs end
-        for (int i = first; i < issued; i += kDensePairs) {
-          if (i < issued - a.slots) continue;
-          const long long t0 = clock64();
-          while (!mbar_try_wait(full + 8 * (i % a.slots), i / a.slots & 1) &&
-                 clock64() - t0 < kGiveUpCycles) {
-          }
-        }
+      if constexpr (kPair) {
+        copied[first] = issued;
+      } else {
+        // copies in flight land before the CTA ends (they have, where all were multiplied)
+        for (int i = first; i < issued; i += kDensePairs)
+          if (i >= issued - a.slots) drain<false>(full + 8 * (i % a.slots), i / a.slots & 1);
+      }
     }
   } else if (warp >= kWarpMma0) {
     // each into an accumulator of its own
@@ -320,11 +310,11 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         const int slot = i % a.slots;
         if (n > 0 && n % kRun == 0) {
           report(done + 8 * first);
-          ok = dense_wait<kPair>(drained + 8 * first, (n / kRun - 1) & 1, failed);
+          ok = ring_wait<kPair>(drained + 8 * first, (n / kRun - 1) & 1, failed, a.wait_limit);
           if (!ok) break;
           tc_fence_after();
         }
-        ok = dense_wait(full + 8 * slot, i / a.slots & 1, failed);
+        ok = ring_wait<false>(full + 8 * slot, i / a.slots & 1, failed, a.wait_limit);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -344,6 +334,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         report(empty + 8 * slot);
       }
       if (n > 0 && ok) report(done + 8 * first);
+      report(idle + 8 * first);
+      drain<kPair>(idle + 8 * first, 0);
     }
   } else {
     // lane + 32 (warp % 4) = token of the tile, half of the experts; in the end
@@ -359,7 +351,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
         // chunk c of MMA thread j, which has the steps j, j + kDensePairs, ...
         if (j + c * kRun * kDensePairs >= k1 - k0) continue;
         any = true;
-        ok = __all_sync(0xffffffffu, dense_wait(done + 8 * j, c & 1, failed));
+        ok = __all_sync(0xffffffffu, ring_wait<false>(done + 8 * j, c & 1, failed, a.wait_limit));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -382,23 +374,53 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       }
       if (!any) break;
     }
-    ok = __all_sync(0xffffffffu, ok && !*failed);
     // (nothing reads the ring any more: all of its copies were multiplied)
     float* row = reinterpret_cast<float*>(smem) + (warp % 4 * 32 + lane) * sum_pitch(a.tile_n) + c0;
+    if (ok)
 #pragma unroll
-    for (int p = 0; p < kMaxTileN / 8; ++p)
-      if (4 * p < cols)
-        *reinterpret_cast<float4*>(row + 4 * p) =
-            ok ? make_float4(sum[4 * p], sum[4 * p + 1], sum[4 * p + 2], sum[4 * p + 3])
-               : make_float4(__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u),
-                             __uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u));
+      for (int p = 0; p < kMaxTileN / 8; ++p)
+        if (4 * p < cols)
+          *reinterpret_cast<float4*>(row + 4 * p) =
+              make_float4(sum[4 * p], sum[4 * p + 1], sum[4 * p + 2], sum[4 * p + 3]);
     fence_proxy_async_smem();  // a bulk copy sends them on
   }
   tc_fence_before();
   __syncwarp();
   __syncthreads();
-  if constexpr (kPair) cluster_sync_all();  // nothing reaches across any more
+  if constexpr (kPair) {
+    if (half == 0 && static_cast<int>(threadIdx.x) < ctas && *failed)
+      st_cluster_s32(map_to_cta(smem_u32(&given_up), threadIdx.x), 1);
+    __syncwarp();
+    cluster_sync_all();  // nothing reaches across any more
+    if (given_up) {
+      // (else every copy has been multiplied.) The two of a pair may have stopped at
+      // different steps: the leader, to which both report, expects what only the other
+      // has copied, counts what that has not, and all that is under way lands.
+      if (half == 0 && threadIdx.x < kDensePairs) {
+        const int first = static_cast<int>(threadIdx.x), mine = copied[first];
+        const int other = ld_cluster_s32(map_to_cta(smem_u32(&copied[first]), leader + 1));
+        const int end = max(mine, other);
+        for (int i = first; i < end; i += kDensePairs) {
+          if (i < end - a.slots) continue;
+          const uint32_t bar = full + 8 * (i % a.slots);
+          if (i >= mine) mbar_arrive_expect_tx(bar, slot_bytes);
+          if (i >= other) mbar_complete_tx(bar, slot_bytes);
+          drain<true>(bar, i / a.slots & 1);
+        }
+      }
+      __syncwarp();
+      cluster_sync_all();
+    }
+  }
+  if (*failed) {  // (only now that no copy is under way into this memory)
+    for (int i = threadIdx.x; i < tile_sums_bytes(a.tile_n) / 4; i += kDenseThreads)
+      reinterpret_cast<float*>(smem)[i] = __uint_as_float(0x7FC00000u);
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   if (warp == kWarpMma0) {
+    if constexpr (kPair)  // also of the second CTA: the last that the leader sends it
+      for (int i = 0; i < kDensePairs; ++i) drain<true>(idle + 8 * i, 0);
     tc_fence_after();
     if constexpr (kPair)
       tmem_dealloc_pair(tmem, static_cast<uint32_t>(a.tmem_cols));
@@ -422,7 +444,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
           "r"(ring + to * share), "r"(share), "r"(map_to_cta(received, cta))
           : "memory");
     }
-    whole = dense_wait(received, 0, failed);
+    whole = ring_wait<false>(received, 0, failed, a.wait_limit);
+    if (!whole) drain<false>(received, 0);
   }
   const float* sums = reinterpret_cast<const float*>(smem);
   const float* others = reinterpret_cast<const float*>(smem + (inbox - ring));
@@ -553,6 +576,7 @@ cudaError_t launch_router_logits(const uint16_t* x, long long x_stride, const ui
   a.logits = logits;
   a.tokens = tokens;
   a.num_experts = num_experts;
+  a.wait_limit = wait_timeout_cycles();
   if (!encode_rows_tmap(&a.x, x, tokens, hidden, x_stride, kTileM) ||
       !encode_rows_tmap(&a.weight, weight, num_experts, hidden, hidden, a.b_rows))
     return cudaErrorInvalidValue;
