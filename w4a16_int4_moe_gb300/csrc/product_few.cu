@@ -366,23 +366,24 @@ cudaError_t run(const ProductArgs& args, int sms, cudaStream_t stream) {
 // Rows of a block and steps in flight by the tokens, and by whether blocks of 32
 // rows are at most one an SM (us in a graph, weights not in L2, hidden 7168 unless
 // said):
-//   INT4, one token, 9728 rows: 32 x 5 12.2, 64 x 4 10.3; 16384 rows 18.0, 15.9; 7168 x
-//     2048 4.0, 3.9; 4096 rows 6.2, 6.8, and with 16 warps for eight 32 x 3 5.5 (1024
-//     rows: 3.6 with eight, 3.7)
-//   INT4, 16 tokens, 9728 rows: 32 x 4 12.9, 64 x 5 12.3; 16384 rows 23.6, 22.2; 4096
-//     rows 7.6, 8.2
-//   INT4, 32 tokens, 4096 rows: 32 x 2 10.3, 32 x 3 10.1, 64 x 3 11.2; 9728 rows 20.2,
-//     19.2, 17.1
-//   BF16, one token, 4096 rows: 32 x 5 10.7, 32 x 3 11.2; 7168 x 2048 7.3, 6.7
-//   BF16, 16 tokens, 4096 rows: 32 x 4 11.4, 32 x 2 12.9; 7168 x 2048 8.3, 7.2
-//   BF16, 32 tokens, 4096 rows: 32 x 3 12.6, 64 x 2 14.9; 7168 x 2048 9.5, 9.1
-// (BF16 before the first weights set out early, which takes off 0.4 to 0.7.)
+//   INT4, one token, 9728 rows: 32 x 5 10.4, 64 x 4 10.0; 16384 rows 17.9, 15.4; 7168 x
+//     2048 4.1, 4.2; 4096 rows 6.5, 7.1, and with 16 warps for eight 32 x 3 5.8 (1024
+//     rows: 4.1 with either)
+//   INT4, 16 tokens, 9728 rows: 32 x 4 12.8, 64 x 5 12.9; 16384 rows 23.2, 22.7; 4096
+//     rows 7.4, 8.4
+//   INT4, 32 tokens, 4096 rows: 32 x 2 10.3, 32 x 3 10.0, 64 x 3 11.7; 9728 rows 20.6,
+//     19.7, 17.5; 7168 x 2048 9.1, 8.3, 7.4
+//   BF16, one token, 4096 rows: 32 x 5 10.7, 32 x 3 11.1; 7168 x 2048 6.2, 6.2; 18432
+//     rows 40.2, 40.9
+//   BF16, 16 tokens, 4096 rows: 32 x 4 11.5, 32 x 2 12.8; 7168 x 2048 7.1, 7.0
+//   BF16, 32 tokens, 4096 rows: 32 x 3 13.0, 64 x 2 15.4; 7168 x 2048 9.9, 9.5; 18432
+//     rows 47.5, 47.9
 // INT4 rows more than 64 an SM and more than 16 tokens go to tcgen05 (us of mma.sync
-// and of tcgen05, 32 tokens; with 17 both are 3 % faster): 12288 rows 32.5, 23.1;
-// 16384 32.8, 23.8; 32768 63.6, 45.1; 16384 x 2048 13.5, 10.0. With fewer rows blocks
-// of 128 are on half of the SMs or fewer: 9728 rows 17.4, 16.4, but 9728 x 2048 7.7,
-// 8.9, and 4096 rows 10.5, 10.7. 16 tokens are half of the MMAs: 16384 rows 22.2,
-// 20.9, but 65536 71.6, 75.9.
+// and of tcgen05, 32 tokens; with 17 both are 3 % faster): 12288 rows 28.7 to 32.1, 23.1;
+// 16384 32.6, 23.4; 32768 63.6, 45.1; 16384 x 2048 13.4, 10.2. With fewer rows blocks
+// of 128 are on half of the SMs or fewer, and a block takes what it takes: 9728 rows
+// 17.5, 23.0, 9728 x 2048 8.0, 9.3, and 4096 rows 10.0, 22.6. 16 tokens are half of the
+// MMAs: 16384 rows 22.7, 20.9, but 65536 74.6, 75.9.
 template <bool kInt4, bool kGated>
 cudaError_t few(const ProductArgs& args, int sms, cudaStream_t stream) {
   const bool one = args.n <= 32 * sms;

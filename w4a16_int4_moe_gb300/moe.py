@@ -320,7 +320,10 @@ class PackedSharedExpert:
     packed with W4A16_LAYOUT_KTILE64_GLU16, both of one expert. Up to
     W4A16_FEW_TOKENS_MAX tokens take two launches (w4a16_linear_few_tokens), more
     the GEMM path, planned for max_tokens, with every token routed to the one
-    expert."""
+    expert. The few-token products round no weight and keep gate and up in FP32;
+    the GEMM path rounds the scaled weights to BF16, and gate and up before silu,
+    as it does for routed experts. Its calls share the expert's buffers: one
+    stream at a time, while few-token calls share nothing."""
 
     def __init__(self, gate_up: PackedExperts, down: PackedExperts, max_tokens: int):
         if gate_up.num_experts != 1 or gate_up.layout != ops.W4A16_LAYOUT_KTILE64_GLU16:
