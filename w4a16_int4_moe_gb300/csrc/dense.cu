@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i)  // (a side is a multiple of eight columns)
             if (c * kChunk + i / 8 * 8 < cols) least = fminf(least, sum[2 * c + i / 16][i % 16]);
-          const bool quick = !p.a.f32_out && least >= kQuickGate;
+          const bool near = least >= kNearGate;
           const auto gated = [&](auto form) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -275,7 +275,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
               v = form(v, sum[(2 * c + i / 16 + kGroups / 2) % kGroups][i % 16]);
             }
           };
-          if (quick)
+          if (near && p.a.f32_out)
+            gated([](float g, float u) { return silu_times_near(g, u); });
+          else if (near)
             gated([](float g, float u) { return silu_times_quick(g, u); });
           else
             gated([](float g, float u) { return silu_times(g, u); });
