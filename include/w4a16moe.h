@@ -584,7 +584,8 @@ w4a16_status w4a16_linear_few_tokens(const void* packed, int layout, int n, int 
  *   out[t, i] = silu(x[t] . weight[i]^T) * (x[t] . weight[n/2 + i]^T)  (gated != 0)
  * FP32 sums, one rounding of the result. (The tensor core, which cuts off where a
  * plain sum would round, keeps them for at most 512 columns, 1024 for BF16
- * outputs; then they are added to sums outside.) A device-side wait that gives up
+ * outputs; then they are added to sums outside. silu is within 8 steps of FP32, for
+ * BF16 outputs of more than 32 tokens within 2^-16.) A device-side wait that gives up
  * (W4A16_WAIT_TIMEOUT_CYCLES, about a second) leaves NaN in the outputs that waited.
  *   weight  BF16 [n, k]; gated: n/2 gate rows, then n/2 up rows;
  *   x       BF16 [tokens, k], row stride x_stride elements;
@@ -603,7 +604,7 @@ w4a16_status w4a16_dense(const uint16_t* weight, int n, int k, int gated, const 
 
 /*
  * How w4a16_dense runs a product. Calls of the same sizes with the same info add in
- * the same order.
+ * the same order (with kernel 0: on devices with the same count of SMs).
  *   at_once  how many pairs of CTAs, and clusters of 1, 2, 4 and 8 CTAs, a device
  *            runs at once (five numbers above 0), or NULL: the current device's.
  * Sizes as w4a16_dense takes them. Host only with at_once given.
